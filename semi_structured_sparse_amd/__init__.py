@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step runs in the HIP kernels of the library; torch
 provides device memory and the current stream. The names follow the C ABI in
-include/nm_sparse.h (nm_pack, nm_spmv, nm_gemv_dense, ...). There is no CPU
+include/nm_sparse.h (nm_pack, nm_spmv, nm_gemv_dense, ...); decode.py binds what stands
+between the products of a decoding step (include/nm_decode.h). There is no CPU
 fallback: if the library is not built, every call raises.
 """
 from __future__ import annotations
@@ -10,6 +11,10 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+
+from .decode import (KVCache, MAX_NODES, NM_ERR_FORMAT, SIGNATURES as _DECODE_SIGNATURES, kv_cache,  # noqa: F401
+                     nm_kv_append, nm_kv_compact, nm_kv_read, nm_rope, nm_rope_kv_append, nm_tree_attention,
+                     nm_verify_chain, nm_verify_tree, rope_turns, tree_attention_workspace, verify_workspace)
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libnmsparse.so")
@@ -64,6 +69,7 @@ SIGNATURES = {
     "nm_probe_read_shaped": (_c.c_int, [_c.c_void_p, _c.c_size_t, _c.c_void_p, _c.c_uint32, _c.c_int, _c.c_int,
                                         _c.c_int, _c.c_int, _c.c_void_p]),
     "nm_probe_copy": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    **_DECODE_SIGNATURES,
 }
 
 _lib = None

@@ -5,6 +5,7 @@
 #include <set>
 #include <utility>
 
+#include "nm_decode.h"
 #include "nm_internal.h"
 #include "nm_sparse.h"
 
@@ -452,6 +453,7 @@ const char* nm_status_string(int status) {
     case NM_ERR_TOO_WIDE: return "cols too large: x does not fit in the LDS of one workgroup";
     case NM_ERR_HIP: return "a HIP runtime call failed";
     case NM_ERR_SCRATCH: return "the column split of this shape needs more than the library's static scratch";
+    case NM_ERR_FORMAT: return "unsupported cache format, rotary layout, head size or page size (nm_decode.h)";
     default: return "unknown status";
   }
 }

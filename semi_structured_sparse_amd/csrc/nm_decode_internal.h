@@ -1,0 +1,135 @@
+// Declarations shared by the translation units of the speculative-decoding operators: the
+// checked arguments their kernels take, and the device helpers of the paged cache and the
+// rotary positions. Not part of the public ABI (include/nm_decode.h is).
+#pragma once
+
+#include <hip/hip_fp16.h>
+
+#include "nm_decode.h"
+#include "nm_internal.h"
+
+namespace nm {
+
+constexpr int kMaxNodes = 64;   // nodes of one sequence's step (a mask word's bits)
+
+// A paged cache and the page table of the sequences that a call works on.
+struct PagedCache {
+  char* k;
+  char* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  int table_width;
+  uint32_t blocks;
+  int kv_heads;
+  int page_shift;
+};
+
+struct RopeArgs {
+  const int32_t* positions;
+  const double* turns;
+  int rot_dim;
+  int layout;
+  float scale;
+};
+
+struct RopeCall {
+  const uint16_t* x;
+  uint16_t* y;
+  int64_t x_stride, y_stride;
+  int64_t tokens;
+  int heads, head_dim;
+  RopeArgs rope;
+};
+
+struct AppendCall {
+  PagedCache cache;
+  const uint16_t *q, *k, *v;
+  uint16_t* q_out;
+  int64_t q_stride, q_out_stride, k_stride, v_stride;
+  const int32_t *start, *count;
+  int64_t batch, tokens;
+  int q_heads;
+  RopeArgs rope;   // positions NULL: no rotation
+};
+
+struct ReadCall {
+  PagedCache cache;
+  uint16_t *k_out, *v_out;
+  const int32_t *start, *count;
+  int64_t batch, tokens;
+};
+
+struct CompactCall {
+  PagedCache cache;
+  const int32_t *start, *path, *accepted;
+  int64_t batch;
+  int nodes;
+};
+
+struct AttnCall {
+  PagedCache cache;
+  const uint16_t* q;
+  uint16_t* out;
+  const int32_t *context, *count;
+  const uint64_t* mask;
+  int64_t q_stride;
+  int batch, tokens, heads, group;
+  float scale;
+};
+
+struct VerifyCall {
+  const float *target, *draft, *uniforms;
+  const int32_t *tokens, *parents, *count;
+  int32_t *accepted, *out_tokens, *path;
+  int batch, nodes, vocab;
+};
+
+hipError_t launch_rope(const RopeCall& c, hipStream_t stream, const DeviceInfo& dev);
+hipError_t launch_append(const AppendCall& c, int head_dim, int format, hipStream_t stream, const DeviceInfo& dev);
+hipError_t launch_read(const ReadCall& c, int head_dim, int format, hipStream_t stream, const DeviceInfo& dev);
+hipError_t launch_compact(const CompactCall& c, int head_dim, int format, hipStream_t stream, const DeviceInfo& dev);
+hipError_t launch_attention(const AttnCall& c, int head_dim, int format, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream, const DeviceInfo& dev);
+size_t attention_workspace_bytes(const AttnCall& c, int head_dim, int format, const DeviceInfo& dev);
+hipError_t launch_verify(const VerifyCall& c, void* workspace, size_t workspace_bytes, hipStream_t stream,
+                         const DeviceInfo& dev);
+size_t verify_workspace_bytes(int64_t batch, int64_t vocab, const DeviceInfo& dev);
+
+// ------------------------------------------------------------------------ device helpers
+// The cache row (token slot of one head) of position pos of sequence b, or -1 where the
+// position or its table entry is out of range.
+__device__ __forceinline__ int64_t cache_row(const PagedCache& c, int64_t b, int64_t pos, int head) {
+  if (pos < 0 || (pos >> c.page_shift) >= c.table_width) return -1;
+  const uint32_t block = uint32_t(c.table[b * c.table_width + (pos >> c.page_shift)]);
+  if (block >= c.blocks) return -1;
+  return (((int64_t(block) * c.kv_heads + head) << c.page_shift) + (pos & ((1 << c.page_shift) - 1)));
+}
+
+// count[b] clamped to 0 .. most (NULL: most).
+__device__ __forceinline__ int count_of(const int32_t* count, int64_t b, int most) {
+  if (count == nullptr) return most;
+  const int n = count[b];
+  return n < 0 ? 0 : n > most ? most : n;
+}
+
+__device__ __forceinline__ float half_bits_to_float(uint32_t bits) {
+  return float(__builtin_bit_cast(_Float16, uint16_t(bits)));
+}
+
+__device__ __forceinline__ uint32_t float_to_half_bits(float x) {   // round to nearest even
+  return __builtin_bit_cast(uint16_t, _Float16(x));
+}
+
+// Cosine and sine of 2 pi * pos * turns, times scale. The product keeps its fraction in 64
+// bits (a position of 10^6 at one turn in 6 leaves 32 bits an angle off by 10^-2); the
+// fraction of a turn then fits 32.
+__device__ __forceinline__ void rotation(int pos, double turns, float scale, float& c, float& s) {
+  const double t = double(pos) * turns;
+  const float f = float(t - rint(t));
+  sincospif(2.0f * f, &s, &c);
+  c *= scale;
+  s *= scale;
+}
+
+}  // namespace nm

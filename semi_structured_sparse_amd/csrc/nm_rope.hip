@@ -1,0 +1,69 @@
+// Rotary positions (nm_rope) and the host table of their frequencies (nm_rope_turns).
+#include <cmath>
+
+#include "nm_decode_internal.h"
+
+namespace nm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// One pair (or, past the rotated part, two elements) per thread.
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeCall a) {
+  const int units = (a.head_dim + 1) / 2, pairs = a.rope.rot_dim / 2;
+  const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= a.tokens * a.heads * units) return;
+  const int u = int(i % units);
+  const int64_t head = i / units % a.heads, token = i / units / a.heads;
+  const uint16_t* x = a.x + token * a.x_stride + head * a.head_dim;
+  uint16_t* y = a.y + token * a.y_stride + head * a.head_dim;
+  if (u >= pairs) {
+    const int e = 2 * u;
+    y[e] = x[e];
+    if (e + 1 < a.head_dim) y[e + 1] = x[e + 1];
+    return;
+  }
+  const bool half = a.rope.layout == NM_ROPE_HALF;
+  const int e0 = half ? u : 2 * u, e1 = half ? u + pairs : 2 * u + 1;
+  float c, s;
+  rotation(a.rope.positions[token], a.rope.turns[u], a.rope.scale, c, s);
+  const float p = half_bits_to_float(x[e0]), q = half_bits_to_float(x[e1]);
+  y[e0] = uint16_t(float_to_half_bits(p * c - q * s));
+  y[e1] = uint16_t(float_to_half_bits(q * c + p * s));
+}
+
+}  // namespace
+
+hipError_t launch_rope(const RopeCall& c, hipStream_t stream, const DeviceInfo& dev) {
+  RopeCall a = c;
+  const int64_t n = c.tokens * c.heads * ((c.head_dim + 1) / 2);
+  const int64_t grid = (n + kThreads - 1) / kThreads;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  void* args[] = {&a};
+  return launch(reinterpret_cast<const void*>(rope_kernel), dim3(uint32_t(grid)), dim3(kThreads), args, 0, stream, dev);
+}
+
+}  // namespace nm
+
+int nm_rope_turns(double* turns, int rot_dim, int scaling, double base, double factor, double length, double low,
+                  double high) {
+  if (!turns) return NM_ERR_NULL;
+  if (scaling < NM_ROPE_PLAIN || scaling > NM_ROPE_BANDS) return NM_ERR_FORMAT;
+  const auto positive = [](double v) { return std::isfinite(v) && v > 0.0; };
+  if (rot_dim < (scaling == NM_ROPE_BASE ? 4 : 2) || rot_dim > 1024 || rot_dim % 2 != 0) return NM_ERR_SHAPE;
+  if (!positive(base) || (scaling != NM_ROPE_PLAIN && !positive(factor))) return NM_ERR_SHAPE;
+  if (scaling == NM_ROPE_BANDS && !(positive(length) && std::isfinite(low) && low >= 0.0 && positive(high) && high > low))
+    return NM_ERR_SHAPE;
+  if (scaling == NM_ROPE_BASE) base *= std::pow(factor, double(rot_dim) / double(rot_dim - 2));
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double t = std::pow(base, -2.0 * i / rot_dim) / (2.0 * 3.14159265358979323846);
+    if (scaling == NM_ROPE_LINEAR) t /= factor;
+    if (scaling == NM_ROPE_BANDS) {
+      double w = (length * t - low) / (high - low);
+      w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+      t = t * w + t / factor * (1.0 - w);
+    }
+    turns[i] = t;
+  }
+  return NM_OK;
+}
