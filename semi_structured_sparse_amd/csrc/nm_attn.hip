@@ -1,100 +1,78 @@
-// Attention of a step's nodes over the paged cache.
-#include <cmath>
-
-#include "nm_decode_internal.h"
+// Launch of the attention kernel (nm_attn_impl.h): rows per workgroup, the split of the
+// contexts over the GPU, and the workspace.
+#include "nm_attn_impl.h"
 
 namespace nm {
 namespace {
 
-constexpr int kThreads = 256;
+struct Plan {
+  int nr;          // row tiles of 16 a workgroup takes
+  int row_tiles;   // workgroups of rows
+  int slots;       // chunks over all sequences; 0: one a sequence
+  uint32_t part_bytes;
+};
+
+template <int FMT, int D>
+const void* kernel_of(int nr) {
+  if (nr == 1) return reinterpret_cast<const void*>(attention_kernel<FMT, D, 1>);
+  if (nr == 2 || D > 128) return reinterpret_cast<const void*>(attention_kernel<FMT, D, 2>);
+  if constexpr (D <= 128) return reinterpret_cast<const void*>(attention_kernel<FMT, D, 4>);
+  return nullptr;
+}
 
 template <int FMT>
-__device__ __forceinline__ float decode(const char* row, int i) {
-  if constexpr (FMT == NM_KV_FP16) return half_bits_to_float(reinterpret_cast<const uint16_t*>(row)[i]);
-  if constexpr (FMT == NM_KV_INT8) return float(reinterpret_cast<const signed char*>(row)[i]);
-  return __builtin_amdgcn_cvt_f32_fp8(int(uint8_t(row[i])), 0);
+const void* kernel_of(int head_dim, int nr) {
+  return head_dim == 64 ? kernel_of<FMT, 64>(nr) : head_dim == 128 ? kernel_of<FMT, 128>(nr) : kernel_of<FMT, 256>(nr);
 }
 
-// One workgroup per query row; its four waves take every fourth key, a lane D/64 elements,
-// with the running maximum and sum of the softmax.
-template <int D, int FMT>
-__global__ __launch_bounds__(kThreads) void attention_kernel(AttnCall a) {
-  constexpr int E = D / 64;
-  constexpr int kBytes = FMT == NM_KV_FP16 ? 2 : 1;
-  __shared__ float part[4][D + 2];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int head = blockIdx.x % a.heads, t = blockIdx.x / a.heads;
-  const int64_t b = blockIdx.y;
-  const int count = count_of(a.count, b, a.tokens);
-  const int64_t most = int64_t(a.cache.table_width) << a.cache.page_shift;
-  const int64_t ctx = a.context[b] < 0 ? 0 : a.context[b] > most ? most : a.context[b];
-  const int64_t keys = ctx + count < most ? ctx + count : most;
-  const uint64_t mask = a.mask != nullptr ? a.mask[b * a.tokens + t] : t >= 63 ? ~0ull : (2ull << t) - 1;
-  uint16_t* out = a.out + ((b * a.tokens + t) * a.heads + head) * D;
-  float q[E], o[E], m = -__builtin_inff(), l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = half_bits_to_float(a.q[(b * a.tokens + t) * a.q_stride + int64_t(head) * D + lane + 64 * e]) * a.scale;
-    o[e] = 0.f;
-  }
-  for (int64_t j = wave; j < keys && t < count; j += 4) {
-    if (j >= ctx && !((mask >> (j - ctx)) & 1)) continue;
-    const int64_t row = cache_row(a.cache, b, j, head / a.group);
-    if (row < 0) continue;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += q[e] * decode<FMT>(a.cache.k + row * D * kBytes, lane + 64 * e);
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) s += __shfl_xor(s, x);
-    if constexpr (FMT != NM_KV_FP16) s *= a.cache.k_scale[row];
-    const float top = fmaxf(m, s);
-    const float old = m > -__builtin_inff() ? expf(m - top) : 0.f, p = s == -__builtin_inff() ? 0.f : expf(s - top);
-    m = top;
-    l = l * old + p;
-    float w = p;
-    if constexpr (FMT != NM_KV_FP16) w *= a.cache.v_scale[row];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * old + w * decode<FMT>(a.cache.v + row * D * kBytes, lane + 64 * e);
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) part[wave][lane + 64 * e] = o[e];
-  if (lane == 0) {
-    part[wave][D] = m;
-    part[wave][D + 1] = l;
-  }
-  __syncthreads();
-  if (wave != 0) return;
-  m = fmaxf(fmaxf(part[0][D], part[1][D]), fmaxf(part[2][D], part[3][D]));
-  l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int w = 0; w < 4; ++w) {
-    const float f = part[w][D] > -__builtin_inff() ? expf(part[w][D] - m) : 0.f;
-    l += part[w][D + 1] * f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += part[w][lane + 64 * e] * f;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[lane + 64 * e] = uint16_t(float_to_half_bits(l == 0.f ? 0.f : o[e] / l));
+const void* kernel_of(int format, int head_dim, int nr) {
+  return format == NM_KV_FP16   ? kernel_of<NM_KV_FP16>(head_dim, nr)
+         : format == NM_KV_INT8 ? kernel_of<NM_KV_INT8>(head_dim, nr)
+                                : kernel_of<NM_KV_E4M3>(head_dim, nr);
 }
 
-template <int D>
-const void* of_format(int format) {
-  return format == NM_KV_FP16   ? reinterpret_cast<const void*>(attention_kernel<D, NM_KV_FP16>)
-         : format == NM_KV_INT8 ? reinterpret_cast<const void*>(attention_kernel<D, NM_KV_INT8>)
-                                : reinterpret_cast<const void*>(attention_kernel<D, NM_KV_E4M3>);
+Plan plan_of(const AttnCall& c, int head_dim, const DeviceInfo& dev) {
+  Plan p;
+  const int rows = c.tokens * c.group;
+  p.nr = rows <= 16 ? 1 : rows <= 32 || head_dim > 128 ? 2 : 4;
+  p.row_tiles = (rows + 16 * p.nr - 1) / (16 * p.nr);
+  p.part_bytes = uint32_t(head_dim / 16 * p.nr * 1024 + p.nr * 128);
+  const int64_t items = int64_t(c.batch) * c.cache.kv_heads * p.row_tiles;
+  const int64_t most = int64_t(c.cache.table_width) << c.cache.page_shift;
+  const int64_t target = int64_t(dev.cu_count) * attn_waves(head_dim, p.nr);
+  // chunks beyond one a sequence: what fills the GPU once, at most one for every kMinChunkTiles
+  const int64_t longest = (most + kTileKeys * kMinChunkTiles - 1) / (kTileKeys * kMinChunkTiles);
+  int64_t extra = target / (int64_t(c.cache.kv_heads) * p.row_tiles);
+  if (extra > longest * c.batch) extra = longest * c.batch;
+  p.slots = items > NM_DECODE_COUNTER_BYTES / 4 || extra <= c.batch || longest <= 1 ? 0 : int(extra) + c.batch;
+  return p;
+}
+
+size_t plan_bytes(const AttnCall& c, const Plan& p) {
+  if (p.slots == 0) return 0;
+  return NM_DECODE_COUNTER_BYTES + size_t(p.slots) * unsigned(c.cache.kv_heads) * unsigned(p.row_tiles) * p.part_bytes;
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(const AttnCall&, int, int, const DeviceInfo&) { return 0; }
+size_t attention_workspace_bytes(const AttnCall& c, int head_dim, int, const DeviceInfo& dev) {
+  return plan_bytes(c, plan_of(c, head_dim, dev));
+}
 
-hipError_t launch_attention(const AttnCall& c, int head_dim, int format, void*, size_t, hipStream_t stream,
-                            const DeviceInfo& dev) {
+hipError_t launch_attention(const AttnCall& c, int head_dim, int format, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream, const DeviceInfo& dev) {
   AttnCall a = c;
-  void* args[] = {&a};
-  const void* f = head_dim == 64 ? of_format<64>(format) : head_dim == 128 ? of_format<128>(format) : of_format<256>(format);
-  return launch(f, dim3(uint32_t(c.heads) * uint32_t(c.tokens), uint32_t(c.batch)), dim3(kThreads), args, 0, stream, dev);
+  Plan p = plan_of(c, head_dim, dev);
+  if (workspace == nullptr || workspace_bytes < plan_bytes(c, p)) p.slots = 0;
+  AttnSplit sp{p.slots, p.row_tiles, static_cast<uint32_t*>(workspace),
+               p.slots ? static_cast<char*>(workspace) + NM_DECODE_COUNTER_BYTES : nullptr, p.part_bytes};
+  void* args[] = {&a, &sp};
+  // Row tiles of one chunk read the same keys: a grid width that is a multiple of the 8 XCDs
+  // puts them on one XCD's L2.
+  const int64_t wide = (int64_t(p.slots ? p.slots : c.batch) * c.cache.kv_heads + 7) / 8 * 8;
+  if (wide > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  return launch(kernel_of(format, head_dim, p.nr), dim3(uint32_t(wide), uint32_t(p.row_tiles)), dim3(kAttnThreads), args,
+                0, stream, dev);
 }
 
 }  // namespace nm

@@ -121,6 +121,19 @@ __device__ __forceinline__ uint32_t float_to_half_bits(float x) {   // round to 
   return __builtin_bit_cast(uint16_t, _Float16(x));
 }
 
+// Partial results cross workgroups on different XCDs, whose L2 caches are not coherent with
+// each other: accesses with the SC1 cache-policy bit are, without a fence that writes back or
+// invalidates a whole L2. `bytes` bounds the resource: accesses past it read zero or are dropped.
+constexpr int kCoherent = 16;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t coherent_buffer(void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(p, 0, bytes, 0x00027000);
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 // Cosine and sine of 2 pi * pos * turns, times scale. The product keeps its fraction in 64
 // bits (a position of 10^6 at one turn in 6 leaves 32 bits an angle off by 10^-2); the
 // fraction of a turn then fits 32.
