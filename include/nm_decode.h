@@ -108,7 +108,7 @@ int nm_rope(const uint16_t* x, uint16_t* y, const int32_t* positions, const doub
  *           (all `tokens`); counts outside 0 .. tokens are clamped
  * Tokens whose position is outside 0 .. table_width * page - 1 or whose table entry is outside
  * 0 .. blocks - 1 are skipped (an entry of -1 is the usual filler). Two tokens of one call must
- * not share a slot. NM_ERR_SHAPE: batch outside 1 .. 65536, tokens outside 1 .. 2^24, batch * tokens
+ * not share a slot. NM_ERR_SHAPE: batch outside 1 .. 65535, tokens outside 1 .. 2^24, batch * tokens
  * above 2^30, table_width outside 1 .. 2^24 or table_width * page above 2^30, kv_heads outside
  * 1 .. 4096, blocks outside 1 .. 2^31 - 1, a stride below the heads' size or above 2^40. */
 int nm_kv_append(const nm_kv_cache* cache, const uint16_t* k, const uint16_t* v, int64_t k_stride,
@@ -165,7 +165,7 @@ int nm_kv_compact(const nm_kv_cache* cache, const int32_t* table, int64_t table_
  * nm_tree_attention and nm_verify calls in stream order. Fewer bytes than
  * nm_tree_attention_workspace_bytes run as NULL does. Calls that overlap on one workspace
  * race. NM_ERR_SHAPE: tokens outside 1 .. 64, heads not a multiple of kv_heads or above 16
- * times kv_heads or 65536, batch outside 1 .. 65536, a scale that is not finite, others as nm_kv_append. */
+ * times kv_heads or 65536, batch outside 1 .. 65535, a scale that is not finite, others as nm_kv_append. */
 #define NM_DECODE_COUNTER_BYTES 65536u
 int nm_tree_attention(const nm_kv_cache* cache, const uint16_t* q, uint16_t* out, int64_t heads,
                       int64_t q_stride, const int32_t* table, int64_t table_width, const int32_t* context,
@@ -196,7 +196,7 @@ size_t nm_tree_attention_workspace_bytes(const nm_kv_cache* cache, int64_t heads
  * A token outside 0 .. vocab - 1 is refused. workspace: as nm_tree_attention's, at least
  * nm_verify_workspace_bytes, or NULL (each sequence on one workgroup); the draw is the same
  * up to the order of 64-bit sums. NM_ERR_SHAPE: nodes outside 1 .. 64, batch outside
- * 1 .. 65536, vocab outside 1 .. 2^24. fp32 and int32 arrays 4-byte aligned, workspace 16. */
+ * 1 .. 65535, vocab outside 1 .. 2^24. fp32 and int32 arrays 4-byte aligned, workspace 16. */
 int nm_verify_chain(const float* target, const float* draft, const int32_t* tokens, const float* uniforms,
                     const int32_t* count, int32_t* accepted, int32_t* out_tokens, int64_t batch, int64_t nodes,
                     int64_t vocab, void* workspace, size_t workspace_bytes, void* stream);

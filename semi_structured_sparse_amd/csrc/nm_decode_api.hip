@@ -31,7 +31,7 @@ int cache_check(const nm_kv_cache* c, const int32_t* table, int64_t table_width,
   if (c->format != NM_KV_FP16 && (!c->k_scale || !c->v_scale)) return NM_ERR_NULL;
   if (!within(c->blocks, 1, 0x7FFFFFFF) || !within(c->kv_heads, 1, 4096)) return NM_ERR_SHAPE;
   if (!within(table_width, 1, int64_t(1) << 24) || table_width * c->page > (int64_t(1) << 30)) return NM_ERR_SHAPE;
-  if (!within(batch, 1, 65536) || !within(tokens, 1, int64_t(1) << 24) || batch * tokens > (int64_t(1) << 30))
+  if (!within(batch, 1, 65535) || !within(tokens, 1, int64_t(1) << 24) || batch * tokens > (int64_t(1) << 30))
     return NM_ERR_SHAPE;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(table, 4)) return NM_ERR_ALIGN;
   if (c->format != NM_KV_FP16 && (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))) return NM_ERR_ALIGN;
@@ -109,7 +109,7 @@ int verify(const VerifyCall& given, int64_t batch, int64_t nodes, int64_t vocab,
            size_t workspace_bytes, void* stream) {
   VerifyCall c = given;
   if (!c.target || !c.tokens || !c.uniforms || !c.accepted || !c.out_tokens) return NM_ERR_NULL;
-  if (!within(batch, 1, 65536) || !within(nodes, 1, kMaxNodes) || !within(vocab, 1, int64_t(1) << 24))
+  if (!within(batch, 1, 65535) || !within(nodes, 1, kMaxNodes) || !within(vocab, 1, int64_t(1) << 24))
     return NM_ERR_SHAPE;
   for (const void* p : {static_cast<const void*>(c.target), static_cast<const void*>(c.draft),
                         static_cast<const void*>(c.uniforms), static_cast<const void*>(c.tokens),
@@ -268,7 +268,7 @@ int nm_verify_tree(const float* target, const int32_t* tokens, const int32_t* pa
 }
 
 size_t nm_verify_workspace_bytes(int64_t batch, int64_t vocab) {
-  if (!within(batch, 1, 65536) || !within(vocab, 1, int64_t(1) << 24)) return 0;
+  if (!within(batch, 1, 65535) || !within(vocab, 1, int64_t(1) << 24)) return 0;
   DeviceInfo dev;
   if (current_device_info(&dev) != hipSuccess) return 0;
   return verify_workspace_bytes(batch, vocab, dev);
