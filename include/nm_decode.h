@@ -109,7 +109,7 @@ int nm_rope(const uint16_t* x, uint16_t* y, const int32_t* positions, const doub
  * Tokens whose position is outside 0 .. table_width * page - 1 or whose table entry is outside
  * 0 .. blocks - 1 are skipped (an entry of -1 is the usual filler). Two tokens of one call must
  * not share a slot. NM_ERR_SHAPE: batch outside 1 .. 65535, tokens outside 1 .. 2^24, batch * tokens
- * above 2^30, table_width outside 1 .. 2^24 or table_width * page above 2^30, kv_heads outside
+ * above 2^30, batch * tokens times the call's heads above 2^31 - 1, table_width outside 1 .. 2^24 or table_width * page above 2^30, kv_heads outside
  * 1 .. 4096, blocks outside 1 .. 2^31 - 1, a stride below the heads' size or above 2^40. */
 int nm_kv_append(const nm_kv_cache* cache, const uint16_t* k, const uint16_t* v, int64_t k_stride,
                  int64_t v_stride, const int32_t* table, int64_t table_width, const int32_t* start,

@@ -134,15 +134,72 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+__device__ __forceinline__ float half_at(u32x4 v, int i) {   // element i of 8 halves
+  return half_bits_to_float((v[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+}
+
+__device__ __forceinline__ u32x4 halves_of(const float (&e)[8]) {   // each to nearest even
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = float_to_half_bits(e[2 * i]) | float_to_half_bits(e[2 * i + 1]) << 16;
+  return v;
+}
+
 // Cosine and sine of 2 pi * pos * turns, times scale. The product keeps its fraction in 64
 // bits (a position of 10^6 at one turn in 6 leaves 32 bits an angle off by 10^-2); the
-// fraction of a turn then fits 32.
+// instructions take a fraction of a turn and are good to 2^-20 of a unit, far below the half
+// step (2^-12 .. 2^-11) of the fp16 or 8-bit result.
 __device__ __forceinline__ void rotation(int pos, double turns, float scale, float& c, float& s) {
   const double t = double(pos) * turns;
   const float f = float(t - rint(t));
-  sincospif(2.0f * f, &s, &c);
-  c *= scale;
-  s *= scale;
+  c = __builtin_amdgcn_cosf(f) * scale;
+  s = __builtin_amdgcn_sinf(f) * scale;
+}
+
+// A unit of a head: 16 elements, as two runs of 8. Of the rotated part they are 8 pairs, which
+// lie rot_dim / 2 apart (NM_ROPE_HALF) or next to each other; elsewhere 16 neighbours.
+struct HeadUnit {
+  int first, second;   // where the runs start
+  bool turned;
+};
+
+__device__ __forceinline__ HeadUnit head_unit(int unit, int rot_dim, int layout) {
+  HeadUnit u;
+  u.turned = 16 * unit < rot_dim;
+  const bool apart = u.turned && layout == NM_ROPE_HALF;
+  u.first = apart ? 8 * unit : 16 * unit;
+  u.second = apart ? rot_dim / 2 + 8 * unit : 16 * unit + 8;
+  return u;
+}
+
+struct UnitRotation {
+  float c[8], s[8];
+};
+
+__device__ __forceinline__ UnitRotation unit_rotation(const RopeArgs& r, int unit, int pos) {
+  UnitRotation t;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) rotation(pos, r.turns[8 * unit + i], r.scale, t.c[i], t.s[i]);
+  return t;
+}
+
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = a * c - b * s;
+  b = b * c + a * s;
+  a = x;
+}
+
+__device__ __forceinline__ void turn_unit(const UnitRotation& t, int layout, float (&a)[8], float (&b)[8]) {
+  if (layout == NM_ROPE_HALF) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn(a[i], b[i], t.c[i], t.s[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      turn(a[2 * i], a[2 * i + 1], t.c[i], t.s[i]);
+      turn(b[2 * i], b[2 * i + 1], t.c[4 + i], t.s[4 + i]);
+    }
+  }
 }
 
 }  // namespace nm

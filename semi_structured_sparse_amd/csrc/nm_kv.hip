@@ -1,5 +1,7 @@
 // The paged key/value cache: appending (with or without rotary positions), reading back, and
 // moving an accepted tree path's rows together.
+#include <type_traits>
+
 #include "nm_decode_internal.h"
 
 namespace nm {
@@ -15,126 +17,171 @@ struct Codes {
 
 constexpr float kTiniest = 1e-30f;   // rows below it are held as zeros
 
-// One wave per (token, head) row; lane l holds elements 2l, 2l+1 (+128 for 256).
+// Lanes that hold a row of D elements, 16 each.
+template <int D>
+struct RowLanes {
+  static constexpr int kLanes = D / 16;
+  static constexpr int kRows = kThreads / kLanes;   // of a workgroup
+};
+
+// The largest of the row's lanes (4, 8 or 16 neighbours): within quads, then mirrored across
+// them.
+template <int LANES>
+__device__ __forceinline__ float row_max(float x) {
+  const auto dpp = [](float v, auto ctrl) {
+    return __uint_as_float(
+        __builtin_amdgcn_update_dpp(0, __float_as_uint(v), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  x = fmaxf(x, dpp(x, std::integral_constant<int, 0xB1>{}));    // quad_perm 1,0,3,2
+  x = fmaxf(x, dpp(x, std::integral_constant<int, 0x4E>{}));    // quad_perm 2,3,0,1
+  if (LANES > 4) x = fmaxf(x, dpp(x, std::integral_constant<int, 0x141>{}));   // row_half_mirror
+  if (LANES > 8) x = fmaxf(x, dpp(x, std::integral_constant<int, 0x140>{}));   // row_mirror
+  return x;
+}
+
+// 8 codes of scaled values.
+template <int FMT>
+__device__ __forceinline__ u32x2 codes_of(const float (&e)[8], float up) {
+  u32x2 w;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      z[i] = fminf(fmaxf(e[4 * h + i] * up, -Codes<FMT>::kLargest), Codes<FMT>::kLargest);
+    if constexpr (FMT == NM_KV_E4M3) {
+      int v = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], 0, false);
+      w[h] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], v, true));
+    } else {
+      w[h] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[h] |= (uint32_t(int(rintf(z[i]))) & 0xFFu) << (8 * i);
+    }
+  }
+  return w;
+}
+
+// D / 16 lanes per (token, head) row; the token's rows are its q heads (turned only), its k
+// heads and its v heads. Bound by the copy: 2 bytes an element in, 1 or 2 out.
 template <int D, int FMT>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendCall a) {
-  constexpr int P = D / 128 > 0 ? D / 128 : 1;
-  const int lane = threadIdx.x & 63;
-  const int heads = a.q_heads + 2 * a.cache.kv_heads;
-  const int64_t row = int64_t(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
-  if (row >= a.batch * a.tokens * heads) return;
-  const int head = int(row % heads);
-  const int64_t token = row / heads, b = token / a.tokens;
-  const int t = int(token % a.tokens);
-  const bool live = t < count_of(a.count, b, int(a.tokens));
+  constexpr int kLanes = RowLanes<D>::kLanes;
+  const uint32_t heads = uint32_t(a.q_heads + 2 * a.cache.kv_heads);
+  const uint32_t row = blockIdx.x * RowLanes<D>::kRows + threadIdx.x / kLanes;
+  const int unit = threadIdx.x % kLanes;
+  if (row >= uint32_t(a.batch * a.tokens) * heads) return;
+  const uint32_t token = row / heads, b = token / uint32_t(a.tokens);
+  const int head = int(row - token * heads), t = int(token - b * uint32_t(a.tokens));
   const bool is_q = head < a.q_heads, is_v = head >= a.q_heads + a.cache.kv_heads;
   const int h = is_q ? head : is_v ? head - a.q_heads - a.cache.kv_heads : head - a.q_heads;
-  const uint16_t* x = is_q ? a.q + token * a.q_stride : is_v ? a.v + token * a.v_stride : a.k + token * a.k_stride;
+  const uint16_t* x = is_q   ? a.q + int64_t(token) * a.q_stride
+                      : is_v ? a.v + int64_t(token) * a.v_stride
+                             : a.k + int64_t(token) * a.k_stride;
   x += int64_t(h) * D;
-  float e[2 * P];
+  const HeadUnit hu = head_unit(unit, is_v ? 0 : a.rope.rot_dim, a.rope.layout);
+  u32x4 p = *reinterpret_cast<const u32x4*>(x + hu.first), q = *reinterpret_cast<const u32x4*>(x + hu.second);
+  const bool live = t < count_of(a.count, b, int(a.tokens));
+  float e[8], f[8];
 #pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = 128 * p + 2 * lane + j;
-      float y = 0.f;
-      if (i < D && live) {
-        y = half_bits_to_float(x[i]);
-        if (!is_v && a.rope.positions != nullptr && i < a.rope.rot_dim) {
-          const int pairs = a.rope.rot_dim / 2;
-          const bool half = a.rope.layout == NM_ROPE_HALF;
-          const bool second = half ? i >= pairs : (i & 1);
-          const int u = half ? (second ? i - pairs : i) : i / 2;
-          const int other = half ? (second ? i - pairs : i + pairs) : i ^ 1;
-          float c, s;
-          rotation(a.rope.positions[token], a.rope.turns[u], a.rope.scale, c, s);
-          const float z = half_bits_to_float(x[other]);
-          y = second ? y * c + z * s : y * c - z * s;
-        }
-      }
-      e[2 * p + j] = y;
+  for (int i = 0; i < 8; ++i) {
+    e[i] = half_at(p, i);
+    f[i] = half_at(q, i);
+  }
+  if (hu.turned) {
+    turn_unit(unit_rotation(a.rope, unit, a.rope.positions[token]), a.rope.layout, e, f);
+    if (is_q || FMT == NM_KV_FP16) {
+      p = halves_of(e);
+      q = halves_of(f);
     }
+  }
   if (is_q) {
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = 128 * p + 2 * lane + j;
-        if (i < D) a.q_out[token * a.q_out_stride + int64_t(h) * D + i] = uint16_t(float_to_half_bits(e[2 * p + j]));
-      }
+    if (!live) p = q = u32x4{0, 0, 0, 0};
+    uint16_t* y = a.q_out + int64_t(token) * a.q_out_stride + int64_t(h) * D;
+    *reinterpret_cast<u32x4*>(y + hu.first) = p;
+    *reinterpret_cast<u32x4*>(y + hu.second) = q;
     return;
   }
-  if (!live) return;
+  if (!live) return;   // a row's lanes go together
   const int64_t at = cache_row(a.cache, b, int64_t(a.start[b]) + t, h);
   if (at < 0) return;
   char* out = (is_v ? a.cache.v : a.cache.k) + at * D * Codes<FMT>::kBytes;
-  float up = 0.f;
-  if constexpr (FMT != NM_KV_FP16) {
+  if constexpr (FMT == NM_KV_FP16) {
+    *reinterpret_cast<u32x4*>(out + 2 * hu.first) = p;
+    *reinterpret_cast<u32x4*>(out + 2 * hu.second) = q;
+  } else {
     float amax = 0.f;
     bool bad = false;
 #pragma unroll
-    for (int j = 0; j < 2 * P; ++j) {
-      amax = fmaxf(amax, fabsf(e[j]));
-      bad |= !(fabsf(e[j]) < __builtin_inff());
+    for (int i = 0; i < 8; ++i) {
+      amax = fmaxf(amax, fmaxf(fabsf(e[i]), fabsf(f[i])));
+      bad |= !(fabsf(e[i]) < __builtin_inff()) || !(fabsf(f[i]) < __builtin_inff());
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-    bad = __any(bad);
+    amax = row_max<kLanes>(bad ? __builtin_inff() : amax);
+    bad = amax == __builtin_inff();
     const bool held = !bad && amax >= kTiniest;
-    up = held ? Codes<FMT>::kLargest / amax : 0.f;
-    if (lane == 0)
+    const float up = held ? Codes<FMT>::kLargest / amax : 0.f;
+    if (unit == 0)
       (is_v ? a.cache.v_scale : a.cache.k_scale)[at] =
           bad ? __builtin_nanf("") : held ? amax / Codes<FMT>::kLargest : 0.f;
-    if (bad)
-#pragma unroll
-      for (int j = 0; j < 2 * P; ++j) e[j] = 0.f;
+    u32x2 c = codes_of<FMT>(e, up), d = codes_of<FMT>(f, up);
+    if (bad) c = d = u32x2{0, 0};
+    *reinterpret_cast<u32x2*>(out + hu.first) = c;
+    *reinterpret_cast<u32x2*>(out + hu.second) = d;
   }
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = 128 * p + 2 * lane + j;
-      if (i >= D) continue;
-      const float y = e[2 * p + j];
-      if constexpr (FMT == NM_KV_FP16) {
-        reinterpret_cast<uint16_t*>(out)[i] = uint16_t(float_to_half_bits(y));
-      } else {
-        const float z = fminf(fmaxf(y * up, -Codes<FMT>::kLargest), Codes<FMT>::kLargest);
-        if constexpr (FMT == NM_KV_INT8)
-          out[i] = char(int(rintf(z)));
-        else
-          out[i] = char(__builtin_amdgcn_cvt_pk_fp8_f32(z, z, 0, false) & 0xFF);
-      }
-    }
 }
 
+// Four codes to fp32.
 template <int FMT>
-__device__ __forceinline__ float decode(const char* row, int i) {
-  if constexpr (FMT == NM_KV_FP16) return half_bits_to_float(reinterpret_cast<const uint16_t*>(row)[i]);
-  if constexpr (FMT == NM_KV_INT8) return float(reinterpret_cast<const signed char*>(row)[i]);
-  return __builtin_amdgcn_cvt_f32_fp8(int(uint8_t(row[i])), 0);
+__device__ __forceinline__ void decode4(uint32_t codes, float (&y)[4]) {
+  if constexpr (FMT == NM_KV_E4M3) {
+    y[0] = __builtin_amdgcn_cvt_f32_fp8(int(codes), 0);
+    y[1] = __builtin_amdgcn_cvt_f32_fp8(int(codes), 1);
+    y[2] = __builtin_amdgcn_cvt_f32_fp8(int(codes), 2);
+    y[3] = __builtin_amdgcn_cvt_f32_fp8(int(codes), 3);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = float(int(codes << (24 - 8 * i)) >> 24);
+  }
 }
 
-// One element of k or v per thread.
+// D / 16 lanes per (token, head) row of k, then of v; a copy, widened to fp16.
 template <int D, int FMT>
 __global__ __launch_bounds__(kThreads) void read_kernel(ReadCall a) {
-  const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t all = a.batch * a.tokens * a.cache.kv_heads * D;
-  if (i >= 2 * all) return;
-  const bool is_v = i >= all;
-  const int64_t j = is_v ? i - all : i;
-  const int e = int(j % D), head = int(j / D % a.cache.kv_heads);
-  const int64_t token = j / D / a.cache.kv_heads, b = token / a.tokens;
-  const int t = int(token % a.tokens);
-  float y = 0.f;
+  constexpr int kLanes = RowLanes<D>::kLanes;
+  const uint32_t heads = uint32_t(a.cache.kv_heads), rows = uint32_t(a.batch * a.tokens) * heads;
+  const uint32_t row = blockIdx.x * RowLanes<D>::kRows + threadIdx.x / kLanes;
+  const int unit = threadIdx.x % kLanes;
+  const bool is_v = blockIdx.y != 0;
+  if (row >= rows) return;
+  const uint32_t token = row / heads, b = token / uint32_t(a.tokens);
+  const int head = int(row - token * heads), t = int(token - b * uint32_t(a.tokens));
+  u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
   if (t < count_of(a.count, b, int(a.tokens))) {
     const int64_t at = cache_row(a.cache, b, int64_t(a.start[b]) + t, head);
     if (at >= 0) {
-      y = decode<FMT>((is_v ? a.cache.v : a.cache.k) + at * D * Codes<FMT>::kBytes, e);
-      if constexpr (FMT != NM_KV_FP16) y *= (is_v ? a.cache.v_scale : a.cache.k_scale)[at];
+      const char* in = (is_v ? a.cache.v : a.cache.k) + (at * D + 16 * unit) * Codes<FMT>::kBytes;
+      if constexpr (FMT == NM_KV_FP16) {
+        lo = reinterpret_cast<const u32x4*>(in)[0];
+        hi = reinterpret_cast<const u32x4*>(in)[1];
+      } else {
+        const u32x4 c = *reinterpret_cast<const u32x4*>(in);
+        const float scale = (is_v ? a.cache.v_scale : a.cache.k_scale)[at];
+        float y[2][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float z[4];
+          decode4<FMT>(c[i], z);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[i >> 1][4 * (i & 1) + j] = z[j] * scale;
+        }
+        lo = halves_of(y[0]);
+        hi = halves_of(y[1]);
+      }
     }
   }
-  (is_v ? a.v_out : a.k_out)[j] = uint16_t(float_to_half_bits(y));
+  u32x4* out = reinterpret_cast<u32x4*>((is_v ? a.v_out : a.k_out) + int64_t(row) * D + 16 * unit);
+  out[0] = lo;
+  out[1] = hi;
 }
 
 // One workgroup per sequence, head and side (k or v). Every row is in registers before any is
@@ -209,15 +256,14 @@ struct CompactKernel { static const void* kernel() { return reinterpret_cast<con
 
 hipError_t launch_append(const AppendCall& c, int head_dim, int format, hipStream_t stream, const DeviceInfo& dev) {
   const int64_t rows = c.batch * c.tokens * (c.q_heads + 2 * c.cache.kv_heads);
-  const int64_t grid = (rows + kThreads / 64 - 1) / (kThreads / 64);
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  return by_kind<AppendKernel>(c, head_dim, format, dim3(uint32_t(grid)), stream, dev);
+  const int64_t per = kThreads / (head_dim / 16);
+  return by_kind<AppendKernel>(c, head_dim, format, dim3(uint32_t((rows + per - 1) / per)), stream, dev);
 }
 
 hipError_t launch_read(const ReadCall& c, int head_dim, int format, hipStream_t stream, const DeviceInfo& dev) {
-  const int64_t grid = (2 * c.batch * c.tokens * c.cache.kv_heads * head_dim + kThreads - 1) / kThreads;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  return by_kind<ReadKernel>(c, head_dim, format, dim3(uint32_t(grid)), stream, dev);
+  const int64_t rows = c.batch * c.tokens * c.cache.kv_heads;
+  const int64_t per = kThreads / (head_dim / 16);
+  return by_kind<ReadKernel>(c, head_dim, format, dim3(uint32_t((rows + per - 1) / per), 2), stream, dev);
 }
 
 hipError_t launch_compact(const CompactCall& c, int head_dim, int format, hipStream_t stream, const DeviceInfo& dev) {

@@ -8,7 +8,8 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// One pair (or, past the rotated part, two elements) per thread.
+// Any head size, stride and alignment: one pair (or, past the rotated part, two elements) per
+// thread.
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeCall a) {
   const int units = (a.head_dim + 1) / 2, pairs = a.rope.rot_dim / 2;
   const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
@@ -32,10 +33,60 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeCall a) {
   y[e1] = uint16_t(float_to_half_bits(q * c + p * s));
 }
 
+// Heads of whole 16-element units with 16-byte alignment. A thread keeps one unit's cosines and
+// sines and turns that unit of every `step`-th head of its token, so that they are worked out
+// once for several heads; what is left is a copy, two 16-byte loads and stores a unit.
+__global__ __launch_bounds__(kThreads) void rope_wide_kernel(RopeCall a, int units, int step, int each) {
+  const int unit = threadIdx.x % units, h0 = blockIdx.y * each + threadIdx.x / units;
+  const int64_t token = blockIdx.x;
+  if (int(threadIdx.x) >= units * step) return;
+  const int end = min(a.heads, (int(blockIdx.y) + 1) * each);
+  const HeadUnit hu = head_unit(unit, a.rope.rot_dim, a.rope.layout);
+  const uint16_t* x = a.x + token * a.x_stride;
+  uint16_t* y = a.y + token * a.y_stride;
+  UnitRotation t;
+  if (hu.turned) t = unit_rotation(a.rope, unit, a.rope.positions[token]);
+#pragma unroll 2
+  for (int h = h0; h < end; h += step) {
+    const int64_t at = int64_t(h) * a.head_dim;
+    u32x4 p = *reinterpret_cast<const u32x4*>(x + at + hu.first), q = *reinterpret_cast<const u32x4*>(x + at + hu.second);
+    if (hu.turned) {
+      float e[8], f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        e[i] = half_at(p, i);
+        f[i] = half_at(q, i);
+      }
+      turn_unit(t, a.rope.layout, e, f);
+      p = halves_of(e);
+      q = halves_of(f);
+    }
+    *reinterpret_cast<u32x4*>(y + at + hu.first) = p;
+    *reinterpret_cast<u32x4*>(y + at + hu.second) = q;
+  }
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
 }  // namespace
 
 hipError_t launch_rope(const RopeCall& c, hipStream_t stream, const DeviceInfo& dev) {
   RopeCall a = c;
+  if (aligned16(c.x) && aligned16(c.y) && c.x_stride % 8 == 0 && c.y_stride % 8 == 0 && c.head_dim % 16 == 0 &&
+      c.rope.rot_dim % 16 == 0) {
+    int units = c.head_dim / 16, step = kThreads / units;
+    // one head a thread where that is needed to fill the GPU, else up to kPasses
+    constexpr int kPasses = 4;
+    const int passes = (c.heads + step - 1) / step;
+    const int64_t room = 8 * int64_t(dev.cu_count);
+    int split = passes;
+    if (c.tokens * passes > room) split = int((room + c.tokens - 1) / c.tokens);
+    if (split < (passes + kPasses - 1) / kPasses) split = (passes + kPasses - 1) / kPasses;
+    int each = (passes + split - 1) / split * step;
+    void* args[] = {&a, &units, &step, &each};
+    return launch(reinterpret_cast<const void*>(rope_wide_kernel), dim3(uint32_t(c.tokens), (c.heads + each - 1) / each),
+                  dim3(kThreads), args, 0, stream, dev);
+  }
   const int64_t n = c.tokens * c.heads * ((c.head_dim + 1) / 2);
   const int64_t grid = (n + kThreads - 1) / kThreads;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;

@@ -81,13 +81,13 @@ def _tensor(t, name, dtype, shape, device):
     """Checks a contiguous tensor argument and returns its address (None for None)."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
@@ -127,24 +127,20 @@ def _rows(t, name, ndim, device):
 def _cache_arg(cache, device):
     """The C structure of a cache, with its tensors checked."""
     import torch
-    k = cache.k
+    k, v, k_scale, v_scale = cache
     form = _formats().get(k.dtype)
     if form is None:
         raise ValueError(f"a cache is fp16, int8 or float8_e4m3fn, not {k.dtype}")
     if k.dim() != 4:
         raise ValueError("a cache's k and v must be [blocks, kv_heads, page, head_dim]")
-    shape = tuple(k.shape)
-    s = _CacheStruct()
-    s.k = _tensor(k, "cache.k", k.dtype, shape, device)
-    s.v = _tensor(cache.v, "cache.v", k.dtype, shape, device)
+    shape = k.shape
     if form:
-        if cache.k_scale is None or cache.v_scale is None:
+        if k_scale is None or v_scale is None:
             raise ValueError("an 8-bit cache needs k_scale and v_scale")
-        s.k_scale = _tensor(cache.k_scale, "cache.k_scale", torch.float32, shape[:3], device)
-        s.v_scale = _tensor(cache.v_scale, "cache.v_scale", torch.float32, shape[:3], device)
-    s.blocks, s.kv_heads, s.page, s.head_dim = shape
-    s.format = form
-    return s
+        k_scale = _tensor(k_scale, "cache.k_scale", torch.float32, shape[:3], device)
+        v_scale = _tensor(v_scale, "cache.v_scale", torch.float32, shape[:3], device)
+    return _CacheStruct(_tensor(k, "cache.k", k.dtype, shape, device), _tensor(v, "cache.v", k.dtype, shape, device),
+                        k_scale, v_scale, *shape, form)
 
 
 def _paging(table, first, first_name, count, batch, device):
@@ -157,18 +153,24 @@ def _paging(table, first, first_name, count, batch, device):
             _tensor(count, "count", torch.int32, (batch,), device))
 
 
+_functions = {}   # of the loaded library, by name
+
+
 def _run(name, device, *args):
     """Calls the library on the tensors' device and its current stream."""
     import torch
-    nm = _nm()
-    fn = getattr(nm.lib(), name)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_nm().lib(), name)
+    index = device.index
+    # the stream's handle without a Stream object: 0.1 us in place of 1.9
+    if torch.cuda.current_device() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st:
-        nm._check(name, st)
+        _nm()._check(name, st)
 
 
 def _layout(layout):
@@ -181,7 +183,7 @@ def _turns(turns, device):
     import torch
     if turns.dim() != 1:
         raise ValueError("turns must be [rot_dim / 2]")
-    return _tensor(turns, "turns", torch.float64, tuple(turns.shape), device), 2 * turns.shape[0]
+    return _tensor(turns, "turns", torch.float64, turns.shape, device), 2 * turns.shape[0]
 
 
 def rope_turns(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -207,7 +209,7 @@ def nm_rope(x, positions, turns, layout: str = "half", scale: float = 1.0, out=N
     xp, xs = _rows(x, "x", 3, device)
     tokens, heads, dim = x.shape
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=torch.float16, device=device)
+        out = x.new_empty((tokens, heads, dim))
     elif out.shape != x.shape:
         raise ValueError("out must have x's shape")
     yp, ys = _rows(out, "out", 3, device)
@@ -252,7 +254,7 @@ def nm_rope_kv_append(cache: KVCache, q, k, v, positions, turns, block_table, st
         if q.shape[:2] != k.shape[:2] or q.shape[3] != c.head_dim:
             raise ValueError(f"q must be [{batch}, {tokens}, heads, {c.head_dim}]")
         if out is None:
-            out = torch.empty((batch, tokens, heads, c.head_dim), dtype=torch.float16, device=device)
+            out = q.new_empty((batch, tokens, heads, c.head_dim))
         elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
         op, os_ = _rows(out, "out", 4, device)
@@ -327,7 +329,7 @@ def nm_tree_attention(q, cache: KVCache, block_table, context, mask=None, count=
     if dim != c.head_dim:
         raise ValueError(f"q's heads have {dim} elements, the cache's {c.head_dim}")
     if out is None:
-        out = torch.empty((batch, tokens, heads, dim), dtype=torch.float16, device=device)
+        out = q.new_empty((batch, tokens, heads, dim))
     op = _tensor(out, "out", torch.float16, (batch, tokens, heads, dim), device)
     tp, xp, np_ = _paging(block_table, context, "context", count, batch, device)
     mp = _tensor(mask, "mask", torch.int64, (batch, tokens), device)
@@ -355,7 +357,7 @@ def _verify_args(target, tokens, uniforms, count, workspace):
     given = (_tensor(tokens, "tokens", torch.int32, (batch, nodes), device),
              _tensor(uniforms, "uniforms", torch.float32, (batch, nodes), device),
              _tensor(count, "count", torch.int32, (batch,), device))
-    made = torch.empty(batch, dtype=torch.int32, device=device), torch.empty((batch, nodes), dtype=torch.int32, device=device)
+    made = tokens.new_empty((batch,)), tokens.new_empty((batch, nodes))
     return (device, _tensor(target, "target", torch.float32, (batch, nodes, vocab), device), given, made,
             (batch, nodes, vocab, *_workspace(workspace, device)))
 
@@ -379,7 +381,7 @@ def nm_verify_tree(target, tokens, parents, uniforms, count=None, workspace=None
     import torch
     device, tp, (kp, up, np_), (accepted, out), rest = _verify_args(target, tokens, uniforms, count, workspace)
     batch, nodes, _ = target.shape
-    path = torch.empty((batch, nodes), dtype=torch.int32, device=device)
+    path = tokens.new_empty((batch, nodes))
     _run("nm_verify_tree", device, tp, kp, _tensor(parents, "parents", torch.int32, (batch, nodes), device), up, np_,
          accepted.data_ptr(), out.data_ptr(), path.data_ptr(), *rest)
     return accepted, out, path
