@@ -1,7 +1,12 @@
 // Launch of the attention kernel (nm_attn_impl.h): rows per workgroup, the split of the
 // contexts over the GPU, and the workspace.
+#include <algorithm>
+
 #include "nm_attn_impl.h"
 
+#ifndef NM_WIDEST
+#define NM_WIDEST 4
+#endif
 namespace nm {
 namespace {
 
@@ -16,7 +21,9 @@ template <int FMT, int D>
 const void* kernel_of(int nr) {
   if (nr == 1) return reinterpret_cast<const void*>(attention_kernel<FMT, D, 1>);
   if (nr == 2 || D > 128) return reinterpret_cast<const void*>(attention_kernel<FMT, D, 2>);
-  if constexpr (D <= 128) return reinterpret_cast<const void*>(attention_kernel<FMT, D, 4>);
+  if constexpr (D <= 128)
+    return nr == 3 ? reinterpret_cast<const void*>(attention_kernel<FMT, D, 3>)
+                   : reinterpret_cast<const void*>(attention_kernel<FMT, D, 4>);
   return nullptr;
 }
 
@@ -34,17 +41,20 @@ const void* kernel_of(int format, int head_dim, int nr) {
 Plan plan_of(const AttnCall& c, int head_dim, const DeviceInfo& dev) {
   Plan p;
   const int rows = c.tokens * c.group;
-  p.nr = rows <= 16 ? 1 : rows <= 32 || head_dim > 128 ? 2 : 4;
-  p.row_tiles = (rows + 16 * p.nr - 1) / (16 * p.nr);
+  // row tiles evenly over the fewest workgroups
+  const int tiles = (rows + 15) / 16, widest = head_dim > 128 ? 2 : NM_WIDEST;
+  p.row_tiles = (tiles + widest - 1) / widest;
+  p.nr = (tiles + p.row_tiles - 1) / p.row_tiles;
   p.part_bytes = uint32_t(head_dim / 16 * p.nr * 1024 + p.nr * 128);
   const int64_t items = int64_t(c.batch) * c.cache.kv_heads * p.row_tiles;
   const int64_t most = int64_t(c.cache.table_width) << c.cache.page_shift;
-  const int64_t target = int64_t(dev.cu_count) * attn_waves(head_dim, p.nr);
-  // chunks beyond one a sequence: what fills the GPU once, at most one for every kMinChunkTiles
-  const int64_t longest = (most + kTileKeys * kMinChunkTiles - 1) / (kTileKeys * kMinChunkTiles);
-  int64_t extra = target / (int64_t(c.cache.kv_heads) * p.row_tiles);
-  if (extra > longest * c.batch) extra = longest * c.batch;
-  p.slots = items > NM_DECODE_COUNTER_BYTES / 4 || extra <= c.batch || longest <= 1 ? 0 : int(extra) + c.batch;
+  // Slots for as many workgroups as the GPU holds at once (once more for every two thirds of
+  // them that the sequences themselves take), none for less than a round of the waves.
+  const int64_t room = int64_t(dev.cu_count) * attn_waves(head_dim, p.nr) / (int64_t(c.cache.kv_heads) * p.row_tiles);
+  const int64_t rounds = room > 0 ? (3 * int64_t(c.batch) + 2 * room - 1) / (2 * room) : 0;
+  const int64_t shortest = kTileKeys * kMinChunkTiles;
+  const int64_t slots = std::min(rounds * room, c.batch * ((most + shortest - 1) / shortest));
+  p.slots = items > NM_DECODE_COUNTER_BYTES / 4 || slots <= c.batch ? 0 : int(slots);
   return p;
 }
 

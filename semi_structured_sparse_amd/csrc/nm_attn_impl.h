@@ -2,11 +2,12 @@
 //
 // Mathematics. For one sequence and key head the T nodes' queries of the G query heads that
 // share it are R = T G rows; S^T = K Q^T gives keys down, rows across, the softmax runs over the
-// keys with a running maximum, and O^T = V^T P^T adds up. Each row keeps a reference m in place
-// of the plain maximum: m >= s_j + log2(scale of v_j) - 0.1 over the keys so far (scores in
-// units of log2), so that the weight 2^(s_j - m) scale_j the second product takes in fp16 is at
-// most about 1 whatever the scale of v, and l = sum 2^(s_j - m) is kept beside it in fp32. m
-// moves only when it would grow by more than 8 (weights up to 2^8 are as exact in fp16).
+// keys with a running maximum, and O^T = V^T P^T adds up. A value's scale z_j goes into the
+// exponent: with x_j = s_j + log2 z_j (scores in units of log2) the weight that the second
+// product takes in fp16 is 2^(x_j - m), and l = sum 2^(x_j - m) / z_j is kept in fp32. Each row's
+// reference m is the largest x_j so far, so the weights stay in fp16's range whatever the
+// scales of v; it moves only when it would grow by more than 8 (weights up to 2^8 are as exact
+// in fp16), which takes the maximum over lanes and the rescaling out of most tiles.
 //
 // Work split. A workgroup of 4 waves takes one key head's rows (16 NR of them) and a chunk of
 // one sequence's keys; its waves take every fourth tile of 32 keys, so that no K or V passes
@@ -33,6 +34,10 @@ constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kTileKeys = 32;
 constexpr int kMinChunkTiles = kAttnWaves;   // one tile a wave
+constexpr float kLowest = -3e38f;            // the reference of a row that has seen nothing
+// A value's scale counts as at least this (rows of zeros have scale 0, and codes 0): far below
+// what fp16 results can show, and its reciprocal times any number of keys is finite.
+constexpr float kLeastScale = 0x1p-100f;
 
 // How the host cuts a call up: `slots` chunks over all sequences (0: one a sequence), row_tiles
 // workgroups of rows, and where the chunks' partial results go.
@@ -52,14 +57,15 @@ struct AttnShape {
   static constexpr int kLoadsK = kRowBytes / 64;      // 16-byte loads of a key row by its 4 lanes
   static constexpr int kWordsV = kRowBytes / 64;      // dwords of a value row by its 16 lanes
   static constexpr int kJ = D / 16;                   // d tiles
-  static constexpr int kOwn = kJ * NR / kAttnWaves;   // (row tile, d tile) units a wave ends up with
+  static constexpr int kOwn = kJ / kAttnWaves;        // d tiles of each row tile a wave ends up with
   static constexpr int kPer = kOwn < 2 ? kOwn : 2;    // of them exchanged in a round
   static constexpr uint32_t kPartBytes = kJ * NR * 1024 + NR * 128;
 };
 
 // Waves a SIMD holds (its 512 registers a lane over the accumulators, Q and one tile), which is
 // also the workgroups a CU holds.
-constexpr int attn_waves(int D, int NR) { return D > 128 ? (NR == 1 ? 2 : 1) : NR == 1 ? 3 : NR == 2 ? 2 : 1; }
+constexpr int kPairRows = 2;
+constexpr int attn_waves(int D, int NR) { return D > 128 ? (NR == 1 ? 2 : 1) : NR == 1 ? 3 : NR <= kPairRows ? 2 : 1; }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -215,7 +221,7 @@ struct AttnWave {
     for (int x = 0; x < 4 / S::kCodeBytes; ++x) f[x] = as_half8(w[x]);
   }
 
-  // The scores of a tile, in units of log2: x[n][e] is this lane's row n, key 8 g + e.
+  // The scores of a tile in units of log2, without log2 z: x[n][e] is this lane's row n, key 8 g + e.
   __device__ __forceinline__ void scores(const AttnTile<FMT, D>& t, float (&x)[NR][8]) const {
     f32x4 s[NR][2];
 #pragma unroll
@@ -255,49 +261,67 @@ struct AttnWave {
     return seen;
   }
 
-  // The softmax's weights of a tile, times the values' scales, in fp16; the running reference
-  // and sum. edge: the tile holds keys that not every node sees, or that are past the end.
-  __device__ __forceinline__ void weights(const AttnTile<FMT, D>& t, float (&x)[NR][8], f16x8 (&w)[NR], bool edge,
+  // The softmax's weights of a tile in fp16; the running reference and sum. edge: the tile holds
+  // keys that not every node sees, or that are past the end.
+  __device__ __forceinline__ void weights(AttnTile<FMT, D>& t, float (&x)[NR][8], f16x8 (&w)[NR], bool edge,
                                           uint32_t key0) {
-    float lg[8];   // log2 of the value's scale to within 0.1, from the float's bits
+    uint32_t bad = 0;   // keys of a draft whose scale is not a number: rows that see them are NaN
+    if constexpr (FMT != NM_KV_FP16) {
+      if (edge) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      lg[e] = FMT == NM_KV_FP16 ? 0.f : fmaxf(float(__float_as_int(t.vs[e])) * 0x1p-23f - 127.0f, -100.0f);
+        for (int e = 0; e < 8; ++e) {
+          const bool b = !(t.vs[e] < __builtin_inff());
+          bad |= uint32_t(b) << e;
+          if (b) t.vs[e] = 1.0f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        t.vs[e] = t.vs[e] < kLeastScale ? kLeastScale : t.vs[e];   // NaN stays
+        const float lz = __builtin_amdgcn_logf(t.vs[e]);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) x[n][e] += lz;
+      }
+    }
+    if (edge) {
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const uint32_t seen = seen_of(n, key0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if ((bad >> e) & 1) x[n][e] = __builtin_nanf("");
+          if (!((seen >> e) & 1)) x[n][e] = -__builtin_inff();
+        }
+      }
+    }
+    float top[NR];
+    bool grows = false;
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      uint32_t seen = 0xFF;
-      if (edge) {
-        seen = seen_of(n, key0);
+      top[n] = fmaxf(fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])),
+                     fmaxf(fmaxf(x[n][4], x[n][5]), fmaxf(x[n][6], x[n][7])));
+      grows |= top[n] > m[n] + 8.0f;
+    }
+    if (__any(grows)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (!((seen >> e) & 1)) x[n][e] = -__builtin_inff();
-      }
-      float top = -__builtin_inff();
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, FMT == NM_KV_FP16 ? x[n][e] : x[n][e] + lg[e]);
-      top = max4(top);
-      if (__any(top > m[n] + 8.0f)) {
-        const float next = fmaxf(m[n], top);
-        const float f = next > -__builtin_inff() ? exp2_fast(m[n] - next) : 1.0f;
+      for (int n = 0; n < NR; ++n) {
+        const float next = fmaxf(m[n], max4(top[n]));
+        const float f = exp2_fast(m[n] - next);
         m[n] = next;
         l[n] *= f;
 #pragma unroll
         for (int j = 0; j < S::kJ; ++j) o[j][n] *= f;
       }
-      const float ref = m[n] > -__builtin_inff() ? m[n] : 0.f;
+    }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float p = exp2_fast(x[n][e] - ref);
-        l[n] += p;
-        x[n][e] = FMT == NM_KV_FP16 ? p : p * t.vs[e];
+    for (int e = 0; e < 8; ++e) {
+      const float iz = FMT == NM_KV_FP16 ? 1.0f : __builtin_amdgcn_rcpf(t.vs[e]);
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const float y = exp2_fast(x[n][e] - m[n]);
+        l[n] = FMT == NM_KV_FP16 ? l[n] + y : fmaf(y, iz, l[n]);
+        w[n][e] = _Float16(y);   // to nearest even: 2^-11 of the weight
       }
-      if (edge) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (!((seen >> e) & 1)) x[n][e] = 0.f;   // 0 times a scale that may be NaN
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[n][e] = _Float16(x[n][e]);   // to nearest even: 2^-11 of the weight
     }
   }
 
@@ -389,34 +413,44 @@ __device__ __forceinline__ void attn_lengths(const AttnCall& a, int b, uint32_t&
   keys = uint32_t(min(int64_t(context) + count, most));
 }
 
+__device__ __forceinline__ uint32_t chunks_of(uint32_t tiles, uint32_t per) {
+  return tiles <= per ? 1u : (tiles + per - 1) / per;
+}
+
 // Every wave works this out for itself: 64 sequences a pass, one a lane.
 __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, int slot) {
   const int lane = threadIdx.x & 63;
-  AttnChunk k;
-  k.b = -1;
+  const auto tiles_of = [&](int b) {
+    uint32_t context, keys = 0;
+    int count;
+    if (b < a.batch) attn_lengths(a, b, context, keys, count);
+    return (keys + kTileKeys - 1) / kTileKeys;
+  };
   uint32_t per = 0x7FFFFFFFu;
   if (slots > a.batch) {
     double total = 0.0;
-    for (int b0 = 0; b0 < a.batch; b0 += 64) {
-      uint32_t context, keys = 0;
-      int count;
-      if (b0 + lane < a.batch) attn_lengths(a, b0 + lane, context, keys, count);
-      total += double((keys + kTileKeys - 1) / kTileKeys);
-    }
+    for (int b0 = 0; b0 < a.batch; b0 += 64) total += double(tiles_of(b0 + lane));
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) total += __shfl_xor(total, o);
-    // rounded up to whole rounds of the workgroup's waves
-    const double even = ceil(total / (double(slots - a.batch) * kAttnWaves));
-    per = even < 1.0 ? kAttnWaves : uint32_t(even) * kAttnWaves;
+    // The last chunk of a sequence is half empty on average: that many slots are set aside, and
+    // one a sequence, which always fits, if they do not do. Whole rounds of the waves.
+    const double half = ceil(total / ((double(slots) - 0.5 * a.batch) * kAttnWaves));
+    per = half < 1.0 ? kAttnWaves : uint32_t(half) * kAttnWaves;
+    uint32_t used = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) used += b0 + lane < a.batch ? chunks_of(tiles_of(b0 + lane), per) : 0u;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) used += __shfl_xor(used, o);
+    if (used > uint32_t(slots)) per = uint32_t(ceil(total / (double(slots - a.batch) * kAttnWaves))) * kAttnWaves;
   }
+  AttnChunk k;
+  k.b = -1;
   int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
     uint32_t context = 0, keys = 0;
     int count = 0, n = 0;
     if (b0 + lane < a.batch) {
       attn_lengths(a, b0 + lane, context, keys, count);
-      const uint32_t tiles = (keys + kTileKeys - 1) / kTileKeys;
-      n = tiles <= per ? 1 : int((tiles + per - 1) / per);
+      n = int(chunks_of((keys + kTileKeys - 1) / kTileKeys, per));
     }
     int upto = n;
 #pragma unroll
@@ -480,7 +514,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, NR)) void attention_ker
       const int d = FMT == NM_KV_FP16 ? 32 * st + 8 * w.g : 64 * (st >> 1) + 16 * w.g + 8 * (st & 1);
       w.q[n][st] = live ? *reinterpret_cast<const u32x4*>(qr + d) : u32x4{0, 0, 0, 0};
     }
-    w.m[n] = -__builtin_inff();
+    w.m[n] = kLowest;
     w.l[n] = 0.f;
 #pragma unroll
     for (int j = 0; j < S::kJ; ++j) w.o[j][n] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -529,114 +563,161 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, NR)) void attention_ker
   float mm[NR], ll[NR];
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    mm[n] = -__builtin_inff();
+    mm[n] = kLowest;
     ll[n] = 0.f;
 #pragma unroll
     for (int x = 0; x < kAttnWaves; ++x) mm[n] = fmaxf(mm[n], stat_m[x][16 * n + w.li]);
-    const float ref = mm[n] > -__builtin_inff() ? mm[n] : 0.f;
 #pragma unroll
-    for (int x = 0; x < kAttnWaves; ++x) ll[n] += stat_l[x][16 * n + w.li] * exp2_fast(stat_m[x][16 * n + w.li] - ref);
-    const float f = exp2_fast(w.m[n] - ref);
+    for (int x = 0; x < kAttnWaves; ++x) ll[n] += stat_l[x][16 * n + w.li] * exp2_fast(stat_m[x][16 * n + w.li] - mm[n]);
+    const float f = exp2_fast(w.m[n] - mm[n]);
 #pragma unroll
     for (int j = 0; j < S::kJ; ++j) w.o[j][n] *= f;
   }
-  f32x4 own[S::kOwn];
+  f32x4 own[NR][S::kOwn];
 #pragma unroll
-  for (int r = 0; r < S::kOwn / S::kPer; ++r) {
-    if (r) __syncthreads();
+  for (int n = 0; n < NR; ++n)
 #pragma unroll
-    for (int x = 0; x < kAttnWaves; ++x)
+    for (int r = 0; r < S::kOwn / S::kPer; ++r) {
+      if (n + r) __syncthreads();
+#pragma unroll
+      for (int x = 0; x < kAttnWaves; ++x)
+#pragma unroll
+        for (int k = 0; k < S::kPer; ++k) xch[wave][x * S::kPer + k][w.lane] = w.o[x * S::kOwn + r * S::kPer + k][n];
+      __syncthreads();
 #pragma unroll
       for (int k = 0; k < S::kPer; ++k) {
-        const int u = x * S::kOwn + r * S::kPer + k;
-        xch[wave][x * S::kPer + k][w.lane] = w.o[u % S::kJ][u / S::kJ];
+        f32x4 sum = xch[0][wave * S::kPer + k][w.lane];
+#pragma unroll
+        for (int x = 1; x < kAttnWaves; ++x) sum += xch[x][wave * S::kPer + k][w.lane];
+        own[n][r * S::kPer + k] = sum;
       }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < S::kPer; ++k) {
-      f32x4 sum = xch[0][wave * S::kPer + k][w.lane];
-#pragma unroll
-      for (int x = 1; x < kAttnWaves; ++x) sum += xch[x][wave * S::kPer + k][w.lane];
-      own[r * S::kPer + k] = sum;
     }
-  }
-  // a wave's units are kOwn neighbouring d tiles of one row tile
-  const int n = wave * S::kOwn / S::kJ, j0 = wave * S::kOwn % S::kJ;
-  const int r = (rt * NR + n) * 16 + w.li;
-  float m1 = mm[0], l1 = ll[0];
+  // d tiles wave * kOwn + k of every row tile are this wave's now
+  int row[NR];
 #pragma unroll
-  for (int x = 1; x < NR; ++x)
-    if (n == x) {
-      m1 = mm[x];
-      l1 = ll[x];
-    }
+  for (int n = 0; n < NR; ++n) row[n] = (rt * NR + n) * 16 + w.li;
 
-  if (chunks > 1) {
-    const uint64_t item = (uint64_t(slot) * a.cache.kv_heads + head) * sp.row_tiles + rt;
-    const uint64_t item0 = (uint64_t(first) * a.cache.kv_heads + head) * sp.row_tiles + rt;
-    const uint64_t stride = uint64_t(a.cache.kv_heads) * sp.row_tiles * S::kPartBytes;
-    __amdgpu_buffer_rsrc_t buf = coherent_buffer(sp.parts + item * S::kPartBytes, S::kPartBytes);
-    if (r < rows) {
+  if (chunks == 1) {
 #pragma unroll
-      for (int k = 0; k < S::kOwn; ++k)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, own[k]), buf,
-                                               ((wave * S::kOwn + k) * 64 + w.lane) * 16, 0, kCoherent);
-      if (j0 == 0 && w.g == 0) {
-        const u32x2 x = {__float_as_uint(m1), __float_as_uint(l1)};
-        __builtin_amdgcn_raw_buffer_store_b64(x, buf, S::kJ * NR * 1024 + (16 * n + w.li) * 8, 0, kCoherent);
+    for (int n = 0; n < NR; ++n) {
+      if (row[n] >= rows) continue;
+      const int t = row[n] / a.group;
+      const float inv = t < count && ll[n] != 0.f ? 1.0f / ll[n] : 0.f;
+      uint16_t* out = a.out + ((int64_t(b) * a.tokens + t) * a.heads + head * a.group + row[n] % a.group) * D;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        typedef uint16_t run_t __attribute__((ext_vector_type(S::kOwn)));
+        run_t y;
+#pragma unroll
+        for (int k = 0; k < S::kOwn; ++k) y[k] = uint16_t(float_to_half_bits(inv == 0.f ? 0.f : own[n][k][i] * inv));
+        *reinterpret_cast<run_t*>(out + S::kJ * (4 * w.g + i) + wave * S::kOwn) = y;
       }
     }
-    __builtin_amdgcn_s_waitcnt(0);   // the partial has reached the coherence point
-    __syncthreads();
-    uint32_t* counter = sp.counters + (int64_t(b) * a.cache.kv_heads + head) * sp.row_tiles + rt;
-    if (tid == 0) arrived = atomicAdd(counter, 1u);
-    __syncthreads();
-    if (arrived != uint32_t(chunks - 1)) return;
-    // the last of the sequence's chunks: all partials are complete
-    if (tid == 0) atomicExch(counter, 0u);
-    char* p0 = sp.parts + item0 * S::kPartBytes;
-    const uint32_t stat = S::kJ * NR * 1024 + (16 * n + w.li) * 8;
-    m1 = -__builtin_inff();
-    for (int c = w.g; c < chunks; c += 4) {
-      __amdgpu_buffer_rsrc_t pc = coherent_buffer(p0 + c * stride, S::kPartBytes);
-      if (r < rows) m1 = fmaxf(m1, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(pc, stat, 0, kCoherent)));
-    }
-    m1 = max4(m1);
-    const float ref = m1 > -__builtin_inff() ? m1 : 0.f;
-    l1 = 0.f;
+    return;
+  }
+
+  // A chunk's partial: the rows' {m, l}, then 16 bytes (4 d's) for each (d tile, lane group, row),
+  // rows fastest; `live` rows of this workgroup's are real.
+  const int live = min(16 * NR, rows - rt * 16 * NR), units = live * (D / 4);
+  const uint32_t stride = uint32_t(a.cache.kv_heads) * uint32_t(sp.row_tiles) * S::kPartBytes;
+  char* p0 = sp.parts + ((uint64_t(first) * a.cache.kv_heads + head) * sp.row_tiles + rt) * S::kPartBytes;
+  constexpr uint32_t kStats = 16 * NR * 8;
+  __amdgpu_buffer_rsrc_t buf = coherent_buffer(p0, (chunks - 1) * stride + S::kPartBytes);
+  const uint32_t mine = (slot - first) * stride;
 #pragma unroll
-    for (int k = 0; k < S::kOwn; ++k) own[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (r < rows) {
-#pragma unroll 4
-      for (int c = 0; c < chunks; ++c) {
-        __amdgpu_buffer_rsrc_t pc = coherent_buffer(p0 + c * stride, S::kPartBytes);
-        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(pc, stat, 0, kCoherent);
-        f32x4 y[S::kOwn];
+  for (int n = 0; n < NR; ++n) {
+    if (row[n] >= rows) continue;
+    const int r = 16 * n + w.li;
 #pragma unroll
-        for (int k = 0; k < S::kOwn; ++k)
-          y[k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                               pc, ((wave * S::kOwn + k) * 64 + w.lane) * 16, 0, kCoherent));
-        const float f = exp2_fast(__uint_as_float(x[0]) - ref);
-        l1 += __uint_as_float(x[1]) * f;
-#pragma unroll
-        for (int k = 0; k < S::kOwn; ++k) own[k] += y[k] * f;
-      }
+    for (int k = 0; k < S::kOwn; ++k)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, own[n][k]), buf,
+                                             mine + kStats + (((wave * S::kOwn + k) * 4 + w.g) * live + r) * 16, 0, kCoherent);
+    if (wave == 0 && w.g == 0) {
+      const u32x2 x = {__float_as_uint(mm[n]), __float_as_uint(ll[n])};
+      __builtin_amdgcn_raw_buffer_store_b64(x, buf, mine + r * 8, 0, kCoherent);
     }
   }
-  if (r >= rows) return;
-  const int t = r / a.group;
-  const float inv = t < count && l1 != 0.f ? 1.0f / l1 : 0.f;
-  uint16_t* out = a.out + ((int64_t(b) * a.tokens + t) * a.heads + head * a.group + r % a.group) * D;
+  __builtin_amdgcn_s_waitcnt(0);   // the partial has reached the coherence point
+  __syncthreads();
+  uint32_t* counter = sp.counters + (int64_t(b) * a.cache.kv_heads + head) * sp.row_tiles + rt;
+  if (tid == 0) arrived = atomicAdd(counter, 1u);
+  __syncthreads();
+  if (arrived != uint32_t(chunks - 1)) return;
+  if (tid == 0) atomicExch(counter, 0u);
+  // The last of the sequence's chunks: all partials are complete. A thread takes units of 16
+  // bytes of every `groups`-th chunk, 8 chunks' loads in flight; the groups' sums, and then the
+  // rows, come together in LDS. The order is fixed, so the result is the same each time.
+  float* sum = reinterpret_cast<float*>(xch);                 // [row][d]
+  const int groups = units < kAttnThreads ? kAttnThreads / units : 1;
+  const int grp = groups > 1 ? tid / units : 0;
+  constexpr int U = 8;
+  // the rows' references and sums: up to 16 threads a row, then one
+  const int threads = min(16, kAttnThreads / live);
+  const int r0 = tid % live, s0 = tid / live;
+  float2* stat = reinterpret_cast<float2*>(xch);
+  if (s0 < threads) {
+    float m1 = kLowest, l1 = 0.f;
+    for (int c0 = s0; c0 < chunks; c0 += threads * U) {
+      u32x2 x[U];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    typedef uint16_t row_t __attribute__((ext_vector_type(S::kOwn)));
-    row_t y;
+      for (int k = 0; k < U; ++k)
+        x[k] = __builtin_amdgcn_raw_buffer_load_b64(buf, min(c0 + k * threads, chunks - 1) * stride + r0 * 8, 0, kCoherent);
 #pragma unroll
-    for (int k = 0; k < S::kOwn; ++k) {
-      const float v = own[k][i] * inv;
-      y[k] = uint16_t(float_to_half_bits(inv == 0.f ? 0.f : v));
+      for (int k = 0; k < U; ++k) {
+        if (c0 + k * threads >= chunks) continue;
+        const float m2 = __uint_as_float(x[k][0]), next = fmaxf(m1, m2);
+        l1 = l1 * exp2_fast(m1 - next) + __uint_as_float(x[k][1]) * exp2_fast(m2 - next);
+        m1 = next;
+      }
     }
-    *reinterpret_cast<row_t*>(out + S::kJ * (4 * w.g + i) + j0) = y;
+    stat[s0 * live + r0] = make_float2(m1, l1);
+  }
+  __syncthreads();
+  if (tid < live) {
+    float m1 = kLowest, l1 = 0.f;
+    for (int x = 0; x < threads; ++x) m1 = fmaxf(m1, stat[x * live + tid].x);
+    for (int x = 0; x < threads; ++x) l1 += stat[x * live + tid].y * exp2_fast(stat[x * live + tid].x - m1);
+    stat_m[0][tid] = m1;
+    stat_l[0][tid] = l1;
+  }
+  __syncthreads();
+  for (int u0 = groups > 1 ? tid - grp * units : tid; u0 < units; u0 += kAttnThreads) {
+    if (grp >= groups) break;
+    const int r = u0 % live, jg = u0 / live, j = jg >> 2, g = jg & 3;
+    const float top = stat_m[0][r];
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = grp; c0 < chunks; c0 += groups * U) {
+      u32x4 y[U];
+      uint32_t mc[U];
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        const uint32_t at = min(c0 + x * groups, chunks - 1) * stride;
+        mc[x] = __builtin_amdgcn_raw_buffer_load_b32(buf, at + r * 8, 0, kCoherent);
+        y[x] = __builtin_amdgcn_raw_buffer_load_b128(buf, at + kStats + u0 * 16, 0, kCoherent);
+      }
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        if (c0 + x * groups >= chunks) continue;
+        acc += __builtin_bit_cast(f32x4, y[x]) * exp2_fast(__uint_as_float(mc[x]) - top);
+      }
+    }
+    float* at = sum + (grp * live + r) * D + S::kJ * 4 * g + j;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at[S::kJ * i] = acc[i];
+  }
+  __syncthreads();
+  for (int u = tid; u < live * (D / 8); u += kAttnThreads) {
+    const int r = u / (D / 8), d = u % (D / 8) * 8, node = (rt * NR * 16 + r) / a.group;
+    const float l1 = stat_l[0][r], inv = node < count && l1 != 0.f ? 1.0f / l1 : 0.f;
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] = 0.f;
+      for (int x = 0; x < groups; ++x) y[e] += sum[(x * live + r) * D + d + e];
+      y[e] = inv == 0.f ? 0.f : y[e] * inv;
+    }
+    *reinterpret_cast<u32x4*>(a.out + ((int64_t(b) * a.tokens + node) * a.heads + head * a.group +
+                                       (rt * NR * 16 + r) % a.group) * D + d) = halves_of(y);
   }
 }
 

@@ -184,50 +184,56 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadCall a) {
   out[1] = hi;
 }
 
-// One workgroup per sequence, head and side (k or v). Every row is in registers before any is
-// written: destinations of some rows are sources of others.
+// One workgroup per sequence, head and side (k or v). The rows' places are looked up by a
+// thread each; then every row is in registers before any is written: destinations of some rows
+// are sources of others. Bound by its chain of dependent loads (path, page table, rows).
 template <int D, int FMT>
 __global__ __launch_bounds__(kThreads) void compact_kernel(CompactCall a) {
   constexpr int kChunks = D * Codes<FMT>::kBytes / 16;           // 16-byte pieces of a row
   constexpr int kEach = (kMaxNodes * kChunks + kThreads - 1) / kThreads;
+  __shared__ int64_t from[kMaxNodes], into[kMaxNodes];
+  const int tid = threadIdx.x;
   const int head = blockIdx.x % a.cache.kv_heads;
-  const bool is_v = blockIdx.x / a.cache.kv_heads;
+  const bool is_v = int(blockIdx.x) >= a.cache.kv_heads;
   const int64_t b = blockIdx.y;
-  char* base = is_v ? a.cache.v : a.cache.k;
+  u32x4* base = reinterpret_cast<u32x4*>(is_v ? a.cache.v : a.cache.k);
   float* scales = is_v ? a.cache.v_scale : a.cache.k_scale;
+  float scale = 0.f;
+  int64_t scale_into = -1;
   const int accepted = count_of(a.accepted, b, a.nodes - 1);
-  const int64_t start = a.start[b];
-  uint4 held[kEach];
-  int64_t to[kEach];
+  if (tid < kMaxNodes) {
+    int64_t f = -1, t = -1;
+    if (tid < a.nodes) {
+      const int node = a.path[b * a.nodes + tid];
+      const int64_t start = a.start[b];
+      if (tid >= 1 && tid <= accepted && node >= 0 && node < a.nodes && node != tid) {
+        f = cache_row(a.cache, b, start + node, head);
+        t = cache_row(a.cache, b, start + tid, head);
+        if (f < 0) t = -1;
+        if (FMT != NM_KV_FP16 && t >= 0) {
+          scale = scales[f];
+          scale_into = t;
+        }
+      }
+    }
+    from[tid] = f;
+    into[tid] = t;
+  }
+  __syncthreads();
+  u32x4 held[kEach];
 #pragma unroll
   for (int j = 0; j < kEach; ++j) {
-    const int piece = threadIdx.x + kThreads * j, d = piece / kChunks + 1;
-    to[j] = -1;
-    if (d > accepted) continue;
-    const int node = a.path[b * a.nodes + d];
-    if (node < 0 || node >= a.nodes || node == d) continue;
-    const int64_t from = cache_row(a.cache, b, start + node, head);
-    const int64_t into = cache_row(a.cache, b, start + d, head);
-    if (from < 0 || into < 0) continue;
-    held[j] = reinterpret_cast<const uint4*>(base + from * D * Codes<FMT>::kBytes)[piece % kChunks];
-    to[j] = into * kChunks + piece % kChunks;
-  }
-  float scale = 0.f;
-  int64_t scale_to = -1;
-  if (FMT != NM_KV_FP16 && threadIdx.x >= 1 && int(threadIdx.x) <= accepted) {
-    const int node = a.path[b * a.nodes + threadIdx.x];
-    if (node >= 0 && node < a.nodes) {
-      const int64_t from = cache_row(a.cache, b, start + node, head);
-      scale_to = cache_row(a.cache, b, start + threadIdx.x, head);
-      if (from >= 0 && scale_to >= 0) scale = scales[from]; else scale_to = -1;
-    }
+    const int piece = tid + kThreads * j, d = piece / kChunks;
+    if (d < kMaxNodes && into[d] >= 0) held[j] = base[from[d] * kChunks + piece % kChunks];
   }
   __builtin_amdgcn_s_waitcnt(0);   // the loads have returned
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kEach; ++j)
-    if (to[j] >= 0) reinterpret_cast<uint4*>(base)[to[j]] = held[j];
-  if (scale_to >= 0) scales[scale_to] = scale;
+  for (int j = 0; j < kEach; ++j) {
+    const int piece = tid + kThreads * j, d = piece / kChunks;
+    if (d < kMaxNodes && into[d] >= 0) base[into[d] * kChunks + piece % kChunks] = held[j];
+  }
+  if (scale_into >= 0) scales[scale_into] = scale;
 }
 
 template <template <int, int> class K, class Call>
