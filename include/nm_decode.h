@@ -149,8 +149,8 @@ int nm_kv_compact(const nm_kv_cache* cache, const int32_t* table, int64_t table_
  * where bit i of mask[b][t] is set and i < count[b] (mask NULL: a chain, node t sees nodes
  * 0 .. t). Query head h reads key head h / (heads / kv_heads). A node that sees no key, and
  * nodes at or past count, get zeros. Keys that a node does not see do not touch its result,
- * whatever they hold (NaN and infinities too). An infinity or NaN in a draft's fp16 v makes
- * that element NaN for the nodes that see it. fp16 products of exact codes, fp32 sums; the
+ * whatever they hold (NaN and infinities too). A draft whose v row has an infinity or
+ * NaN in it makes the results of the nodes that see it NaN. fp16 products of exact codes, fp32 sums; the
  * weights times v's scale are rounded to fp16 (relative 2^-11) for the second product. Bit-identical from run
  * to run for the same lengths and workspace.
  *   q     fp16, token (b, t)'s head h at [(b * tokens + t) * q_stride + h * head_dim]; 16-byte

@@ -17,28 +17,38 @@ struct Plan {
   uint32_t part_bytes;
 };
 
+struct Kernel {
+  const void* f;
+  int waves;       // workgroups of a CU
+  int lds;
+};
+
+template <int FMT, int D, int NR>
+Kernel kernel_of() {
+  using S = AttnShape<FMT, D, NR>;
+  return {reinterpret_cast<const void*>(attention_kernel<FMT, D, NR>), S::kWaves, S::kLdsBytes};
+}
+
 template <int FMT, int D>
-const void* kernel_of(int nr) {
-  if (nr == 1) return reinterpret_cast<const void*>(attention_kernel<FMT, D, 1>);
-  if (nr == 2 || D > 128) return reinterpret_cast<const void*>(attention_kernel<FMT, D, 2>);
-  if constexpr (D <= 128)
-    return nr == 3 ? reinterpret_cast<const void*>(attention_kernel<FMT, D, 3>)
-                   : reinterpret_cast<const void*>(attention_kernel<FMT, D, 4>);
-  return nullptr;
+Kernel kernel_of(int nr) {
+  if (nr == 1) return kernel_of<FMT, D, 1>();
+  if (nr == 2 || D > 128) return kernel_of<FMT, D, 2>();
+  if constexpr (D <= 128) return nr == 3 ? kernel_of<FMT, D, 3>() : kernel_of<FMT, D, 4>();
+  return {};
 }
 
 template <int FMT>
-const void* kernel_of(int head_dim, int nr) {
+Kernel kernel_of(int head_dim, int nr) {
   return head_dim == 64 ? kernel_of<FMT, 64>(nr) : head_dim == 128 ? kernel_of<FMT, 128>(nr) : kernel_of<FMT, 256>(nr);
 }
 
-const void* kernel_of(int format, int head_dim, int nr) {
+Kernel kernel_of(int format, int head_dim, int nr) {
   return format == NM_KV_FP16   ? kernel_of<NM_KV_FP16>(head_dim, nr)
          : format == NM_KV_INT8 ? kernel_of<NM_KV_INT8>(head_dim, nr)
                                 : kernel_of<NM_KV_E4M3>(head_dim, nr);
 }
 
-Plan plan_of(const AttnCall& c, int head_dim, const DeviceInfo& dev) {
+Plan plan_of(const AttnCall& c, int head_dim, int format, const DeviceInfo& dev) {
   Plan p;
   const int rows = c.tokens * c.group;
   // row tiles evenly over the fewest workgroups
@@ -50,7 +60,7 @@ Plan plan_of(const AttnCall& c, int head_dim, const DeviceInfo& dev) {
   const int64_t most = int64_t(c.cache.table_width) << c.cache.page_shift;
   // Slots for as many workgroups as the GPU holds at once (once more for every two thirds of
   // them that the sequences themselves take), none for less than a round of the waves.
-  const int64_t room = int64_t(dev.cu_count) * attn_waves(head_dim, p.nr) / (int64_t(c.cache.kv_heads) * p.row_tiles);
+  const int64_t room = int64_t(dev.cu_count) * kernel_of(format, head_dim, p.nr).waves / (int64_t(c.cache.kv_heads) * p.row_tiles);
   const int64_t rounds = room > 0 ? (3 * int64_t(c.batch) + 2 * room - 1) / (2 * room) : 0;
   const int64_t shortest = kTileKeys * kMinChunkTiles;
   const int64_t slots = std::min(rounds * room, c.batch * ((most + shortest - 1) / shortest));
@@ -65,14 +75,14 @@ size_t plan_bytes(const AttnCall& c, const Plan& p) {
 
 }  // namespace
 
-size_t attention_workspace_bytes(const AttnCall& c, int head_dim, int, const DeviceInfo& dev) {
-  return plan_bytes(c, plan_of(c, head_dim, dev));
+size_t attention_workspace_bytes(const AttnCall& c, int head_dim, int format, const DeviceInfo& dev) {
+  return plan_bytes(c, plan_of(c, head_dim, format, dev));
 }
 
 hipError_t launch_attention(const AttnCall& c, int head_dim, int format, void* workspace, size_t workspace_bytes,
                             hipStream_t stream, const DeviceInfo& dev) {
   AttnCall a = c;
-  Plan p = plan_of(c, head_dim, dev);
+  Plan p = plan_of(c, head_dim, format, dev);
   if (workspace == nullptr || workspace_bytes < plan_bytes(c, p)) p.slots = 0;
   AttnSplit sp{p.slots, p.row_tiles, static_cast<uint32_t*>(workspace),
                p.slots ? static_cast<char*>(workspace) + NM_DECODE_COUNTER_BYTES : nullptr, p.part_bytes};
@@ -81,8 +91,8 @@ hipError_t launch_attention(const AttnCall& c, int head_dim, int format, void* w
   // puts them on one XCD's L2.
   const int64_t wide = (int64_t(p.slots ? p.slots : c.batch) * c.cache.kv_heads + 7) / 8 * 8;
   if (wide > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  return launch(kernel_of(format, head_dim, p.nr), dim3(uint32_t(wide), uint32_t(p.row_tiles)), dim3(kAttnThreads), args,
-                0, stream, dev);
+  const Kernel k = kernel_of(format, head_dim, p.nr);
+  return launch(k.f, dim3(uint32_t(wide), uint32_t(p.row_tiles)), dim3(kAttnThreads), args, size_t(k.lds), stream, dev);
 }
 
 }  // namespace nm

@@ -49,23 +49,44 @@ struct AttnSplit {
   uint32_t part_bytes;
 };
 
+// Waves of a SIMD, which are also the workgroups of a CU: by the registers of NR row tiles, and
+// by the LDS of one tile in flight a wave.
+constexpr int attn_waves(int D, int row_bytes, int NR) {
+  const int by_rows = D * NR <= 64 ? 4 : D * NR <= 128 ? 3 : D * NR <= 256 && NR <= 2 ? 2 : 1, by_lds = row_bytes <= 128 ? 4 : row_bytes == 256 ? 2 : 1;
+  return by_rows < by_lds ? by_rows : by_lds;
+}
+
+// What a kernel variant holds: registers and LDS set the waves of a SIMD (the workgroups of a
+// CU), the row bytes the loads of a tile, and what is left of the 160 KiB the tiles in flight.
 template <int FMT, int D, int NR>
 struct AttnShape {
   static constexpr int kCodeBytes = FMT == NM_KV_FP16 ? 2 : 1;
   static constexpr int kRowBytes = D * kCodeBytes;
   static constexpr int kSteps = D / 32;               // matrix steps of a score
-  static constexpr int kLoadsK = kRowBytes / 64;      // 16-byte loads of a key row by its 4 lanes
-  static constexpr int kWordsV = kRowBytes / 64;      // dwords of a value row by its 16 lanes
+  static constexpr int kLoadsK = kRowBytes / 64;      // 16-byte pieces of a key row for each of its 4 lanes
+  static constexpr int kWordsV = kRowBytes / 64;      // dwords of a value row for each of its 16 lanes
   static constexpr int kJ = D / 16;                   // d tiles
   static constexpr int kOwn = kJ / kAttnWaves;        // d tiles of each row tile a wave ends up with
   static constexpr int kPer = kOwn < 2 ? kOwn : 2;    // of them exchanged in a round
   static constexpr uint32_t kPartBytes = kJ * NR * 1024 + NR * 128;
-};
 
-// Waves a SIMD holds (its 512 registers a lane over the accumulators, Q and one tile), which is
-// also the workgroups a CU holds.
-constexpr int kPairRows = 2;
-constexpr int attn_waves(int D, int NR) { return D > 128 ? (NR == 1 ? 2 : 1) : NR == 1 ? 3 : NR <= kPairRows ? 2 : 1; }
+  static constexpr int kPieces = kRowBytes / 16;      // of a row
+  static constexpr int kLoadRows = 64 / kPieces;      // rows one load of the wave brings
+  static constexpr int kLoads = kTileKeys / kLoadRows;                   // of a tile's keys, or values
+  static constexpr int kScaleLoads = FMT == NM_KV_FP16 ? 0 : 1;          // both scales, with the keys
+  static constexpr int kSideBytes = kTileKeys * kRowBytes;
+  static constexpr int kSlotBytes = 2 * kSideBytes + 256 * kScaleLoads;  // a tile
+  static constexpr int kWaves = attn_waves(D, kRowBytes, NR);
+  static constexpr int kRoom = 160 * 1024 / kWaves / kAttnWaves - 1024;  // LDS of a wave's tiles
+  static constexpr int kDepth = kRoom / kSlotBytes > 4 ? 4 : kRoom / kSlotBytes;
+  static constexpr int kWaveBytes = kDepth * kSlotBytes;
+  static constexpr int kXchBytes = kAttnWaves * kAttnWaves * kPer * 1024;
+  // the tiles, whose LDS the exchange takes after them, then each wave's {m, l} and a flag (all of
+  // it dynamic: a kernel's limit is raised for dynamic LDS alone)
+  static constexpr int kStatAt = kAttnWaves * kWaveBytes > kXchBytes ? kAttnWaves * kWaveBytes : kXchBytes;
+  static constexpr int kLdsBytes = kStatAt + 2 * kAttnWaves * 16 * NR * 4 + 16;
+  static_assert(kDepth >= 1, "a tile fits");
+};
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -112,7 +133,61 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t v) {
   return ((v & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
 }
 
-// One tile of 32 keys in a lane's registers.
+// The 16-byte pieces of a row in LDS are permuted by its number, so that the 8 lanes that read
+// one piece of 8 different rows at a time find them in 8 different bank groups: piece p of row
+// r lies at p ^ swizzle(r). (Rows of one read are 8 (li / 4) + li % 4 (+ 4), hence the bits.)
+template <int ROW_BYTES>
+constexpr __host__ __device__ int swizzle(int r) {
+  return ROW_BYTES == 64 ? ((r >> 1) & 1) | ((r >> 3) & 1) << 1 : (r & 3) | ((r >> 3) & 1) << 2;
+}
+
+// Reads of LDS that direct loads have filled. The compiler would wait for every such load in
+// flight before any read of LDS; the counted waits below are enough, so the reads are written
+// out, each group with its own wait.
+template <int N>
+__device__ __forceinline__ void lds_read16(u32x4 (&d)[N], const uint32_t (&at)[N]) {
+  static_assert(N == 2 || N == 4 || N == 8, "");
+  if constexpr (N == 2)
+    asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0]), "=&v"(d[1]) : "v"(at[0]), "v"(at[1]) : "memory");
+  if constexpr (N == 4)
+    asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3])
+                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]) : "memory");
+  if constexpr (N == 8)
+    asm volatile("ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\tds_read_b128 %3, %11\n\t"
+                 "ds_read_b128 %4, %12\n\tds_read_b128 %5, %13\n\tds_read_b128 %6, %14\n\tds_read_b128 %7, %15\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5]), "=&v"(d[6]), "=&v"(d[7])
+                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7])
+                 : "memory");
+}
+__device__ __forceinline__ void lds_read8(u32x2 (&d)[8], const uint32_t (&at)[8]) {
+  asm volatile("ds_read_b64 %0, %8\n\tds_read_b64 %1, %9\n\tds_read_b64 %2, %10\n\tds_read_b64 %3, %11\n\t"
+               "ds_read_b64 %4, %12\n\tds_read_b64 %5, %13\n\tds_read_b64 %6, %14\n\tds_read_b64 %7, %15\n\t"
+               "s_waitcnt lgkmcnt(0)"
+               : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5]), "=&v"(d[6]), "=&v"(d[7])
+               : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7])
+               : "memory");
+}
+__device__ __forceinline__ void lds_read4(uint32_t (&d)[8], const uint32_t (&at)[8]) {
+  asm volatile("ds_read_b32 %0, %8\n\tds_read_b32 %1, %9\n\tds_read_b32 %2, %10\n\tds_read_b32 %3, %11\n\t"
+               "ds_read_b32 %4, %12\n\tds_read_b32 %5, %13\n\tds_read_b32 %6, %14\n\tds_read_b32 %7, %15\n\t"
+               "s_waitcnt lgkmcnt(0)"
+               : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5]), "=&v"(d[6]), "=&v"(d[7])
+               : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7])
+               : "memory");
+}
+
+// Waits until at most N loads are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "");
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// A lane's share of a tile, as read from LDS.
 template <int FMT, int D>
 struct AttnTile {
   using S = AttnShape<FMT, D, 1>;
@@ -133,69 +208,153 @@ struct AttnWave {
   uint64_t mask[NR];
   f32x4 o[S::kJ][NR];
   float m[NR], l[NR];
+  uint32_t tile0, step, tiles;   // this wave's tiles: tile0 + i * step, i < tiles
+  char* ring;                    // its LDS: kDepth slots of {keys, values, scales}
+  uint32_t ring_at;              // the same as an LDS address
+  uint32_t page;                 // pages of 32 tiles ahead: lane 2 i + h has half h of tile i's
+  uint32_t fetch;                // byte offset of this lane's piece in a load's rows
+  uint32_t read_k, read_v[4];    // LDS offsets of this lane's first pieces in a slot
 
-  // The pages of a tile: of this lane's K rows (8 (li / 4) + ..) and of its V rows (8 g + ..).
-  struct Pages {
-    uint32_t k, v;
-  };
-  __device__ __forceinline__ Pages pages(uint32_t tile) const {
-    const uint32_t last = uint32_t(cache.table_width) - 1, base = tile * kTileKeys;
-    Pages p;
-    p.k = uint32_t(table[min((base + 8u * (li >> 2)) >> cache.page_shift, last)]);
-    p.v = uint32_t(table[min((base + 8u * g) >> cache.page_shift, last)]);
-    return p;
-  }
-
-  __device__ __forceinline__ int64_t row_of(uint32_t block, uint32_t pos) const {
-    block = min(block, cache.blocks - 1u);   // a bad entry reads some page of the cache
-    return ((int64_t(block) * cache.kv_heads + head) << cache.page_shift) +
-           (pos & ((1u << cache.page_shift) - 1u));
-  }
-
-  // 8 fp32 scales of the keys from row on.
-  static __device__ __forceinline__ void load_scales(float (&s)[8], const float* base, int64_t row) {
-    const float4* p = reinterpret_cast<const float4*>(base + row);
+  __device__ __forceinline__ void begin(uint32_t first, uint32_t end, uint32_t every, char* lds) {
+    tile0 = first;
+    step = every;
+    tiles = first < end ? (end - first + every - 1) / every : 0;
+    ring = lds;
+    ring_at = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(lds)));
+    const int r = lane / S::kPieces;
+    fetch = uint32_t(r * S::kRowBytes + ((lane % S::kPieces) ^ swizzle<S::kRowBytes>(r)) * 16);
+    const int rk = 8 * (li >> 2) + (li & 3);
+    read_k = uint32_t(rk * S::kRowBytes + (g ^ swizzle<S::kRowBytes>(rk)) * 16);
+    constexpr int kBytes = 4 * S::kWordsV;   // of a value row a lane takes
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 a = p[h];
-      s[4 * h] = a.x;
-      s[4 * h + 1] = a.y;
-      s[4 * h + 2] = a.z;
-      s[4 * h + 3] = a.w;
+    for (int x = 0; x < 4; ++x) {
+      const int rv = 8 * g + x;
+      read_v[x] = uint32_t(rv * S::kRowBytes + ((li * kBytes / 16) ^ swizzle<S::kRowBytes>(rv)) * 16 + li * kBytes % 16);
     }
   }
 
-  __device__ __forceinline__ void load_keys(AttnTile<FMT, D>& t, uint32_t tile, const Pages& p) const {
-    const uint32_t base = tile * kTileKeys;
-    const char* kr = cache.k + row_of(p.k, base + 8u * (li >> 2) + (li & 3)) * S::kRowBytes + 16 * g;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < S::kLoadsK; ++j)
-        t.k[h][j] = *reinterpret_cast<const u32x4*>(kr + h * 4 * S::kRowBytes + 64 * j);
-    if constexpr (FMT != NM_KV_FP16) load_scales(t.ks, cache.k_scale, row_of(p.v, base + 8u * g));
+  __device__ __forceinline__ void load_pages(uint32_t i) {
+    const uint32_t last = uint32_t(cache.table_width) - 1;
+    const uint32_t key = (tile0 + (i + (uint32_t(lane) >> 1)) * step) * kTileKeys + 16u * (lane & 1);
+    page = uint32_t(table[min(key >> cache.page_shift, last)]);
   }
 
-  __device__ __forceinline__ void load_values(AttnTile<FMT, D>& t, uint32_t tile, const Pages& p) const {
-    const int64_t vrow = row_of(p.v, tile * kTileKeys + 8u * g);
-    if constexpr (FMT != NM_KV_FP16) load_scales(t.vs, cache.v_scale, vrow);
-    const char* vr = cache.v + vrow * S::kRowBytes + 4 * S::kWordsV * li;
+  // The cache row where half h of tile i starts (a tile's halves may be in two pages).
+  __device__ __forceinline__ int64_t half_row(uint32_t i, int h) const {
+    uint32_t block = __builtin_amdgcn_readlane(page, int(2 * (i & 31)) + h);
+    block = min(block, cache.blocks - 1u);   // a bad entry reads some page of the cache
+    const uint32_t key = (tile0 + i * step) * kTileKeys + 16u * h;
+    return ((int64_t(block) * cache.kv_heads + head) << cache.page_shift) + (key & ((1u << cache.page_shift) - 1u));
+  }
+
+  typedef __attribute__((address_space(3))) void lds_void;
+  typedef __attribute__((address_space(1))) const void global_void;
+
+  // Starts the loads of a tile's keys (with both scales) or values into its slot.
+  template <bool KEYS>
+  __device__ __forceinline__ void start(uint32_t i, uint32_t slot) {
+    if (KEYS && (i & 31) == 0 && i > 0) load_pages(i);
+    const int64_t row[2] = {half_row(i, 0), half_row(i, 1)};
+    const char* side = KEYS ? cache.k : cache.v;
+    char* to = ring + slot * S::kSlotBytes + (KEYS ? 0 : S::kSideBytes);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const char* r = vr + e * S::kRowBytes;
-      if constexpr (S::kWordsV == 1) {
-        t.v[e][0] = *reinterpret_cast<const uint32_t*>(r);
-      } else if constexpr (S::kWordsV == 2) {
-        const u32x2 x = *reinterpret_cast<const u32x2*>(r);
-        t.v[e][0] = x[0];
-        t.v[e][1] = x[1];
-      } else {
+    for (int j = 0; j < S::kLoads; ++j) {
+      const int r = j * S::kLoadRows;   // the load's first row
+      const char* from = side + (row[r / 16] + r % 16) * S::kRowBytes + (fetch ^ uint32_t(swizzle<S::kRowBytes>(r) * 16));
+      __builtin_amdgcn_global_load_lds((global_void*)from, (lds_void*)(to + j * 1024), 16, 0, 0);
+    }
+    if constexpr (KEYS && FMT != NM_KV_FP16) {
+      const float* s = lane < 32 ? cache.k_scale : cache.v_scale;
+      const float* from = s + ((lane & 16) ? row[1] : row[0]) + (lane & 15);
+      __builtin_amdgcn_global_load_lds((global_void*)from, (lds_void*)(ring + slot * S::kSlotBytes + 2 * S::kSideBytes), 4, 0, 0);
+    }
+  }
+
+  // Waits for a tile's keys (values): all loads started after them may still be in flight,
+  // those of min(kDepth, left) tiles in all, the last of which may lack its values.
+  template <int N>
+  static __device__ __forceinline__ void wait_keys(uint32_t left) {
+    if constexpr (N > 1) {
+      if (left < N) return wait_keys<N - 1>(left);
+    }
+    wait_loads<N * S::kLoads + (N - 1) * (S::kLoads + S::kScaleLoads)>();
+  }
+  template <int N>
+  static __device__ __forceinline__ void wait_values(uint32_t after) {
+    if constexpr (N > 0) {
+      if (after < N) return wait_values<N - 1>(after);
+    }
+    constexpr int V = N < S::kDepth ? N : N - 1;
+    wait_loads<N * (S::kLoads + S::kScaleLoads) + V * S::kLoads>();
+  }
+
+  __device__ __forceinline__ void read_keys(AttnTile<FMT, D>& t, uint32_t slot) const {
+    const uint32_t base = ring_at + slot * S::kSlotBytes;
+    constexpr int L = S::kLoadsK;
+    if constexpr (L <= 4) {
+      u32x4 d[2 * L];
+      uint32_t at[2 * L];
 #pragma unroll
-        for (int c = 0; c < S::kWordsV / 4; ++c) {
-          const u32x4 x = reinterpret_cast<const u32x4*>(r)[c];
+      for (int x = 0; x < 2 * L; ++x)
+        at[x] = base + (read_k ^ (x % L % 2 * 64)) + x % L / 2 * 128 + x / L * 4 * S::kRowBytes;
+      lds_read16(d, at);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) t.v[e][4 * c + i] = x[i];
-        }
+      for (int x = 0; x < 2 * L; ++x) t.k[x / L][x % L] = d[x];
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        u32x4 d[L];
+        uint32_t at[L];
+#pragma unroll
+        for (int x = 0; x < L; ++x) at[x] = base + (read_k ^ (x % 2 * 64)) + x / 2 * 128 + h * 4 * S::kRowBytes;
+        lds_read16(d, at);
+#pragma unroll
+        for (int x = 0; x < L; ++x) t.k[h][x] = d[x];
+      }
+    }
+    if constexpr (FMT != NM_KV_FP16) {
+      u32x4 d[4];
+      const uint32_t s = base + 2 * S::kSideBytes + 32 * g;
+      const uint32_t at[4] = {s, s + 16, s + 128, s + 144};
+      lds_read16(d, at);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        t.ks[e] = __uint_as_float(d[e >> 2][e & 3]);
+        t.vs[e] = __uint_as_float(d[2 + (e >> 2)][e & 3]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void read_values(AttnTile<FMT, D>& t, uint32_t slot) const {
+    const uint32_t base = ring_at + slot * S::kSlotBytes + S::kSideBytes;
+    uint32_t at[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) at[e] = base + read_v[e & 3] + (e >> 2) * 4 * S::kRowBytes;
+    if constexpr (S::kWordsV == 1) {
+      uint32_t d[8];
+      lds_read4(d, at);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t.v[e][0] = d[e];
+    } else if constexpr (S::kWordsV == 2) {
+      u32x2 d[8];
+      lds_read8(d, at);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        t.v[e][0] = d[e][0];
+        t.v[e][1] = d[e][1];
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < S::kWordsV / 4; ++c) {
+        u32x4 d[8];
+        if (c > 0)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) at[e] ^= 16;   // the other half of a 32-byte run
+        lds_read16(d, at);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t.v[e][4 * c + i] = d[e][i];
       }
     }
   }
@@ -262,10 +421,10 @@ struct AttnWave {
   }
 
   // The softmax's weights of a tile in fp16; the running reference and sum. edge: the tile holds
-  // keys that not every node sees, or that are past the end.
+  // keys that not every node sees, or that are past the end; bad: keys, a bit each, that make the
+  // rows that see them NaN (a scale that is not a number does too).
   __device__ __forceinline__ void weights(AttnTile<FMT, D>& t, float (&x)[NR][8], f16x8 (&w)[NR], bool edge,
-                                          uint32_t key0) {
-    uint32_t bad = 0;   // keys of a draft whose scale is not a number: rows that see them are NaN
+                                          uint32_t bad, uint32_t key0) {
     if constexpr (FMT != NM_KV_FP16) {
       if (edge) {
 #pragma unroll
@@ -325,24 +484,33 @@ struct AttnWave {
     }
   }
 
-  // O^T += V^T P^T.
-  __device__ __forceinline__ void product(AttnTile<FMT, D>& t, const f16x8 (&w)[NR], bool edge, uint32_t key0) {
-    if (edge) {
-      uint32_t bad = 0;   // whether this lane holds a non-finite half of a draft
+  // Values of an edge tile: those past the end, which were never written and may be NaN, become
+  // 0, since 0 times them is not; so does a draft's fp16 row with an infinity or NaN in it, whose
+  // key is returned as a bit: the rows that see it are NaN, the others must not be.
+  __device__ __forceinline__ uint32_t edge_values(AttnTile<FMT, D>& t, uint32_t key0) const {
+    uint32_t bad = 0;
+    if constexpr (FMT == NM_KV_FP16) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t held = key0 + e < keys ? ~0u : 0u, draft = key0 + e < context ? 0u : ~0u;
+        uint32_t any = 0;
 #pragma unroll
-        for (int c = 0; c < S::kWordsV; ++c) {
-          t.v[e][c] &= held;   // past the end: never written, perhaps NaN, and 0 times that is not 0
-          if (FMT == NM_KV_FP16) bad |= non_finite(t.v[e][c]) & draft;
-        }
+        for (int c = 0; c < S::kWordsV; ++c) any |= non_finite(t.v[e][c]);
+        bad |= uint32_t(any != 0 && key0 + e >= context) << e;
       }
-      if (FMT == NM_KV_FP16 && __any(bad != 0)) {
-        poisoned(t, w, key0);
-        return;
-      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) bad |= __shfl_xor(bad, o);   // over the row's lanes
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t held = key0 + e < keys && !((bad >> e) & 1) ? ~0u : 0u;
+#pragma unroll
+      for (int c = 0; c < S::kWordsV; ++c) t.v[e][c] &= held;
+    }
+    return bad;
+  }
+
+  // O^T += V^T P^T.
+  __device__ __forceinline__ void product(const AttnTile<FMT, D>& t, const f16x8 (&w)[NR]) {
 #pragma unroll
     for (int c = 0; c < S::kWordsV; ++c) {
       constexpr int F = 4 / S::kCodeBytes;
@@ -353,43 +521,6 @@ struct AttnWave {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
           o[F * c + x][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[x], w[n], o[F * c + x][n], 0, 0, 0);
-    }
-  }
-
-  // The second product of a tile in which a draft's fp16 v holds infinities or NaN: they are
-  // taken out of it, and a product of "is one" with "is seen" marks the results they reach.
-  __device__ __forceinline__ void poisoned(AttnTile<FMT, D>& t, const f16x8 (&w)[NR], uint32_t key0) {
-    f16x8 on[NR];
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      const uint32_t seen = seen_of(n, key0);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) on[n][e] = _Float16(float((seen >> e) & 1));
-    }
-#pragma unroll
-    for (int c = 0; c < S::kWordsV; ++c) {
-      AttnTile<FMT, D> ind;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t n = key0 + e < context ? 0u : non_finite(t.v[e][c]);
-        const uint32_t halves = (n >> 15) * 0xFFFFu;
-        ind.v[e][c] = halves & 0x3C003C00u;
-        t.v[e][c] &= ~halves;
-      }
-      f16x8 f[4 / S::kCodeBytes], b[4 / S::kCodeBytes];
-      value_frags(t, c, f);
-      value_frags(ind, c, b);
-#pragma unroll
-      for (int x = 0; x < 4 / S::kCodeBytes; ++x)
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-          const int j = (4 / S::kCodeBytes) * c + x;
-          o[j][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[x], w[n], o[j][n], 0, 0, 0);
-          const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[x], on[n], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (hit[i] > 0.f) o[j][n][i] = __builtin_nanf("");
-        }
     }
   }
 };
@@ -476,11 +607,13 @@ __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, in
 }
 
 template <int FMT, int D, int NR>
-__global__ __launch_bounds__(kAttnThreads, attn_waves(D, NR)) void attention_kernel(AttnCall a, AttnSplit sp) {
+__global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void attention_kernel(AttnCall a, AttnSplit sp) {
   using S = AttnShape<FMT, D, NR>;
-  __shared__ f32x4 xch[kAttnWaves][kAttnWaves * S::kPer][64];
-  __shared__ float stat_m[kAttnWaves][16 * NR], stat_l[kAttnWaves][16 * NR];
-  __shared__ uint32_t arrived;
+  extern __shared__ __align__(16) char lds[];
+  f32x4(*xch)[kAttnWaves * S::kPer][64] = reinterpret_cast<f32x4(*)[kAttnWaves * S::kPer][64]>(lds);
+  float(*stat_m)[16 * NR] = reinterpret_cast<float(*)[16 * NR]>(lds + S::kStatAt);
+  float(*stat_l)[16 * NR] = stat_m + kAttnWaves;
+  uint32_t* arrived = reinterpret_cast<uint32_t*>(stat_l + kAttnWaves);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int head = int(blockIdx.x) % a.cache.kv_heads, slot = int(blockIdx.x) / a.cache.kv_heads;
   const int rt = blockIdx.y;
@@ -520,34 +653,45 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, NR)) void attention_ker
     for (int j = 0; j < S::kJ; ++j) w.o[j][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // this chunk's tiles, every fourth a wave's. A tile's registers are loaded again as soon as it
-  // is done with them: the next keys after the scores, the next values after their product
+  // this chunk's tiles, every fourth a wave's; kDepth of them in flight into the wave's own part
+  // of LDS, whose keys and values are fetched again as soon as they are read
   const uint32_t all = (w.keys + kTileKeys - 1) / kTileKeys;
-  const uint32_t begin = uint32_t(slot - first) * per;
-  const uint32_t end = min(all, begin + per);   // per <= 2^31 - 1, begin <= all
-  uint32_t tile = begin + wave;
-  if (tile < end) {
-    using Wave = AttnWave<FMT, D, NR>;
-    AttnTile<FMT, D> t;
-    typename Wave::Pages p = w.pages(tile), next = w.pages(tile + kAttnWaves);
-    w.load_keys(t, tile, p);
-    w.load_values(t, tile, p);
-    while (true) {
-      const uint32_t after = tile + kAttnWaves, key0 = tile * kTileKeys + 8u * w.g;
+  const uint32_t begin = uint32_t(slot - first) * per;   // per <= 2^31 - 1, begin <= all
+  w.begin(begin + wave, min(all, begin + per), kAttnWaves, lds + wave * S::kWaveBytes);
+  if (w.tiles > 0) {
+    w.load_pages(0);
+    for (uint32_t i = 0; i < uint32_t(S::kDepth) && i < w.tiles; ++i) {
+      w.template start<true>(i, i);
+      w.template start<false>(i, i);
+    }
+    uint32_t slot_i = 0;
+    for (uint32_t i = 0; i < w.tiles; ++i) {
+      const uint32_t tile = w.tile0 + i * w.step, key0 = tile * kTileKeys + 8u * w.g, left = w.tiles - i;
       const bool edge = (tile + 1) * kTileKeys > w.context;
-      p = next;
-      next = w.pages(after + kAttnWaves);
+      AttnTile<FMT, D> t;
       float x[NR][8];
       f16x8 y[NR];
+      w.template wait_keys<S::kDepth>(left);
+      w.read_keys(t, slot_i);
+      if (left > uint32_t(S::kDepth)) w.template start<true>(i + S::kDepth, slot_i);
       w.scores(t, x);
-      if (after < end) w.load_keys(t, after, p);
-      w.weights(t, x, y, edge, key0);
-      w.product(t, y, edge, key0);
-      if (after >= end) break;
-      w.load_values(t, after, p);
-      tile = after;
+      uint32_t bad = 0;
+      if (edge) {
+        w.template wait_values<S::kDepth>(left - 1);
+        w.read_values(t, slot_i);
+        bad = w.edge_values(t, key0);
+      }
+      w.weights(t, x, y, edge, bad, key0);
+      if (!edge) {
+        w.template wait_values<S::kDepth>(left - 1);
+        w.read_values(t, slot_i);
+      }
+      if (left > uint32_t(S::kDepth)) w.template start<false>(i + S::kDepth, slot_i);
+      w.product(t, y);
+      slot_i = slot_i + 1 == uint32_t(S::kDepth) ? 0 : slot_i + 1;
     }
   }
+  __syncthreads();   // the waves' tiles are done with: the exchange takes their LDS
 
   // the waves' results together: each scaled to the common reference, then every wave adds up
   // its share of the (row tile, d tile) units over the waves in order
@@ -640,9 +784,9 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(D, NR)) void attention_ker
   __builtin_amdgcn_s_waitcnt(0);   // the partial has reached the coherence point
   __syncthreads();
   uint32_t* counter = sp.counters + (int64_t(b) * a.cache.kv_heads + head) * sp.row_tiles + rt;
-  if (tid == 0) arrived = atomicAdd(counter, 1u);
+  if (tid == 0) *arrived = atomicAdd(counter, 1u);
   __syncthreads();
-  if (arrived != uint32_t(chunks - 1)) return;
+  if (*arrived != uint32_t(chunks - 1)) return;
   if (tid == 0) atomicExch(counter, 0u);
   // The last of the sequence's chunks: all partials are complete. A thread takes units of 16
   // bytes of every `groups`-th chunk, 8 chunks' loads in flight; the groups' sums, and then the
