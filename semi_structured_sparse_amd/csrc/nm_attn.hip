@@ -5,7 +5,7 @@
 #include "nm_attn_impl.h"
 
 #ifndef NM_WIDEST
-#define NM_WIDEST 4
+#define NM_WIDEST (head_dim > 128 ? 2 : head_dim > 64 ? 3 : 4)
 #endif
 namespace nm {
 namespace {
@@ -52,7 +52,7 @@ Plan plan_of(const AttnCall& c, int head_dim, int format, const DeviceInfo& dev)
   Plan p;
   const int rows = c.tokens * c.group;
   // row tiles evenly over the fewest workgroups
-  const int tiles = (rows + 15) / 16, widest = head_dim > 128 ? 2 : NM_WIDEST;
+  const int tiles = (rows + 15) / 16, widest = NM_WIDEST;
   p.row_tiles = (tiles + widest - 1) / widest;
   p.nr = (tiles + p.row_tiles - 1) / p.row_tiles;
   p.part_bytes = uint32_t(head_dim / 16 * p.nr * 1024 + p.nr * 128);

@@ -23,6 +23,8 @@
 // is exact up to its fp32 sums.
 #pragma once
 
+#include <type_traits>
+
 #include "nm_decode_internal.h"
 
 namespace nm {
@@ -49,13 +51,6 @@ struct AttnSplit {
   uint32_t part_bytes;
 };
 
-// Waves of a SIMD, which are also the workgroups of a CU: by the registers of NR row tiles, and
-// by the LDS of one tile in flight a wave.
-constexpr int attn_waves(int D, int row_bytes, int NR) {
-  const int by_rows = D * NR <= 64 ? 4 : D * NR <= 128 ? 3 : D * NR <= 256 && NR <= 2 ? 2 : 1, by_lds = row_bytes <= 128 ? 4 : row_bytes == 256 ? 2 : 1;
-  return by_rows < by_lds ? by_rows : by_lds;
-}
-
 // What a kernel variant holds: registers and LDS set the waves of a SIMD (the workgroups of a
 // CU), the row bytes the loads of a tile, and what is left of the 160 KiB the tiles in flight.
 template <int FMT, int D, int NR>
@@ -74,17 +69,32 @@ struct AttnShape {
   static constexpr int kLoadRows = 64 / kPieces;      // rows one load of the wave brings
   static constexpr int kLoads = kTileKeys / kLoadRows;                   // of a tile's keys, or values
   static constexpr int kScaleLoads = FMT == NM_KV_FP16 ? 0 : 1;          // both scales, with the keys
+  static constexpr int kTileLoads = 2 * kLoads + kScaleLoads;
   static constexpr int kSideBytes = kTileKeys * kRowBytes;
   static constexpr int kSlotBytes = 2 * kSideBytes + 256 * kScaleLoads;  // a tile
-  static constexpr int kWaves = attn_waves(D, kRowBytes, NR);
-  static constexpr int kRoom = 160 * 1024 / kWaves / kAttnWaves - 1024;  // LDS of a wave's tiles
-  static constexpr int kDepth = kRoom / kSlotBytes > 4 ? 4 : kRoom / kSlotBytes;
-  static constexpr int kWaveBytes = kDepth * kSlotBytes;
+
+  // LDS: Q in operand order, {m, l} of each wave and row, a flag, and the waves' tiles (all of it
+  // dynamic: a kernel's limit is raised for dynamic LDS alone). The exchange of results and the
+  // join of partials take the tiles' LDS after them.
+  static constexpr int kQBytes = NR * kSteps * 1024;
+  static constexpr int kFixedBytes = kQBytes + 2 * kAttnWaves * 16 * NR * 4 + 16;
   static constexpr int kXchBytes = kAttnWaves * kAttnWaves * kPer * 1024;
-  // the tiles, whose LDS the exchange takes after them, then each wave's {m, l} and a flag (all of
-  // it dynamic: a kernel's limit is raised for dynamic LDS alone)
-  static constexpr int kStatAt = kAttnWaves * kWaveBytes > kXchBytes ? kAttnWaves * kWaveBytes : kXchBytes;
-  static constexpr int kLdsBytes = kStatAt + 2 * kAttnWaves * 16 * NR * 4 + 16;
+  static constexpr int tiles_of(int waves) { return (160 * 1024 / waves - kFixedBytes) / kAttnWaves / kSlotBytes; }
+  // Waves of a SIMD, which are also the workgroups of a CU: as the accumulators allow (beyond 256
+  // registers the compiler moves them to and fro every tile), if a tile a wave fits in LDS.
+  static constexpr int kByRows = D * NR <= 64 ? 4 : D * NR <= 128 ? 3 : 2;
+  static constexpr int kWaves = tiles_of(kByRows) >= 1 ? kByRows : tiles_of(2) >= 1 && kByRows > 2 ? 2 : 1;
+  static constexpr int kDepth = tiles_of(kWaves) > 4 ? 4 : tiles_of(kWaves);   // tiles in flight
+  static constexpr int kWaveBytes = kDepth * kSlotBytes;
+  static constexpr int kTilesAt = kQBytes;
+  // chunks a sequence may have: 8 for each of the threads that take a row's {m, l} in the join
+  static constexpr int kRowThreads = kAttnThreads / (16 * NR) < 16 ? kAttnThreads / (16 * NR) : 16;
+  static constexpr int kMaxChunks = 8 * kRowThreads;
+  static constexpr int kSumBytes = 16 * NR * D * 4, kFactorBytes = kMaxChunks * 16 * NR * 4;
+  static constexpr int kAfterBytes = kXchBytes > kSumBytes + kFactorBytes ? kXchBytes : kSumBytes + kFactorBytes;
+  static constexpr int kTilesBytes = kAttnWaves * kWaveBytes > kAfterBytes ? kAttnWaves * kWaveBytes : kAfterBytes;
+  static constexpr int kStatAt = kTilesAt + kTilesBytes;
+  static constexpr int kLdsBytes = kStatAt + kFixedBytes - kQBytes;
   static_assert(kDepth >= 1, "a tile fits");
 };
 
@@ -146,10 +156,13 @@ constexpr __host__ __device__ int swizzle(int r) {
 // out, each group with its own wait.
 template <int N>
 __device__ __forceinline__ void lds_read16(u32x4 (&d)[N], const uint32_t (&at)[N]) {
-  static_assert(N == 2 || N == 4 || N == 8, "");
+  static_assert(N == 2 || N == 3 || N == 4 || N == 8, "");
   if constexpr (N == 2)
     asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
                  : "=&v"(d[0]), "=&v"(d[1]) : "v"(at[0]), "v"(at[1]) : "memory");
+  if constexpr (N == 3)
+    asm volatile("ds_read_b128 %0, %3\n\tds_read_b128 %1, %4\n\tds_read_b128 %2, %5\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]) : "v"(at[0]), "v"(at[1]), "v"(at[2]) : "memory");
   if constexpr (N == 4)
     asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\t"
                  "s_waitcnt lgkmcnt(0)"
@@ -204,23 +217,27 @@ struct AttnWave {
   int head, lane, li, g;
   uint32_t keys, context;     // all of the sequence's keys; those every node sees
   float scale;                // of the scores, times log2 e
-  u32x4 q[NR][S::kSteps];
   uint64_t mask[NR];
   f32x4 o[S::kJ][NR];
   float m[NR], l[NR];
   uint32_t tile0, step, tiles;   // this wave's tiles: tile0 + i * step, i < tiles
   char* ring;                    // its LDS: kDepth slots of {keys, values, scales}
-  uint32_t ring_at;              // the same as an LDS address
+  uint32_t ring_at, q_at;        // LDS addresses of the same, and of this lane's piece of Q
   uint32_t page;                 // pages of 32 tiles ahead: lane 2 i + h has half h of tile i's
   uint32_t fetch;                // byte offset of this lane's piece in a load's rows
   uint32_t read_k, read_v[4];    // LDS offsets of this lane's first pieces in a slot
 
-  __device__ __forceinline__ void begin(uint32_t first, uint32_t end, uint32_t every, char* lds) {
+  static __device__ __forceinline__ uint32_t lds_address(const char* p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)(p)));
+  }
+
+  __device__ __forceinline__ void begin(uint32_t first, uint32_t end, uint32_t every, const char* q, char* slots) {
     tile0 = first;
     step = every;
     tiles = first < end ? (end - first + every - 1) / every : 0;
-    ring = lds;
-    ring_at = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(lds)));
+    ring = slots;
+    ring_at = lds_address(slots);
+    q_at = lds_address(q) + 16u * lane;
     const int r = lane / S::kPieces;
     fetch = uint32_t(r * S::kRowBytes + ((lane % S::kPieces) ^ swizzle<S::kRowBytes>(r)) * 16);
     const int rk = 8 * (li >> 2) + (li & 3);
@@ -250,18 +267,33 @@ struct AttnWave {
   typedef __attribute__((address_space(3))) void lds_void;
   typedef __attribute__((address_space(1))) const void global_void;
 
+  // 16 bytes of each lane's own address to 1 KiB of LDS, in lane order.
+  static __device__ __forceinline__ void start_piece(const void* from, void* to) {
+    __builtin_amdgcn_global_load_lds((global_void*)from, (lds_void*)to, 16, 0, 0);
+  }
+
+  // The J-th and later loads of a half's rows, 1024 bytes each.
+  template <int J>
+  __device__ __forceinline__ void start_rows(const char* from, char* to, int h) const {
+    if constexpr (J < S::kLoads / 2) {
+      const uint32_t piece = fetch ^ uint32_t(swizzle<S::kRowBytes>(16 * h + J * S::kLoadRows) * 16);
+      __builtin_amdgcn_global_load_lds((global_void*)(from + J / 4 * 4096 + piece), (lds_void*)(to + J / 4 * 4096), 16,
+                                       J % 4 * 1024, 0);
+      start_rows<J + 1>(from, to, h);
+    }
+  }
+
   // Starts the loads of a tile's keys (with both scales) or values into its slot.
   template <bool KEYS>
   __device__ __forceinline__ void start(uint32_t i, uint32_t slot) {
     if (KEYS && (i & 31) == 0 && i > 0) load_pages(i);
     const int64_t row[2] = {half_row(i, 0), half_row(i, 1)};
-    const char* side = KEYS ? cache.k : cache.v;
     char* to = ring + slot * S::kSlotBytes + (KEYS ? 0 : S::kSideBytes);
 #pragma unroll
-    for (int j = 0; j < S::kLoads; ++j) {
-      const int r = j * S::kLoadRows;   // the load's first row
-      const char* from = side + (row[r / 16] + r % 16) * S::kRowBytes + (fetch ^ uint32_t(swizzle<S::kRowBytes>(r) * 16));
-      __builtin_amdgcn_global_load_lds((global_void*)from, (lds_void*)(to + j * 1024), 16, 0, 0);
+    for (int h = 0; h < 2; ++h) {
+      // a half's rows follow each other in memory as in LDS: one base and an offset of both
+      const char* from = (KEYS ? cache.k : cache.v) + row[h] * S::kRowBytes;
+      start_rows<0>(from, to + h * 16 * S::kRowBytes, h);
     }
     if constexpr (KEYS && FMT != NM_KV_FP16) {
       const float* s = lane < 32 ? cache.k_scale : cache.v_scale;
@@ -277,15 +309,14 @@ struct AttnWave {
     if constexpr (N > 1) {
       if (left < N) return wait_keys<N - 1>(left);
     }
-    wait_loads<N * S::kLoads + (N - 1) * (S::kLoads + S::kScaleLoads)>();
+    wait_loads<N * S::kTileLoads - S::kLoads - S::kScaleLoads>();
   }
   template <int N>
   static __device__ __forceinline__ void wait_values(uint32_t after) {
     if constexpr (N > 0) {
       if (after < N) return wait_values<N - 1>(after);
     }
-    constexpr int V = N < S::kDepth ? N : N - 1;
-    wait_loads<N * (S::kLoads + S::kScaleLoads) + V * S::kLoads>();
+    wait_loads<N * S::kTileLoads - (N == S::kDepth && N > 0 ? S::kLoads : 0)>();
   }
 
   __device__ __forceinline__ void read_keys(AttnTile<FMT, D>& t, uint32_t slot) const {
@@ -385,22 +416,32 @@ struct AttnWave {
     f32x4 s[NR][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    constexpr int G = NR == 1 ? (S::kSteps < 4 ? S::kSteps : 4) : NR == 2 ? 2 : 1;   // steps of Q read at a time
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int s0 = 0; s0 < S::kSteps; s0 += G) {
+      u32x4 q[NR * G];
+      uint32_t at[NR * G];
 #pragma unroll
-      for (int st = 0; st < S::kSteps; ++st) {
-        f16x8 a;
-        if constexpr (FMT == NM_KV_FP16) {
-          a = __builtin_bit_cast(f16x8, t.k[h][st]);
-        } else {
-          const uint32_t c0 = flipped<FMT>(t.k[h][st / 2][2 * (st & 1)]), c1 = flipped<FMT>(t.k[h][st / 2][2 * (st & 1) + 1]);
-          const uint32_t w[4] = {pair_of<FMT>(c0, false), pair_of<FMT>(c0, true), pair_of<FMT>(c1, false), pair_of<FMT>(c1, true)};
-          a = as_half8(w);
+      for (int x = 0; x < NR * G; ++x) at[x] = q_at + ((x % NR) * S::kSteps + s0 + x / NR) * 1024;
+      lds_read16(q, at);
+#pragma unroll
+      for (int u = 0; u < G; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int st = s0 + u;
+          f16x8 a;
+          if constexpr (FMT == NM_KV_FP16) {
+            a = __builtin_bit_cast(f16x8, t.k[h][st]);
+          } else {
+            const uint32_t c0 = flipped<FMT>(t.k[h][st / 2][2 * (st & 1)]), c1 = flipped<FMT>(t.k[h][st / 2][2 * (st & 1) + 1]);
+            const uint32_t w[4] = {pair_of<FMT>(c0, false), pair_of<FMT>(c0, true), pair_of<FMT>(c1, false), pair_of<FMT>(c1, true)};
+            a = as_half8(w);
+          }
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+            s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(f16x8, q[u * NR + n]), s[n][h], 0, 0, 0);
         }
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-          s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(f16x8, q[n][st]), s[n][h], 0, 0, 0);
-      }
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float c = FMT == NM_KV_FP16 ? scale : t.ks[e] * scale;
@@ -544,12 +585,17 @@ __device__ __forceinline__ void attn_lengths(const AttnCall& a, int b, uint32_t&
   keys = uint32_t(min(int64_t(context) + count, most));
 }
 
+// Tiles of a sequence's chunk: `per`, more where that would make more than `most` chunks.
+__device__ __forceinline__ uint32_t chunk_tiles(uint32_t tiles, uint32_t per, uint32_t most) {
+  const uint32_t least = (tiles + most * kAttnWaves - 1) / (most * kAttnWaves) * kAttnWaves;
+  return per > least ? per : least;
+}
 __device__ __forceinline__ uint32_t chunks_of(uint32_t tiles, uint32_t per) {
   return tiles <= per ? 1u : (tiles + per - 1) / per;
 }
 
 // Every wave works this out for itself: 64 sequences a pass, one a lane.
-__device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, int slot) {
+__device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, int slot, uint32_t most) {
   const int lane = threadIdx.x & 63;
   const auto tiles_of = [&](int b) {
     uint32_t context, keys = 0;
@@ -568,7 +614,7 @@ __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, in
     const double half = ceil(total / ((double(slots) - 0.5 * a.batch) * kAttnWaves));
     per = half < 1.0 ? kAttnWaves : uint32_t(half) * kAttnWaves;
     uint32_t used = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 64) used += b0 + lane < a.batch ? chunks_of(tiles_of(b0 + lane), per) : 0u;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) used += b0 + lane < a.batch ? chunks_of(tiles_of(b0 + lane), per) : 0u;   // the cap makes them fewer
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) used += __shfl_xor(used, o);
     if (used > uint32_t(slots)) per = uint32_t(ceil(total / (double(slots - a.batch) * kAttnWaves))) * kAttnWaves;
@@ -578,10 +624,13 @@ __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, in
   int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
     uint32_t context = 0, keys = 0;
+    uint32_t mine = per;
     int count = 0, n = 0;
     if (b0 + lane < a.batch) {
       attn_lengths(a, b0 + lane, context, keys, count);
-      n = int(chunks_of((keys + kTileKeys - 1) / kTileKeys, per));
+      const uint32_t tiles = (keys + kTileKeys - 1) / kTileKeys;
+      if (slots > a.batch) mine = chunk_tiles(tiles, per, most);
+      n = int(chunks_of(tiles, mine));
     }
     int upto = n;
 #pragma unroll
@@ -595,7 +644,7 @@ __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, in
       k.b = b0 + at;
       k.chunks = __shfl(n, at);
       k.first = before + __shfl(upto, at) - k.chunks;
-      k.tiles = per;
+      k.tiles = __shfl(mine, at);
       k.context = __shfl(context, at);
       k.keys = __shfl(keys, at);
       k.count = __shfl(count, at);
@@ -610,14 +659,14 @@ template <int FMT, int D, int NR>
 __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void attention_kernel(AttnCall a, AttnSplit sp) {
   using S = AttnShape<FMT, D, NR>;
   extern __shared__ __align__(16) char lds[];
-  f32x4(*xch)[kAttnWaves * S::kPer][64] = reinterpret_cast<f32x4(*)[kAttnWaves * S::kPer][64]>(lds);
+  f32x4(*xch)[kAttnWaves * S::kPer][64] = reinterpret_cast<f32x4(*)[kAttnWaves * S::kPer][64]>(lds + S::kTilesAt);
   float(*stat_m)[16 * NR] = reinterpret_cast<float(*)[16 * NR]>(lds + S::kStatAt);
   float(*stat_l)[16 * NR] = stat_m + kAttnWaves;
   uint32_t* arrived = reinterpret_cast<uint32_t*>(stat_l + kAttnWaves);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int head = int(blockIdx.x) % a.cache.kv_heads, slot = int(blockIdx.x) / a.cache.kv_heads;
   const int rt = blockIdx.y;
-  AttnChunk ck = find_chunk(a, sp.slots, slot);
+  AttnChunk ck = find_chunk(a, sp.slots, slot, S::kMaxChunks);
   const int b = __builtin_amdgcn_readfirstlane(ck.b);
   if (b < 0) return;
   const int chunks = __builtin_amdgcn_readfirstlane(ck.chunks), first = __builtin_amdgcn_readfirstlane(ck.first);
@@ -638,15 +687,9 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
   for (int n = 0; n < NR; ++n) {
     const int r = (rt * NR + n) * 16 + w.li, t = r / a.group;
     const bool live = r < rows && t < count;
-    const uint16_t* qr = a.q + (int64_t(b) * a.tokens + t) * a.q_stride + int64_t(head * a.group + r % a.group) * D;
     uint64_t mk = 0;
     if (live) mk = a.mask != nullptr ? a.mask[int64_t(b) * a.tokens + t] : t >= 63 ? ~0ull : (2ull << t) - 1;
     w.mask[n] = count >= 64 ? mk : mk & ((1ull << count) - 1);
-#pragma unroll
-    for (int st = 0; st < S::kSteps; ++st) {
-      const int d = FMT == NM_KV_FP16 ? 32 * st + 8 * w.g : 64 * (st >> 1) + 16 * w.g + 8 * (st & 1);
-      w.q[n][st] = live ? *reinterpret_cast<const u32x4*>(qr + d) : u32x4{0, 0, 0, 0};
-    }
     w.m[n] = kLowest;
     w.l[n] = 0.f;
 #pragma unroll
@@ -657,13 +700,31 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
   // of LDS, whose keys and values are fetched again as soon as they are read
   const uint32_t all = (w.keys + kTileKeys - 1) / kTileKeys;
   const uint32_t begin = uint32_t(slot - first) * per;   // per <= 2^31 - 1, begin <= all
-  w.begin(begin + wave, min(all, begin + per), kAttnWaves, lds + wave * S::kWaveBytes);
+  w.begin(begin + wave, min(all, begin + per), kAttnWaves, lds, lds + S::kTilesAt + wave * S::kWaveBytes);
+  // Q, in operand order: every wave loads its share of the (row tile, step) fragments. Rows past
+  // the last node's repeat row 0: nothing of theirs is stored.
+#pragma unroll
+  for (int f = 0; f < (NR * S::kSteps + kAttnWaves - 1) / kAttnWaves; ++f) {
+    const int x = f * kAttnWaves + wave, fn = x / S::kSteps, st = x % S::kSteps;
+    if (x >= NR * S::kSteps) break;
+    int r = (rt * NR + fn) * 16 + w.li;
+    r = r < rows ? r : 0;
+    const int d = FMT == NM_KV_FP16 ? 32 * st + 8 * w.g : 64 * (st >> 1) + 16 * w.g + 8 * (st & 1);
+    const uint16_t* from = a.q + (int64_t(b) * a.tokens + r / a.group) * a.q_stride +
+                           int64_t(head * a.group + r % a.group) * D + d;
+    w.start_piece(from, lds + x * 1024);
+  }
+  if (w.tiles > 0) w.load_pages(0);
+  for (uint32_t i = 0; i < uint32_t(S::kDepth) && i < w.tiles; ++i) {
+    w.template start<true>(i, i);
+    w.template start<false>(i, i);
+  }
+  if (w.tiles >= uint32_t(S::kDepth))
+    wait_loads<S::kDepth * S::kTileLoads>();
+  else
+    wait_loads<0>();
+  __builtin_amdgcn_s_barrier();   // all of Q has arrived
   if (w.tiles > 0) {
-    w.load_pages(0);
-    for (uint32_t i = 0; i < uint32_t(S::kDepth) && i < w.tiles; ++i) {
-      w.template start<true>(i, i);
-      w.template start<false>(i, i);
-    }
     uint32_t slot_i = 0;
     for (uint32_t i = 0; i < w.tiles; ++i) {
       const uint32_t tile = w.tile0 + i * w.step, key0 = tile * kTileKeys + 8u * w.g, left = w.tiles - i;
@@ -788,70 +849,90 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
   __syncthreads();
   if (*arrived != uint32_t(chunks - 1)) return;
   if (tid == 0) atomicExch(counter, 0u);
-  // The last of the sequence's chunks: all partials are complete. A thread takes units of 16
-  // bytes of every `groups`-th chunk, 8 chunks' loads in flight; the groups' sums, and then the
-  // rows, come together in LDS. The order is fixed, so the result is the same each time.
-  float* sum = reinterpret_cast<float*>(xch);                 // [row][d]
-  const int groups = units < kAttnThreads ? kAttnThreads / units : 1;
-  const int grp = groups > 1 ? tid / units : 0;
-  constexpr int U = 8;
-  // the rows' references and sums: up to 16 threads a row, then one
-  const int threads = min(16, kAttnThreads / live);
+  // The last of the sequence's chunks: all partials are complete. First the rows' common
+  // references and sums, and what each chunk's partial is worth against them.
+  float* sum = reinterpret_cast<float*>(lds + S::kTilesAt);                        // [group][row][d]
+  float* factor = reinterpret_cast<float*>(lds + S::kTilesAt + S::kSumBytes);      // [chunk][row]
   const int r0 = tid % live, s0 = tid / live;
-  float2* stat = reinterpret_cast<float2*>(xch);
-  if (s0 < threads) {
+  if (s0 < S::kRowThreads) {
     float m1 = kLowest, l1 = 0.f;
-    for (int c0 = s0; c0 < chunks; c0 += threads * U) {
-      u32x2 x[U];
+    u32x2 x[8];
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        x[k] = __builtin_amdgcn_raw_buffer_load_b64(buf, min(c0 + k * threads, chunks - 1) * stride + r0 * 8, 0, kCoherent);
+    for (int k = 0; k < 8; ++k)
+      if (s0 + k * S::kRowThreads < chunks)
+        x[k] = __builtin_amdgcn_raw_buffer_load_b64(buf, (s0 + k * S::kRowThreads) * stride + r0 * 8, 0, kCoherent);
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        if (c0 + k * threads >= chunks) continue;
-        const float m2 = __uint_as_float(x[k][0]), next = fmaxf(m1, m2);
-        l1 = l1 * exp2_fast(m1 - next) + __uint_as_float(x[k][1]) * exp2_fast(m2 - next);
-        m1 = next;
+    for (int k = 0; k < 8; ++k)
+      if (s0 + k * S::kRowThreads < chunks) m1 = fmaxf(m1, __uint_as_float(x[k][0]));
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s0 + k * S::kRowThreads < chunks) {
+        const float f = exp2_fast(__uint_as_float(x[k][0]) - m1);
+        l1 += __uint_as_float(x[k][1]) * f;
+        factor[(s0 + k * S::kRowThreads) * live + r0] = f;
       }
-    }
-    stat[s0 * live + r0] = make_float2(m1, l1);
+    reinterpret_cast<float2*>(sum)[s0 * live + r0] = make_float2(m1, l1);
   }
   __syncthreads();
-  if (tid < live) {
+  float f0 = 0.f;   // of this thread's chunks, from its own reference to the row's
+  if (s0 < S::kRowThreads) {
+    const float2* part = reinterpret_cast<const float2*>(sum);
     float m1 = kLowest, l1 = 0.f;
-    for (int x = 0; x < threads; ++x) m1 = fmaxf(m1, stat[x * live + tid].x);
-    for (int x = 0; x < threads; ++x) l1 += stat[x * live + tid].y * exp2_fast(stat[x * live + tid].x - m1);
-    stat_m[0][tid] = m1;
-    stat_l[0][tid] = l1;
+#pragma unroll
+    for (int x = 0; x < S::kRowThreads; ++x) m1 = fmaxf(m1, part[x * live + r0].x);
+#pragma unroll
+    for (int x = 0; x < S::kRowThreads; ++x) l1 += part[x * live + r0].y * exp2_fast(part[x * live + r0].x - m1);
+    f0 = exp2_fast(part[s0 * live + r0].x - m1);
+    if (s0 == 0) stat_l[0][r0] = l1;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s0 + k * S::kRowThreads < chunks) factor[(s0 + k * S::kRowThreads) * live + r0] *= f0;
   }
   __syncthreads();
-  for (int u0 = groups > 1 ? tid - grp * units : tid; u0 < units; u0 += kAttnThreads) {
-    if (grp >= groups) break;
-    const int r = u0 % live, jg = u0 / live, j = jg >> 2, g = jg & 3;
-    const float top = stat_m[0][r];
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int c0 = grp; c0 < chunks; c0 += groups * U) {
-      u32x4 y[U];
-      uint32_t mc[U];
+  // Then the partials, 16 bytes a unit: a thread takes units of every `groups`-th chunk, as many
+  // loads in flight as it has registers for; the groups' sums and the rows come together in LDS.
+  // The order is fixed, so the result is the same each time.
+  const int groups = units < kAttnThreads ? kAttnThreads / units : 1, grp = groups > 1 ? tid / units : 0;
+  const auto join = [&](auto units_at_once, auto chunks_at_once) {
+    constexpr int UU = decltype(units_at_once)::value, CC = decltype(chunks_at_once)::value;
+    for (int u0 = groups > 1 ? tid - grp * units : tid; u0 < units && grp < groups; u0 += kAttnThreads * UU) {
+      f32x4 acc[UU];
 #pragma unroll
-      for (int x = 0; x < U; ++x) {
-        const uint32_t at = min(c0 + x * groups, chunks - 1) * stride;
-        mc[x] = __builtin_amdgcn_raw_buffer_load_b32(buf, at + r * 8, 0, kCoherent);
-        y[x] = __builtin_amdgcn_raw_buffer_load_b128(buf, at + kStats + u0 * 16, 0, kCoherent);
+      for (int v = 0; v < UU; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int c0 = grp; c0 < chunks; c0 += groups * CC) {
+        u32x4 y[UU][CC];
+#pragma unroll
+        for (int x = 0; x < CC; ++x)
+          if (c0 + x * groups < chunks)
+#pragma unroll
+            for (int v = 0; v < UU; ++v)   // units past the last: within the sequence's partials, not used
+              y[v][x] = __builtin_amdgcn_raw_buffer_load_b128(
+                  buf, (c0 + x * groups) * stride + kStats + (u0 + v * kAttnThreads) * 16, 0, kCoherent);
+#pragma unroll
+        for (int x = 0; x < CC; ++x)
+          if (c0 + x * groups < chunks)
+#pragma unroll
+            for (int v = 0; v < UU; ++v)
+              acc[v] += __builtin_bit_cast(f32x4, y[v][x]) * factor[(c0 + x * groups) * live + (u0 + v * kAttnThreads) % live];
       }
 #pragma unroll
-      for (int x = 0; x < U; ++x) {
-        if (c0 + x * groups >= chunks) continue;
-        acc += __builtin_bit_cast(f32x4, y[x]) * exp2_fast(__uint_as_float(mc[x]) - top);
+      for (int v = 0; v < UU; ++v) {
+        const int u = u0 + v * kAttnThreads;
+        if (u >= units) break;
+        const int r = u % live, jg = u / live;
+        float* at = sum + (grp * live + r) * D + S::kJ * 4 * (jg & 3) + (jg >> 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[S::kJ * i] = acc[v][i];
       }
     }
-    float* at = sum + (grp * live + r) * D + S::kJ * 4 * g + j;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) at[S::kJ * i] = acc[i];
-  }
+  };
+  if (units <= kAttnThreads)
+    join(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
+  else
+    join(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
   __syncthreads();
   for (int u = tid; u < live * (D / 8); u += kAttnThreads) {
-    const int r = u / (D / 8), d = u % (D / 8) * 8, node = (rt * NR * 16 + r) / a.group;
+    const int r = u / (D / 8), d = u % (D / 8) * 8, at = rt * NR * 16 + r, node = at / a.group;
     const float l1 = stat_l[0][r], inv = node < count && l1 != 0.f ? 1.0f / l1 : 0.f;
     float y[8];
 #pragma unroll
@@ -860,8 +941,8 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
       for (int x = 0; x < groups; ++x) y[e] += sum[(x * live + r) * D + d + e];
       y[e] = inv == 0.f ? 0.f : y[e] * inv;
     }
-    *reinterpret_cast<u32x4*>(a.out + ((int64_t(b) * a.tokens + node) * a.heads + head * a.group +
-                                       (rt * NR * 16 + r) % a.group) * D + d) = halves_of(y);
+    *reinterpret_cast<u32x4*>(a.out + ((int64_t(b) * a.tokens + node) * a.heads + head * a.group + at % a.group) * D + d) =
+        halves_of(y);
   }
 }
 
