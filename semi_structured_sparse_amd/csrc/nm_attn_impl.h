@@ -35,7 +35,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kTileKeys = 32;
-constexpr int kMinChunkTiles = kAttnWaves;   // one tile a wave
+constexpr int kMinChunkTiles = 2 * kAttnWaves;   // two tiles a wave: a chunk more costs the join as much
 constexpr float kLowest = -3e38f;            // the reference of a row that has seen nothing
 // A value's scale counts as at least this (rows of zeros have scale 0, and codes 0): far below
 // what fp16 results can show, and its reciprocal times any number of keys is finite.
@@ -71,7 +71,7 @@ struct AttnShape {
   static constexpr int kScaleLoads = FMT == NM_KV_FP16 ? 0 : 1;          // both scales, with the keys
   static constexpr int kTileLoads = 2 * kLoads + kScaleLoads;
   static constexpr int kSideBytes = kTileKeys * kRowBytes;
-  static constexpr int kSlotBytes = 2 * kSideBytes + 256 * kScaleLoads;  // a tile
+  static constexpr int kSlotBytes = 2 * kSideBytes + 384 * kScaleLoads;  // a tile
 
   // LDS: Q in operand order, {m, l} of each wave and row, a flag, and the waves' tiles (all of it
   // dynamic: a kernel's limit is raised for dynamic LDS alone). The exchange of results and the
@@ -82,8 +82,8 @@ struct AttnShape {
   static constexpr int tiles_of(int waves) { return (160 * 1024 / waves - kFixedBytes) / kAttnWaves / kSlotBytes; }
   // Waves of a SIMD, which are also the workgroups of a CU: as the accumulators allow (beyond 256
   // registers the compiler moves them to and fro every tile), if a tile a wave fits in LDS.
-  static constexpr int kByRows = D * NR <= 64 ? 4 : D * NR <= 128 ? 3 : 2;
-  static constexpr int kWaves = tiles_of(kByRows) >= 1 ? kByRows : tiles_of(2) >= 1 && kByRows > 2 ? 2 : 1;
+  static constexpr int kByRows = D * NR <= 128 ? 3 : 2;
+  static constexpr int kWaves = tiles_of(kByRows) >= 1 ? kByRows : tiles_of(2) >= 1 ? 2 : 1;
   static constexpr int kDepth = tiles_of(kWaves) > 4 ? 4 : tiles_of(kWaves);   // tiles in flight
   static constexpr int kWaveBytes = kDepth * kSlotBytes;
   static constexpr int kTilesAt = kQBytes;
@@ -114,18 +114,19 @@ __device__ __forceinline__ float sum4(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// Two fp16 from bytes 0, 1 (hi: 2, 3) of a word of codes. int8 codes come with their sign bit
-// flipped: 0x6400 + u is 1024 + u in fp16, and 1152 taken off is exact.
+// Two fp16 of a word of codes: bytes 0, 1 (hi: 2, 3) of e4m3. int8 codes come with their sign
+// bit flipped, u = code + 128, and zero-extended to 16 bits they are the subnormals u 2^-24,
+// exact in the matrix instruction; the sums are corrected by 128 times the other side's sum.
+constexpr float kCodeUnit = 0x1p24f;    // int8: the products come out in 2^-24
+constexpr float kCodeBias = 128.0f;
+
 template <int FMT>
 __device__ __forceinline__ uint32_t pair_of(uint32_t codes, bool hi) {
-  if constexpr (FMT == NM_KV_E4M3) {
+  if constexpr (FMT == NM_KV_E4M3)
     return hi ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(codes), 1.0f, true))
               : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(codes), 1.0f, false));
-  } else {
-    const uint32_t u = __builtin_amdgcn_perm(codes, 0x64646464u, hi ? 0x00070006u : 0x00050004u);
-    const f16x2 c = {_Float16(1152.0f), _Float16(1152.0f)};
-    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, u) - c);
-  }
+  else
+    return __builtin_amdgcn_perm(codes, codes, hi ? 0x0C030C02u : 0x0C010C00u);   // 0x0C: a zero byte
 }
 
 template <int FMT>
@@ -206,7 +207,9 @@ struct AttnTile {
   using S = AttnShape<FMT, D, 1>;
   u32x4 k[2][S::kLoadsK];
   uint32_t v[8][S::kWordsV];
-  float ks[8], vs[8];   // scales of keys 8 g + 0..7 (8-bit formats)
+  // of keys 8 g + 0..7 in the 8-bit formats: the key's scale times the softmax's, log2 of the
+  // value's scale and its reciprocal
+  float kc[8], lz[8], iz[8];
 };
 
 template <int FMT, int D, int NR>
@@ -220,6 +223,7 @@ struct AttnWave {
   uint64_t mask[NR];
   f32x4 o[S::kJ][NR];
   float m[NR], l[NR];
+  float qs[NR], ws[NR];   // int8: -128 sum(q), and the sum of the weights, for the codes' bias
   uint32_t tile0, step, tiles;   // this wave's tiles: tile0 + i * step, i < tiles
   char* ring;                    // its LDS: kDepth slots of {keys, values, scales}
   uint32_t ring_at, q_at;        // LDS addresses of the same, and of this lane's piece of Q
@@ -343,17 +347,40 @@ struct AttnWave {
         for (int x = 0; x < L; ++x) t.k[h][x] = d[x];
       }
     }
-    if constexpr (FMT != NM_KV_FP16) {
-      u32x4 d[4];
-      const uint32_t s = base + 2 * S::kSideBytes + 32 * g;
-      const uint32_t at[4] = {s, s + 16, s + 128, s + 144};
-      lds_read16(d, at);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        t.ks[e] = __uint_as_float(d[e >> 2][e & 3]);
-        t.vs[e] = __uint_as_float(d[2 + (e >> 2)][e & 3]);
-      }
+  }
+
+  // What the scores need of a tile's scales, worked out once a key (by the lane of its number)
+  // and handed round through LDS, in place of the scales. Returns the keys, a bit each of this
+  // lane's 8, whose value's scale is not a number (edge tiles; elsewhere it makes NaN by itself).
+  __device__ __forceinline__ uint32_t read_scales(AttnTile<FMT, D>& t, uint32_t slot, bool edge) const {
+    if constexpr (FMT == NM_KV_FP16) return 0;
+    const uint32_t base = ring_at + slot * S::kSlotBytes + 2 * S::kSideBytes, mine = base + 4 * (lane & 31);
+    float ks, vs;
+    asm volatile("ds_read_b32 %0, %2\n\tds_read_b32 %1, %2 offset:128\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(ks), "=&v"(vs) : "v"(mine) : "memory");
+    uint32_t bad = 0;
+    if (edge) {
+      const bool b = !(vs < __builtin_inff());
+      bad = uint32_t(__ballot(b)) >> (8 * g) & 0xFFu;
+      if (b) vs = 1.0f;
     }
+    vs = vs < kLeastScale ? kLeastScale : vs;   // NaN stays
+    const float kc = ks * scale, lz = __builtin_amdgcn_logf(vs), iz = __builtin_amdgcn_rcpf(vs);
+    const uint32_t from = base + 32 * g;
+    u32x4 d[6];
+    asm volatile("ds_write_b32 %6, %7\n\tds_write_b32 %6, %8 offset:128\n\tds_write_b32 %6, %9 offset:256\n\t"
+                 "ds_read_b128 %0, %10\n\tds_read_b128 %1, %10 offset:16\n\t"
+                 "ds_read_b128 %2, %10 offset:128\n\tds_read_b128 %3, %10 offset:144\n\t"
+                 "ds_read_b128 %4, %10 offset:256\n\tds_read_b128 %5, %10 offset:272\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5])
+                 : "v"(mine), "v"(kc), "v"(lz), "v"(iz), "v"(from) : "memory");
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      t.kc[e] = __uint_as_float(d[e >> 2][e & 3]);
+      t.lz[e] = __uint_as_float(d[2 + (e >> 2)][e & 3]);
+      t.iz[e] = __uint_as_float(d[4 + (e >> 2)][e & 3]);
+    }
+    return bad;
   }
 
   __device__ __forceinline__ void read_values(AttnTile<FMT, D>& t, uint32_t slot) const {
@@ -400,18 +427,25 @@ struct AttnWave {
         w[1][p] = __builtin_amdgcn_perm(t.v[2 * p + 1][c], t.v[2 * p][c], 0x07060302u);
       } else {
         const uint32_t a = flipped<FMT>(t.v[2 * p][c]), b = flipped<FMT>(t.v[2 * p + 1][c]);
-        const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x05010400u), hi = __builtin_amdgcn_perm(b, a, 0x07030602u);
-        w[0][p] = pair_of<FMT>(lo, false);
-        w[1][p] = pair_of<FMT>(lo, true);
-        w[2][p] = pair_of<FMT>(hi, false);
-        w[3][p] = pair_of<FMT>(hi, true);
+        if constexpr (FMT == NM_KV_INT8) {
+          w[0][p] = __builtin_amdgcn_perm(b, a, 0x0C040C00u);
+          w[1][p] = __builtin_amdgcn_perm(b, a, 0x0C050C01u);
+          w[2][p] = __builtin_amdgcn_perm(b, a, 0x0C060C02u);
+          w[3][p] = __builtin_amdgcn_perm(b, a, 0x0C070C03u);
+        } else {
+          const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x05010400u), hi = __builtin_amdgcn_perm(b, a, 0x07030602u);
+          w[0][p] = pair_of<FMT>(lo, false);
+          w[1][p] = pair_of<FMT>(lo, true);
+          w[2][p] = pair_of<FMT>(hi, false);
+          w[3][p] = pair_of<FMT>(hi, true);
+        }
       }
     }
 #pragma unroll
     for (int x = 0; x < 4 / S::kCodeBytes; ++x) f[x] = as_half8(w[x]);
   }
 
-  // The scores of a tile in units of log2, without log2 z: x[n][e] is this lane's row n, key 8 g + e.
+  // The scores of a tile in units of log2, with log2 z: x[n][e] is this lane's row n, key 8 g + e.
   __device__ __forceinline__ void scores(const AttnTile<FMT, D>& t, float (&x)[NR][8]) const {
     f32x4 s[NR][2];
 #pragma unroll
@@ -443,10 +477,34 @@ struct AttnWave {
         }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float c = FMT == NM_KV_FP16 ? scale : t.ks[e] * scale;
+    for (int e = 0; e < 8; ++e)
 #pragma unroll
-      for (int n = 0; n < NR; ++n) x[n][e] = s[n][e >> 2][e & 3] * c;
+      for (int n = 0; n < NR; ++n) {
+        const float y = FMT == NM_KV_INT8 ? s[n][e >> 2][e & 3] + qs[n] : s[n][e >> 2][e & 3];
+        x[n][e] = FMT == NM_KV_FP16 ? y * scale : fmaf(y, t.kc[e], t.lz[e]);
+      }
+  }
+
+  // -128 times each row's sum of q, in the products' unit (a product with ones gives every lane
+  // its row's sum).
+  __device__ __forceinline__ void sum_queries() {
+    if constexpr (FMT != NM_KV_INT8) return;
+    f16x8 ones;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ones[e] = _Float16(1.0f);
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int st = 0; st < S::kSteps; st += 2) {
+        u32x4 q[2];
+        const uint32_t at[2] = {q_at + (n * S::kSteps + st) * 1024, q_at + (n * S::kSteps + st + 1) * 1024};
+        lds_read16(q, at);
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, __builtin_bit_cast(f16x8, q[0]), sum, 0, 0, 0);
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, __builtin_bit_cast(f16x8, q[1]), sum, 0, 0, 0);
+      }
+      qs[n] = sum[0] * (-kCodeBias / kCodeUnit);
+      ws[n] = 0.f;
     }
   }
 
@@ -464,25 +522,8 @@ struct AttnWave {
   // The softmax's weights of a tile in fp16; the running reference and sum. edge: the tile holds
   // keys that not every node sees, or that are past the end; bad: keys, a bit each, that make the
   // rows that see them NaN (a scale that is not a number does too).
-  __device__ __forceinline__ void weights(AttnTile<FMT, D>& t, float (&x)[NR][8], f16x8 (&w)[NR], bool edge,
+  __device__ __forceinline__ void weights(const AttnTile<FMT, D>& t, float (&x)[NR][8], f16x8 (&w)[NR], bool edge,
                                           uint32_t bad, uint32_t key0) {
-    if constexpr (FMT != NM_KV_FP16) {
-      if (edge) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool b = !(t.vs[e] < __builtin_inff());
-          bad |= uint32_t(b) << e;
-          if (b) t.vs[e] = 1.0f;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        t.vs[e] = t.vs[e] < kLeastScale ? kLeastScale : t.vs[e];   // NaN stays
-        const float lz = __builtin_amdgcn_logf(t.vs[e]);
-#pragma unroll
-        for (int n = 0; n < NR; ++n) x[n][e] += lz;
-      }
-    }
     if (edge) {
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
@@ -509,18 +550,23 @@ struct AttnWave {
         const float f = exp2_fast(m[n] - next);
         m[n] = next;
         l[n] *= f;
+        if (FMT == NM_KV_INT8) ws[n] *= f;
 #pragma unroll
         for (int j = 0; j < S::kJ; ++j) o[j][n] *= f;
       }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float iz = FMT == NM_KV_FP16 ? 1.0f : __builtin_amdgcn_rcpf(t.vs[e]);
+    for (int n = 0; n < NR; ++n) {
 #pragma unroll
-      for (int n = 0; n < NR; ++n) {
+      for (int e = 0; e < 8; ++e) {
         const float y = exp2_fast(x[n][e] - m[n]);
-        l[n] = FMT == NM_KV_FP16 ? l[n] + y : fmaf(y, iz, l[n]);
+        l[n] = FMT == NM_KV_FP16 ? l[n] + y : fmaf(y, t.iz[e], l[n]);
         w[n][e] = _Float16(y);   // to nearest even: 2^-11 of the weight
+      }
+      if constexpr (FMT == NM_KV_INT8) {
+        const f16x2 ones = {_Float16(1.0f), _Float16(1.0f)};
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) ws[n] = __builtin_amdgcn_fdot2(f16x2{w[n][e], w[n][e + 1]}, ones, ws[n], false);
       }
     }
   }
@@ -594,6 +640,17 @@ __device__ __forceinline__ uint32_t chunks_of(uint32_t tiles, uint32_t per) {
   return tiles <= per ? 1u : (tiles + per - 1) / per;
 }
 
+// Inclusive sums over the wave.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);   // the row before's last, rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);   // the first half's last, rows 2 and 3
+  return x;
+}
+
 // Every wave works this out for itself: 64 sequences a pass, one a lane.
 __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, int slot, uint32_t most) {
   const int lane = threadIdx.x & 63;
@@ -601,56 +658,52 @@ __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, in
     uint32_t context, keys = 0;
     int count;
     if (b < a.batch) attn_lengths(a, b, context, keys, count);
-    return (keys + kTileKeys - 1) / kTileKeys;
+    return (keys + kTileKeys - 1) / kTileKeys;   // at most 2^25
   };
   uint32_t per = 0x7FFFFFFFu;
   if (slots > a.batch) {
-    double total = 0.0;
-    for (int b0 = 0; b0 < a.batch; b0 += 64) total += double(tiles_of(b0 + lane));
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) total += __shfl_xor(total, o);
+    uint64_t total = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64)
+      total += uint32_t(__builtin_amdgcn_readlane(wave_scan(tiles_of(b0 + lane)), 63));
     // The last chunk of a sequence is half empty on average: that many slots are set aside, and
     // one a sequence, which always fits, if they do not do. Whole rounds of the waves.
-    const double half = ceil(total / ((double(slots) - 0.5 * a.batch) * kAttnWaves));
-    per = half < 1.0 ? kAttnWaves : uint32_t(half) * kAttnWaves;
+    const double half = ceil(double(total) / ((double(slots) - 0.5 * a.batch) * kAttnWaves));
+    per = uint32_t(fmax(half * kAttnWaves, double(kMinChunkTiles)));
     uint32_t used = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 64) used += b0 + lane < a.batch ? chunks_of(tiles_of(b0 + lane), per) : 0u;   // the cap makes them fewer
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) used += __shfl_xor(used, o);
-    if (used > uint32_t(slots)) per = uint32_t(ceil(total / (double(slots - a.batch) * kAttnWaves))) * kAttnWaves;
+    for (int b0 = 0; b0 < a.batch; b0 += 64)
+      used += uint32_t(__builtin_amdgcn_readlane(
+          wave_scan(b0 + lane < a.batch ? chunks_of(tiles_of(b0 + lane), per) : 0u), 63));
+    if (used > uint32_t(slots)) per = uint32_t(ceil(double(total) / (double(slots - a.batch) * kAttnWaves))) * kAttnWaves;
   }
   AttnChunk k;
   k.b = -1;
   int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    uint32_t context = 0, keys = 0;
-    uint32_t mine = per;
+    uint32_t context = 0, keys = 0, mine = per;
     int count = 0, n = 0;
     if (b0 + lane < a.batch) {
       attn_lengths(a, b0 + lane, context, keys, count);
       const uint32_t tiles = (keys + kTileKeys - 1) / kTileKeys;
-      if (slots > a.batch) mine = chunk_tiles(tiles, per, most);
+      if (slots > a.batch) {   // as many chunks as `per` asks for, of even size
+        n = int(chunks_of(tiles, chunk_tiles(tiles, per, most)));
+        mine = max((tiles + n * kAttnWaves - 1) / (n * kAttnWaves), 1u) * kAttnWaves;
+      }
       n = int(chunks_of(tiles, mine));
     }
-    int upto = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int x = __shfl_up(upto, o);
-      if (lane >= o) upto += x;
-    }
-    const uint64_t past = __ballot(before + upto > slot);
+    const uint32_t upto = wave_scan(uint32_t(n));
+    const uint64_t past = __ballot(before + int(upto) > slot);
     if (past != 0) {
       const int at = __builtin_ctzll(past);
       k.b = b0 + at;
-      k.chunks = __shfl(n, at);
-      k.first = before + __shfl(upto, at) - k.chunks;
-      k.tiles = __shfl(mine, at);
-      k.context = __shfl(context, at);
-      k.keys = __shfl(keys, at);
-      k.count = __shfl(count, at);
+      k.chunks = __builtin_amdgcn_readlane(n, at);
+      k.first = before + int(__builtin_amdgcn_readlane(upto, at)) - k.chunks;
+      k.tiles = __builtin_amdgcn_readlane(mine, at);
+      k.context = __builtin_amdgcn_readlane(context, at);
+      k.keys = __builtin_amdgcn_readlane(keys, at);
+      k.count = __builtin_amdgcn_readlane(count, at);
       return k;
     }
-    before += __shfl(upto, 63);
+    before += int(__builtin_amdgcn_readlane(upto, 63));
   }
   return k;
 }
@@ -680,7 +733,7 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
   w.g = w.lane >> 4;
   w.context = __builtin_amdgcn_readfirstlane(ck.context);
   w.keys = __builtin_amdgcn_readfirstlane(ck.keys);
-  w.scale = a.scale * 1.44269504088896341f;
+  w.scale = a.scale * 1.44269504088896341f * (FMT == NM_KV_INT8 ? kCodeUnit : 1.0f);
   const int rows = a.tokens * a.group;
   // the nodes' rows: t = r / group, query head head * group + r % group
 #pragma unroll
@@ -725,6 +778,7 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
     wait_loads<0>();
   __builtin_amdgcn_s_barrier();   // all of Q has arrived
   if (w.tiles > 0) {
+    w.sum_queries();
     uint32_t slot_i = 0;
     for (uint32_t i = 0; i < w.tiles; ++i) {
       const uint32_t tile = w.tile0 + i * w.step, key0 = tile * kTileKeys + 8u * w.g, left = w.tiles - i;
@@ -734,13 +788,13 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
       f16x8 y[NR];
       w.template wait_keys<S::kDepth>(left);
       w.read_keys(t, slot_i);
+      uint32_t bad = w.read_scales(t, slot_i, edge);
       if (left > uint32_t(S::kDepth)) w.template start<true>(i + S::kDepth, slot_i);
       w.scores(t, x);
-      uint32_t bad = 0;
       if (edge) {
         w.template wait_values<S::kDepth>(left - 1);
         w.read_values(t, slot_i);
-        bad = w.edge_values(t, key0);
+        bad |= w.edge_values(t, key0);
       }
       w.weights(t, x, y, edge, bad, key0);
       if (!edge) {
@@ -759,6 +813,11 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     w.l[n] = sum4(w.l[n]);
+    if constexpr (FMT == NM_KV_INT8) {   // O in its own unit, without the codes' bias
+      const float bias = w.tiles > 0 ? sum4(w.ws[n]) * kCodeBias : 0.f;
+#pragma unroll
+      for (int j = 0; j < S::kJ; ++j) w.o[j][n] = w.o[j][n] * kCodeUnit - bias;
+    }
     if (w.g == 0) {
       stat_m[wave][16 * n + w.li] = w.m[n];
       stat_l[wave][16 * n + w.li] = w.l[n];
@@ -927,7 +986,7 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
     }
   };
   if (units <= kAttnThreads)
-    join(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
+    join(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
   else
     join(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
   __syncthreads();
