@@ -4,9 +4,6 @@
 
 #include "nm_attn_impl.h"
 
-#ifndef NM_WIDEST
-#define NM_WIDEST (head_dim > 128 ? 2 : head_dim > 64 ? 3 : 4)
-#endif
 namespace nm {
 namespace {
 
@@ -29,12 +26,17 @@ Kernel kernel_of() {
   return {reinterpret_cast<const void*>(attention_kernel<FMT, D, NR>), S::kWaves, S::kLdsBytes};
 }
 
+// The most row tiles a workgroup takes: what its accumulators leave two waves a SIMD (one for
+// heads of 256 elements).
+int widest(int head_dim) { return head_dim > 128 ? 2 : head_dim > 64 ? 3 : 4; }
+
 template <int FMT, int D>
 Kernel kernel_of(int nr) {
-  if (nr == 1) return kernel_of<FMT, D, 1>();
-  if (nr == 2 || D > 128) return kernel_of<FMT, D, 2>();
-  if constexpr (D <= 128) return nr == 3 ? kernel_of<FMT, D, 3>() : kernel_of<FMT, D, 4>();
-  return {};
+  if constexpr (D <= 64)
+    if (nr == 4) return kernel_of<FMT, D, 4>();
+  if constexpr (D <= 128)
+    if (nr == 3) return kernel_of<FMT, D, 3>();
+  return nr == 2 ? kernel_of<FMT, D, 2>() : kernel_of<FMT, D, 1>();
 }
 
 template <int FMT>
@@ -52,8 +54,8 @@ Plan plan_of(const AttnCall& c, int head_dim, int format, const DeviceInfo& dev)
   Plan p;
   const int rows = c.tokens * c.group;
   // row tiles evenly over the fewest workgroups
-  const int tiles = (rows + 15) / 16, widest = NM_WIDEST;
-  p.row_tiles = (tiles + widest - 1) / widest;
+  const int tiles = (rows + 15) / 16, most_tiles = widest(head_dim);
+  p.row_tiles = (tiles + most_tiles - 1) / most_tiles;
   p.nr = (tiles + p.row_tiles - 1) / p.row_tiles;
   p.part_bytes = uint32_t(head_dim / 16 * p.nr * 1024 + p.nr * 128);
   const int64_t items = int64_t(c.batch) * c.cache.kv_heads * p.row_tiles;

@@ -154,44 +154,140 @@ constexpr __host__ __device__ int swizzle(int r) {
 
 // Reads of LDS that direct loads have filled. The compiler would wait for every such load in
 // flight before any read of LDS; the counted waits below are enough, so the reads are written
-// out, each group with its own wait.
+// out, each group with its own wait, and as few groups as may be: a wait costs some 200 cycles.
+
+// N fragments of Q, 1 KiB apart.
 template <int N>
-__device__ __forceinline__ void lds_read16(u32x4 (&d)[N], const uint32_t (&at)[N]) {
-  static_assert(N == 2 || N == 3 || N == 4 || N == 8, "");
+__device__ __forceinline__ void lds_read_fragments(u32x4 (&d)[N], uint32_t at) {
+  static_assert(N == 2 || N == 4 || N == 6, "");
   if constexpr (N == 2)
-    asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(d[0]), "=&v"(d[1]) : "v"(at[0]), "v"(at[1]) : "memory");
-  if constexpr (N == 3)
-    asm volatile("ds_read_b128 %0, %3\n\tds_read_b128 %1, %4\n\tds_read_b128 %2, %5\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]) : "v"(at[0]), "v"(at[1]), "v"(at[2]) : "memory");
+    asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:1024\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0]), "=&v"(d[1])
+                 : "v"(at) : "memory");
   if constexpr (N == 4)
-    asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\t"
-                 "s_waitcnt lgkmcnt(0)"
+    asm volatile("ds_read_b128 %0, %4\n\t"
+                 "ds_read_b128 %1, %4 offset:1024\n\t"
+                 "ds_read_b128 %2, %4 offset:2048\n\t"
+                 "ds_read_b128 %3, %4 offset:3072\n\ts_waitcnt lgkmcnt(0)"
                  : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3])
-                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]) : "memory");
-  if constexpr (N == 8)
-    asm volatile("ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\tds_read_b128 %3, %11\n\t"
-                 "ds_read_b128 %4, %12\n\tds_read_b128 %5, %13\n\tds_read_b128 %6, %14\n\tds_read_b128 %7, %15\n\t"
-                 "s_waitcnt lgkmcnt(0)"
-                 : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5]), "=&v"(d[6]), "=&v"(d[7])
-                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7])
-                 : "memory");
+                 : "v"(at) : "memory");
+  if constexpr (N == 6)
+    asm volatile("ds_read_b128 %0, %6\n\t"
+                 "ds_read_b128 %1, %6 offset:1024\n\t"
+                 "ds_read_b128 %2, %6 offset:2048\n\t"
+                 "ds_read_b128 %3, %6 offset:3072\n\t"
+                 "ds_read_b128 %4, %6 offset:4096\n\t"
+                 "ds_read_b128 %5, %6 offset:5120\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5])
+                 : "v"(at) : "memory");
 }
-__device__ __forceinline__ void lds_read8(u32x2 (&d)[8], const uint32_t (&at)[8]) {
+
+// 8 pieces of 16, 8 or 4 bytes: 4 at a[0..3], and 4 OFFSET bytes further.
+template <int OFFSET>
+__device__ __forceinline__ void lds_read_rows(u32x4 (&d)[8], const uint32_t (&a)[4]) {
+  asm volatile("ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\tds_read_b128 %3, %11\n\t"
+               "ds_read_b128 %4, %8 offset:%12\n\tds_read_b128 %5, %9 offset:%12\n\t"
+               "ds_read_b128 %6, %10 offset:%12\n\tds_read_b128 %7, %11 offset:%12\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5]), "=&v"(d[6]), "=&v"(d[7])
+               : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(OFFSET) : "memory");
+}
+template <int OFFSET>
+__device__ __forceinline__ void lds_read_rows(u32x2 (&d)[8], const uint32_t (&a)[4]) {
   asm volatile("ds_read_b64 %0, %8\n\tds_read_b64 %1, %9\n\tds_read_b64 %2, %10\n\tds_read_b64 %3, %11\n\t"
-               "ds_read_b64 %4, %12\n\tds_read_b64 %5, %13\n\tds_read_b64 %6, %14\n\tds_read_b64 %7, %15\n\t"
-               "s_waitcnt lgkmcnt(0)"
+               "ds_read_b64 %4, %8 offset:%12\n\tds_read_b64 %5, %9 offset:%12\n\t"
+               "ds_read_b64 %6, %10 offset:%12\n\tds_read_b64 %7, %11 offset:%12\n\ts_waitcnt lgkmcnt(0)"
                : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5]), "=&v"(d[6]), "=&v"(d[7])
-               : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7])
-               : "memory");
+               : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(OFFSET) : "memory");
 }
-__device__ __forceinline__ void lds_read4(uint32_t (&d)[8], const uint32_t (&at)[8]) {
+template <int OFFSET>
+__device__ __forceinline__ void lds_read_rows(uint32_t (&d)[8], const uint32_t (&a)[4]) {
   asm volatile("ds_read_b32 %0, %8\n\tds_read_b32 %1, %9\n\tds_read_b32 %2, %10\n\tds_read_b32 %3, %11\n\t"
-               "ds_read_b32 %4, %12\n\tds_read_b32 %5, %13\n\tds_read_b32 %6, %14\n\tds_read_b32 %7, %15\n\t"
-               "s_waitcnt lgkmcnt(0)"
+               "ds_read_b32 %4, %8 offset:%12\n\tds_read_b32 %5, %9 offset:%12\n\t"
+               "ds_read_b32 %6, %10 offset:%12\n\tds_read_b32 %7, %11 offset:%12\n\ts_waitcnt lgkmcnt(0)"
                : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5]), "=&v"(d[6]), "=&v"(d[7])
-               : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7])
-               : "memory");
+               : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(OFFSET) : "memory");
+}
+
+// A key row's pieces for both halves of a tile (rows 4 apart): L of each, from `a` on, and this
+// lane's key's two scales at `s` (SCALES).
+template <int L, int ROW_BYTES, bool SCALES>
+__device__ __forceinline__ void lds_read_keys(u32x4 (&d)[2][L], float& ks, float& vs, uint32_t a, uint32_t s) {
+  const uint32_t b = a ^ 64;   // the odd pieces of a row, every 128 bytes like the even ones
+  if constexpr (L == 1)
+    asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:%6\n\t"
+                 "ds_read_b32 %2, %5\n\tds_read_b32 %3, %5 offset:128\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0][0]), "=&v"(d[1][0]), "=&v"(ks), "=&v"(vs) : "v"(a), "v"(s), "n"(4 * ROW_BYTES) : "memory");
+  if constexpr (L == 2 && SCALES)
+    asm volatile("ds_read_b128 %0, %6\n\tds_read_b128 %1, %7\n\tds_read_b128 %2, %6 offset:%9\n\t"
+                 "ds_read_b128 %3, %7 offset:%9\n\tds_read_b32 %4, %8\n\tds_read_b32 %5, %8 offset:128\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0][0]), "=&v"(d[0][1]), "=&v"(d[1][0]), "=&v"(d[1][1]), "=&v"(ks), "=&v"(vs)
+                 : "v"(a), "v"(b), "v"(s), "n"(4 * ROW_BYTES) : "memory");
+  if constexpr (L == 2 && !SCALES)
+    asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %4 offset:%6\n\t"
+                 "ds_read_b128 %3, %5 offset:%6\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0][0]), "=&v"(d[0][1]), "=&v"(d[1][0]), "=&v"(d[1][1]) : "v"(a), "v"(b), "n"(4 * ROW_BYTES)
+                 : "memory");
+  if constexpr (L == 4 && SCALES)
+    asm volatile("ds_read_b128 %0, %10\n\tds_read_b128 %1, %11\n\tds_read_b128 %2, %10 offset:128\n\t"
+                 "ds_read_b128 %3, %11 offset:128\n\tds_read_b128 %4, %10 offset:%13\n\tds_read_b128 %5, %11 offset:%13\n\t"
+                 "ds_read_b128 %6, %10 offset:%14\n\tds_read_b128 %7, %11 offset:%14\n\t"
+                 "ds_read_b32 %8, %12\n\tds_read_b32 %9, %12 offset:128\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0][0]), "=&v"(d[0][1]), "=&v"(d[0][2]), "=&v"(d[0][3]), "=&v"(d[1][0]), "=&v"(d[1][1]),
+                   "=&v"(d[1][2]), "=&v"(d[1][3]), "=&v"(ks), "=&v"(vs)
+                 : "v"(a), "v"(b), "v"(s), "n"(4 * ROW_BYTES), "n"(4 * ROW_BYTES + 128) : "memory");
+  if constexpr (L == 4 && !SCALES)
+    asm volatile("ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %8 offset:128\n\t"
+                 "ds_read_b128 %3, %9 offset:128\n\tds_read_b128 %4, %8 offset:%10\n\tds_read_b128 %5, %9 offset:%10\n\t"
+                 "ds_read_b128 %6, %8 offset:%11\n\tds_read_b128 %7, %9 offset:%11\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(d[0][0]), "=&v"(d[0][1]), "=&v"(d[0][2]), "=&v"(d[0][3]), "=&v"(d[1][0]), "=&v"(d[1][1]),
+                   "=&v"(d[1][2]), "=&v"(d[1][3])
+                 : "v"(a), "v"(b), "n"(4 * ROW_BYTES), "n"(4 * ROW_BYTES + 128) : "memory");
+  if constexpr (L == 8)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %8 offset:128\n\t"
+                   "ds_read_b128 %3, %9 offset:128\n\tds_read_b128 %4, %8 offset:256\n\tds_read_b128 %5, %9 offset:256\n\t"
+                   "ds_read_b128 %6, %8 offset:384\n\tds_read_b128 %7, %9 offset:384\n\ts_waitcnt lgkmcnt(0)"
+                   : "=&v"(d[h][0]), "=&v"(d[h][1]), "=&v"(d[h][2]), "=&v"(d[h][3]), "=&v"(d[h][4]), "=&v"(d[h][5]),
+                     "=&v"(d[h][6]), "=&v"(d[h][7])
+                   : "v"(a + h * 4 * ROW_BYTES), "v"(b + h * 4 * ROW_BYTES) : "memory");
+}
+
+// Hands three numbers of each key (by the lane of its number, at `to`) to the lanes that need
+// them, 8 keys' from `from` on, and reads the first fragments of Q, 1 KiB apart from `qa` on.
+__device__ __forceinline__ void lds_share(u32x4 (&d)[6], u32x4 (&q)[2], uint32_t to, float x, float y, float z,
+                                          uint32_t from, uint32_t qa) {
+  asm volatile("ds_write_b32 %8, %9\n\tds_write_b32 %8, %10 offset:128\n\tds_write_b32 %8, %11 offset:256\n\t"
+               "ds_read_b128 %6, %13\n\tds_read_b128 %7, %13 offset:1024\n\t"
+               "ds_read_b128 %0, %12\n\tds_read_b128 %1, %12 offset:16\n\tds_read_b128 %2, %12 offset:128\n\t"
+               "ds_read_b128 %3, %12 offset:144\n\tds_read_b128 %4, %12 offset:256\n\tds_read_b128 %5, %12 offset:272\n\t"
+               "s_waitcnt lgkmcnt(0)"
+               : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5]),
+                 "=&v"(q[0]), "=&v"(q[1])
+               : "v"(to), "v"(x), "v"(y), "v"(z), "v"(from), "v"(qa) : "memory");
+}
+__device__ __forceinline__ void lds_share(u32x4 (&d)[6], u32x4 (&q)[4], uint32_t to, float x, float y, float z,
+                                          uint32_t from, uint32_t qa) {
+  asm volatile("ds_write_b32 %10, %11\n\tds_write_b32 %10, %12 offset:128\n\tds_write_b32 %10, %13 offset:256\n\t"
+               "ds_read_b128 %6, %15\n\tds_read_b128 %7, %15 offset:1024\n\tds_read_b128 %8, %15 offset:2048\n\tds_read_b128 %9, %15 offset:3072\n\t"
+               "ds_read_b128 %0, %14\n\tds_read_b128 %1, %14 offset:16\n\tds_read_b128 %2, %14 offset:128\n\t"
+               "ds_read_b128 %3, %14 offset:144\n\tds_read_b128 %4, %14 offset:256\n\tds_read_b128 %5, %14 offset:272\n\t"
+               "s_waitcnt lgkmcnt(0)"
+               : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5]),
+                 "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2]), "=&v"(q[3])
+               : "v"(to), "v"(x), "v"(y), "v"(z), "v"(from), "v"(qa) : "memory");
+}
+__device__ __forceinline__ void lds_share(u32x4 (&d)[6], u32x4 (&q)[6], uint32_t to, float x, float y, float z,
+                                          uint32_t from, uint32_t qa) {
+  asm volatile("ds_write_b32 %12, %13\n\tds_write_b32 %12, %14 offset:128\n\tds_write_b32 %12, %15 offset:256\n\t"
+               "ds_read_b128 %6, %17\n\tds_read_b128 %7, %17 offset:1024\n\tds_read_b128 %8, %17 offset:2048\n\tds_read_b128 %9, %17 offset:3072\n\tds_read_b128 %10, %17 offset:4096\n\tds_read_b128 %11, %17 offset:5120\n\t"
+               "ds_read_b128 %0, %16\n\tds_read_b128 %1, %16 offset:16\n\tds_read_b128 %2, %16 offset:128\n\t"
+               "ds_read_b128 %3, %16 offset:144\n\tds_read_b128 %4, %16 offset:256\n\tds_read_b128 %5, %16 offset:272\n\t"
+               "s_waitcnt lgkmcnt(0)"
+               : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5]),
+                 "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2]), "=&v"(q[3]), "=&v"(q[4]), "=&v"(q[5])
+               : "v"(to), "v"(x), "v"(y), "v"(z), "v"(from), "v"(qa) : "memory");
 }
 
 // Waits until at most N loads are in flight.
@@ -323,79 +419,52 @@ struct AttnWave {
     wait_loads<N * S::kTileLoads - (N == S::kDepth && N > 0 ? S::kLoads : 0)>();
   }
 
-  __device__ __forceinline__ void read_keys(AttnTile<FMT, D>& t, uint32_t slot) const {
-    const uint32_t base = ring_at + slot * S::kSlotBytes;
-    constexpr int L = S::kLoadsK;
-    if constexpr (L <= 4) {
-      u32x4 d[2 * L];
-      uint32_t at[2 * L];
-#pragma unroll
-      for (int x = 0; x < 2 * L; ++x)
-        at[x] = base + (read_k ^ (x % L % 2 * 64)) + x % L / 2 * 128 + x / L * 4 * S::kRowBytes;
-      lds_read16(d, at);
-#pragma unroll
-      for (int x = 0; x < 2 * L; ++x) t.k[x / L][x % L] = d[x];
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 d[L];
-        uint32_t at[L];
-#pragma unroll
-        for (int x = 0; x < L; ++x) at[x] = base + (read_k ^ (x % 2 * 64)) + x / 2 * 128 + h * 4 * S::kRowBytes;
-        lds_read16(d, at);
-#pragma unroll
-        for (int x = 0; x < L; ++x) t.k[h][x] = d[x];
-      }
-    }
-  }
+  static constexpr int kGroup = NR == 1 ? (S::kSteps < 4 ? S::kSteps : 4) : NR < 4 ? 2 : 1;   // steps of Q read at a time
 
-  // What the scores need of a tile's scales, worked out once a key (by the lane of its number)
-  // and handed round through LDS, in place of the scales. Returns the keys, a bit each of this
-  // lane's 8, whose value's scale is not a number (edge tiles; elsewhere it makes NaN by itself).
-  __device__ __forceinline__ uint32_t read_scales(AttnTile<FMT, D>& t, uint32_t slot, bool edge) const {
-    if constexpr (FMT == NM_KV_FP16) return 0;
-    const uint32_t base = ring_at + slot * S::kSlotBytes + 2 * S::kSideBytes, mine = base + 4 * (lane & 31);
-    float ks, vs;
-    asm volatile("ds_read_b32 %0, %2\n\tds_read_b32 %1, %2 offset:128\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(ks), "=&v"(vs) : "v"(mine) : "memory");
-    uint32_t bad = 0;
-    if (edge) {
-      const bool b = !(vs < __builtin_inff());
-      bad = uint32_t(__ballot(b)) >> (8 * g) & 0xFFu;
-      if (b) vs = 1.0f;
-    }
-    vs = vs < kLeastScale ? kLeastScale : vs;   // NaN stays
-    const float kc = ks * scale, lz = __builtin_amdgcn_logf(vs), iz = __builtin_amdgcn_rcpf(vs);
-    const uint32_t from = base + 32 * g;
-    u32x4 d[6];
-    asm volatile("ds_write_b32 %6, %7\n\tds_write_b32 %6, %8 offset:128\n\tds_write_b32 %6, %9 offset:256\n\t"
-                 "ds_read_b128 %0, %10\n\tds_read_b128 %1, %10 offset:16\n\t"
-                 "ds_read_b128 %2, %10 offset:128\n\tds_read_b128 %3, %10 offset:144\n\t"
-                 "ds_read_b128 %4, %10 offset:256\n\tds_read_b128 %5, %10 offset:272\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(d[4]), "=&v"(d[5])
-                 : "v"(mine), "v"(kc), "v"(lz), "v"(iz), "v"(from) : "memory");
+  // A tile's keys, the first group of Q, and what the scores need of the scales, worked out once
+  // a key and handed round through LDS in place of the scales. Returns the keys, a bit each of
+  // this lane's 8, whose value's scale is not a number (edge tiles; elsewhere it makes NaN by
+  // itself).
+  __device__ __forceinline__ uint32_t read_keys(AttnTile<FMT, D>& t, u32x4 (&q)[NR * kGroup], uint32_t slot, bool edge) const {
+    const uint32_t base = ring_at + slot * S::kSlotBytes, shared = base + 2 * S::kSideBytes, mine = shared + 4 * (lane & 31);
+    float ks = 0.f, vs = 0.f;
+    lds_read_keys<S::kLoadsK, S::kRowBytes, FMT != NM_KV_FP16>(t.k, ks, vs, base + read_k, mine);
+    if constexpr (FMT == NM_KV_FP16) {
+      lds_read_fragments(q, q_at);
+      return 0;
+    } else {
+      uint32_t bad = 0;
+      if (edge) {
+        const bool b = !(vs < __builtin_inff());
+        bad = uint32_t(__ballot(b)) >> (8 * g) & 0xFFu;
+        if (b) vs = 1.0f;
+      }
+      vs = vs < kLeastScale ? kLeastScale : vs;   // NaN stays
+      u32x4 d[6];
+      lds_share(d, q, mine, ks * scale, __builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs), shared + 32 * g, q_at);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      t.kc[e] = __uint_as_float(d[e >> 2][e & 3]);
-      t.lz[e] = __uint_as_float(d[2 + (e >> 2)][e & 3]);
-      t.iz[e] = __uint_as_float(d[4 + (e >> 2)][e & 3]);
+      for (int e = 0; e < 8; ++e) {
+        t.kc[e] = __uint_as_float(d[e >> 2][e & 3]);
+        t.lz[e] = __uint_as_float(d[2 + (e >> 2)][e & 3]);
+        t.iz[e] = __uint_as_float(d[4 + (e >> 2)][e & 3]);
+      }
+      return bad;
     }
-    return bad;
   }
 
   __device__ __forceinline__ void read_values(AttnTile<FMT, D>& t, uint32_t slot) const {
     const uint32_t base = ring_at + slot * S::kSlotBytes + S::kSideBytes;
-    uint32_t at[8];
+    uint32_t at[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) at[e] = base + read_v[e & 3] + (e >> 2) * 4 * S::kRowBytes;
+    for (int x = 0; x < 4; ++x) at[x] = base + read_v[x];
     if constexpr (S::kWordsV == 1) {
       uint32_t d[8];
-      lds_read4(d, at);
+      lds_read_rows<4 * S::kRowBytes>(d, at);
 #pragma unroll
       for (int e = 0; e < 8; ++e) t.v[e][0] = d[e];
     } else if constexpr (S::kWordsV == 2) {
       u32x2 d[8];
-      lds_read8(d, at);
+      lds_read_rows<4 * S::kRowBytes>(d, at);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         t.v[e][0] = d[e][0];
@@ -405,14 +474,13 @@ struct AttnWave {
 #pragma unroll
       for (int c = 0; c < S::kWordsV / 4; ++c) {
         u32x4 d[8];
-        if (c > 0)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) at[e] ^= 16;   // the other half of a 32-byte run
-        lds_read16(d, at);
+        lds_read_rows<4 * S::kRowBytes>(d, at);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
 #pragma unroll
           for (int i = 0; i < 4; ++i) t.v[e][4 * c + i] = d[e][i];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) at[x] ^= 16;   // the other half of a 32-byte run
       }
     }
   }
@@ -446,20 +514,15 @@ struct AttnWave {
   }
 
   // The scores of a tile in units of log2, with log2 z: x[n][e] is this lane's row n, key 8 g + e.
-  __device__ __forceinline__ void scores(const AttnTile<FMT, D>& t, float (&x)[NR][8]) const {
+  __device__ __forceinline__ void scores(const AttnTile<FMT, D>& t, u32x4 (&q)[NR * kGroup], float (&x)[NR][8]) const {
     f32x4 s[NR][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    constexpr int G = NR == 1 ? (S::kSteps < 4 ? S::kSteps : 4) : NR == 2 ? 2 : 1;   // steps of Q read at a time
 #pragma unroll
-    for (int s0 = 0; s0 < S::kSteps; s0 += G) {
-      u32x4 q[NR * G];
-      uint32_t at[NR * G];
+    for (int s0 = 0; s0 < S::kSteps; s0 += kGroup) {
+      if (s0 > 0) lds_read_fragments(q, q_at + s0 * NR * 1024);
 #pragma unroll
-      for (int x = 0; x < NR * G; ++x) at[x] = q_at + ((x % NR) * S::kSteps + s0 + x / NR) * 1024;
-      lds_read16(q, at);
-#pragma unroll
-      for (int u = 0; u < G; ++u)
+      for (int u = 0; u < kGroup; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int st = s0 + u;
@@ -492,18 +555,20 @@ struct AttnWave {
     f16x8 ones;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ones[e] = _Float16(1.0f);
+    f32x4 sum[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) sum[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s0 = 0; s0 < S::kSteps; s0 += kGroup) {
+      u32x4 q[NR * kGroup];
+      lds_read_fragments(q, q_at + s0 * NR * 1024);
+#pragma unroll
+      for (int x = 0; x < NR * kGroup; ++x)
+        sum[x % NR] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, __builtin_bit_cast(f16x8, q[x]), sum[x % NR], 0, 0, 0);
+    }
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int st = 0; st < S::kSteps; st += 2) {
-        u32x4 q[2];
-        const uint32_t at[2] = {q_at + (n * S::kSteps + st) * 1024, q_at + (n * S::kSteps + st + 1) * 1024};
-        lds_read16(q, at);
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, __builtin_bit_cast(f16x8, q[0]), sum, 0, 0, 0);
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, __builtin_bit_cast(f16x8, q[1]), sum, 0, 0, 0);
-      }
-      qs[n] = sum[0] * (-kCodeBias / kCodeUnit);
+      qs[n] = sum[n][0] * (-kCodeBias / kCodeUnit);
       ws[n] = 0.f;
     }
   }
@@ -665,15 +730,22 @@ __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, in
     uint64_t total = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64)
       total += uint32_t(__builtin_amdgcn_readlane(wave_scan(tiles_of(b0 + lane)), 63));
-    // The last chunk of a sequence is half empty on average: that many slots are set aside, and
-    // one a sequence, which always fits, if they do not do. Whole rounds of the waves.
-    const double half = ceil(double(total) / ((double(slots) - 0.5 * a.batch) * kAttnWaves));
-    per = uint32_t(fmax(half * kAttnWaves, double(kMinChunkTiles)));
-    uint32_t used = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 64)
-      used += uint32_t(__builtin_amdgcn_readlane(
-          wave_scan(b0 + lane < a.batch ? chunks_of(tiles_of(b0 + lane), per) : 0u), 63));
-    if (used > uint32_t(slots)) per = uint32_t(ceil(double(total) / (double(slots - a.batch) * kAttnWaves))) * kAttnWaves;
+    // The smallest chunk, in whole rounds of the waves, whose number fits the slots: steps of a
+    // 32nd up from an even split, and from there to one slot a sequence set aside, which always fits.
+    const double round = 1.0 / kAttnWaves;
+    per = max(uint32_t(ceil(double(total) / slots * round)) * kAttnWaves, uint32_t(kMinChunkTiles));
+    for (int tries = 0;; ++tries) {
+      uint32_t used = 0;
+      for (int b0 = 0; b0 < a.batch; b0 += 64)
+        used += uint32_t(__builtin_amdgcn_readlane(
+            wave_scan(b0 + lane < a.batch ? chunks_of(tiles_of(b0 + lane), per) : 0u), 63));
+      if (used <= uint32_t(slots)) break;
+      if (tries == 8) {
+        per = uint32_t(ceil(double(total) / (slots - a.batch) * round)) * kAttnWaves;
+        break;
+      }
+      per += (per / 32 + kAttnWaves) / kAttnWaves * kAttnWaves;
+    }
   }
   AttnChunk k;
   k.b = -1;
@@ -758,7 +830,7 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
   // the last node's repeat row 0: nothing of theirs is stored.
 #pragma unroll
   for (int f = 0; f < (NR * S::kSteps + kAttnWaves - 1) / kAttnWaves; ++f) {
-    const int x = f * kAttnWaves + wave, fn = x / S::kSteps, st = x % S::kSteps;
+    const int x = f * kAttnWaves + wave, fn = x % NR, st = x / NR;
     if (x >= NR * S::kSteps) break;
     int r = (rt * NR + fn) * 16 + w.li;
     r = r < rows ? r : 0;
@@ -787,10 +859,10 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
       float x[NR][8];
       f16x8 y[NR];
       w.template wait_keys<S::kDepth>(left);
-      w.read_keys(t, slot_i);
-      uint32_t bad = w.read_scales(t, slot_i, edge);
+      u32x4 q[NR * AttnWave<FMT, D, NR>::kGroup];
+      uint32_t bad = w.read_keys(t, q, slot_i, edge);
       if (left > uint32_t(S::kDepth)) w.template start<true>(i + S::kDepth, slot_i);
-      w.scores(t, x);
+      w.scores(t, q, x);
       if (edge) {
         w.template wait_values<S::kDepth>(left - 1);
         w.read_values(t, slot_i);
