@@ -36,6 +36,7 @@ constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kTileKeys = 32;
 constexpr int kMinChunkTiles = 2 * kAttnWaves;   // two tiles a wave: a chunk more costs the join as much
+constexpr int kNonTemporal = 2;              // cache policy bit of a load
 constexpr float kLowest = -3e38f;            // the reference of a row that has seen nothing
 // A value's scale counts as at least this (rows of zeros have scale 0, and codes 0): far below
 // what fp16 results can show, and its reciprocal times any number of keys is finite.
@@ -316,6 +317,7 @@ struct AttnWave {
   int head, lane, li, g;
   uint32_t keys, context;     // all of the sequence's keys; those every node sees
   float scale;                // of the scores, times log2 e
+  bool once;                  // one workgroup of rows: keys and values are read by it alone
   uint64_t mask[NR];
   f32x4 o[S::kJ][NR];
   float m[NR], l[NR];
@@ -373,13 +375,13 @@ struct AttnWave {
   }
 
   // The J-th and later loads of a half's rows, 1024 bytes each.
-  template <int J>
+  template <int J, int POLICY>
   __device__ __forceinline__ void start_rows(const char* from, char* to, int h) const {
     if constexpr (J < S::kLoads / 2) {
       const uint32_t piece = fetch ^ uint32_t(swizzle<S::kRowBytes>(16 * h + J * S::kLoadRows) * 16);
       __builtin_amdgcn_global_load_lds((global_void*)(from + J / 4 * 4096 + piece), (lds_void*)(to + J / 4 * 4096), 16,
-                                       J % 4 * 1024, 0);
-      start_rows<J + 1>(from, to, h);
+                                       J % 4 * 1024, POLICY);
+      start_rows<J + 1, POLICY>(from, to, h);
     }
   }
 
@@ -393,7 +395,12 @@ struct AttnWave {
     for (int h = 0; h < 2; ++h) {
       // a half's rows follow each other in memory as in LDS: one base and an offset of both
       const char* from = (KEYS ? cache.k : cache.v) + row[h] * S::kRowBytes;
-      start_rows<0>(from, to + h * 16 * S::kRowBytes, h);
+      // Read once, they need not stay in the caches: 2 x 131071 int8 tokens 120 -> 110 us. With
+      // several workgroups of rows they are read again, from L2.
+      if (once)
+        start_rows<0, kNonTemporal>(from, to + h * 16 * S::kRowBytes, h);
+      else
+        start_rows<0, 0>(from, to + h * 16 * S::kRowBytes, h);
     }
     if constexpr (KEYS && FMT != NM_KV_FP16) {
       const float* s = lane < 32 ? cache.k_scale : cache.v_scale;
@@ -716,29 +723,39 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
   return x;
 }
 
-// Every wave works this out for itself: 64 sequences a pass, one a lane.
+// Every wave works this out for itself: 64 sequences a pass, one a lane; the first 64 stay in
+// registers.
 __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, int slot, uint32_t most) {
   const int lane = threadIdx.x & 63;
-  const auto tiles_of = [&](int b) {
-    uint32_t context, keys = 0;
+  struct Lengths {
+    uint32_t context, keys, tiles;   // tiles: at most 2^25
     int count;
-    if (b < a.batch) attn_lengths(a, b, context, keys, count);
-    return (keys + kTileKeys - 1) / kTileKeys;   // at most 2^25
   };
+  const auto load = [&](int b) {
+    Lengths x{0, 0, 0, 0};
+    if (b < a.batch) {
+      attn_lengths(a, b, x.context, x.keys, x.count);
+      x.tiles = (x.keys + kTileKeys - 1) / kTileKeys;
+    }
+    return x;
+  };
+  const Lengths front = load(lane);
+  const auto at_group = [&](int b0) { return b0 == 0 ? front : load(b0 + lane); };
   uint32_t per = 0x7FFFFFFFu;
   if (slots > a.batch) {
     uint64_t total = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64)
-      total += uint32_t(__builtin_amdgcn_readlane(wave_scan(tiles_of(b0 + lane)), 63));
+      total += uint32_t(__builtin_amdgcn_readlane(wave_scan(at_group(b0).tiles), 63));
     // The smallest chunk, in whole rounds of the waves, whose number fits the slots: steps of a
-    // 32nd up from an even split, and from there to one slot a sequence set aside, which always fits.
+    // 32nd up from an even split, and from there to one slot a sequence set aside, which always
+    // fits. (The sums are below 2^41, exact in 64-bit floats.)
     const double round = 1.0 / kAttnWaves;
     per = max(uint32_t(ceil(double(total) / slots * round)) * kAttnWaves, uint32_t(kMinChunkTiles));
     for (int tries = 0;; ++tries) {
       uint32_t used = 0;
       for (int b0 = 0; b0 < a.batch; b0 += 64)
         used += uint32_t(__builtin_amdgcn_readlane(
-            wave_scan(b0 + lane < a.batch ? chunks_of(tiles_of(b0 + lane), per) : 0u), 63));
+            wave_scan(b0 + lane < a.batch ? chunks_of(at_group(b0).tiles, per) : 0u), 63));
       if (used <= uint32_t(slots)) break;
       if (tries == 8) {
         per = uint32_t(ceil(double(total) / (slots - a.batch) * round)) * kAttnWaves;
@@ -751,16 +768,15 @@ __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, in
   k.b = -1;
   int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    uint32_t context = 0, keys = 0, mine = per;
-    int count = 0, n = 0;
+    const Lengths x = at_group(b0);
+    uint32_t mine = per;
+    int n = 0;
     if (b0 + lane < a.batch) {
-      attn_lengths(a, b0 + lane, context, keys, count);
-      const uint32_t tiles = (keys + kTileKeys - 1) / kTileKeys;
       if (slots > a.batch) {   // as many chunks as `per` asks for, of even size
-        n = int(chunks_of(tiles, chunk_tiles(tiles, per, most)));
-        mine = max((tiles + n * kAttnWaves - 1) / (n * kAttnWaves), 1u) * kAttnWaves;
+        n = int(chunks_of(x.tiles, chunk_tiles(x.tiles, per, most)));
+        mine = max((x.tiles + n * kAttnWaves - 1) / (n * kAttnWaves), 1u) * kAttnWaves;
       }
-      n = int(chunks_of(tiles, mine));
+      n = int(chunks_of(x.tiles, mine));
     }
     const uint32_t upto = wave_scan(uint32_t(n));
     const uint64_t past = __ballot(before + int(upto) > slot);
@@ -770,9 +786,9 @@ __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, in
       k.chunks = __builtin_amdgcn_readlane(n, at);
       k.first = before + int(__builtin_amdgcn_readlane(upto, at)) - k.chunks;
       k.tiles = __builtin_amdgcn_readlane(mine, at);
-      k.context = __builtin_amdgcn_readlane(context, at);
-      k.keys = __builtin_amdgcn_readlane(keys, at);
-      k.count = __builtin_amdgcn_readlane(count, at);
+      k.context = __builtin_amdgcn_readlane(x.context, at);
+      k.keys = __builtin_amdgcn_readlane(x.keys, at);
+      k.count = __builtin_amdgcn_readlane(x.count, at);
       return k;
     }
     before += int(__builtin_amdgcn_readlane(upto, 63));
@@ -805,6 +821,7 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
   w.g = w.lane >> 4;
   w.context = __builtin_amdgcn_readfirstlane(ck.context);
   w.keys = __builtin_amdgcn_readfirstlane(ck.keys);
+  w.once = sp.row_tiles == 1;
   w.scale = a.scale * 1.44269504088896341f * (FMT == NM_KV_INT8 ? kCodeUnit : 1.0f);
   const int rows = a.tokens * a.group;
   // the nodes' rows: t = r / group, query head head * group + r % group
@@ -1036,9 +1053,10 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
         for (int x = 0; x < CC; ++x)
           if (c0 + x * groups < chunks)
 #pragma unroll
-            for (int v = 0; v < UU; ++v)   // units past the last: within the sequence's partials, not used
-              y[v][x] = __builtin_amdgcn_raw_buffer_load_b128(
-                  buf, (c0 + x * groups) * stride + kStats + (u0 + v * kAttnThreads) * 16, 0, kCoherent);
+            for (int v = 0; v < UU; ++v)
+              if (v == 0 || u0 + v * kAttnThreads < units)
+                y[v][x] = __builtin_amdgcn_raw_buffer_load_b128(
+                    buf, (c0 + x * groups) * stride + kStats + (u0 + v * kAttnThreads) * 16, 0, kCoherent);
 #pragma unroll
         for (int x = 0; x < CC; ++x)
           if (c0 + x * groups < chunks)
@@ -1057,7 +1075,9 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
       }
     }
   };
-  if (units <= kAttnThreads)
+  // (16 loads: 32 need more registers than there are. 20 rows of 64, 2 x 16384 tokens: 27.7 us with
+  // 1 x 16, 30.7 with 4 x 4; 16 rows of 256, 4 x 16384: 44.9 and 40.6.)
+  if (units <= 2 * kAttnThreads)
     join(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
   else
     join(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
