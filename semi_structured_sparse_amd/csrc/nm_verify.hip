@@ -2,16 +2,15 @@
 //
 // Mathematics. A chain's drafts i are accepted while u_i q(x_i) < p(x_i); the tests of all
 // drafts are independent, so one wave makes them at once and the first failure ends the chain.
-// A tree's child c stands if u_c (1 - mass of its earlier siblings) < p(x_c), which also depends
-// on its own row and siblings only: every node is decided at once, and the walk from the root
-// follows the first child that stands. The next token is the first index whose running sum of
-// the last row's weights exceeds u_0 times their sum, in 64 bits, so that the order of the sums
-// moves a border by about 2^-50.
+// A tree's child c stands if u_c (1 - mass of its earlier siblings) < p(x_c): the nodes' p are
+// gathered at once, and the walk from the root tests the children of the nodes it reaches. The
+// next token is the first index whose running sum of the last row's weights exceeds u_0 times
+// their sum, in 64 bits, so that the order of the sums moves a border by about 2^-50.
 //
 // What bounds it: one row of the target (and of the draft) a sequence is read for the draw,
 // e.g. 64 x 128256 x 8 bytes. A single workgroup reads a row at the rate of one CU, so a row
-// goes to several: each sums a chunk, the last to arrive finds the chunk the threshold falls
-// in and walks that one alone. The decisions cost a chain of dependent loads (count, tokens,
+// goes to several: each sums a chunk, the last to arrive finds the run of it that the threshold
+// falls in and walks that one alone. The decisions cost a chain of dependent loads (tokens,
 // probabilities), so every workgroup makes them for itself rather than wait for another.
 #include "nm_decode_internal.h"
 
@@ -22,7 +21,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMaxChunks = 64;                     // workgroups of a row
 constexpr int kMaxParts = kMaxChunks * kWaves;     // its waves' runs: four a lane of the joining wave
-constexpr int kMinChunk = 2048;                    // elements: shorter rows are not worth the hand-over
+constexpr int kMinChunk = 1024;                    // elements: one load of 16 bytes a lane
 
 // Where a row's waves leave the sums of their runs: {with the draft (or the refused tokens)
 // taken off, the target alone} for every sequence and run.
@@ -35,7 +34,7 @@ struct VerifySplit {
 struct Row {               // the row the next token is drawn from
   const float* target;
   const float* draft;      // NULL: none subtracted
-  const int* refused;      // LDS, tokens of weight zero
+  int refused;             // lane k < refusals: a token of weight zero
   int refusals;
 };
 
@@ -48,46 +47,65 @@ struct Pair {
   double rest, whole;      // weights with what is taken off, and of the target alone
 };
 
-// The weights of element i, exact (or rounded once) in 64 bits.
+// The refused tokens (lanes, a bit each) in [lo, hi): mostly none.
+__device__ __forceinline__ uint64_t refused_in(const Row& w, int lo, int hi) {
+  return __ballot(int(threadIdx.x & 63) < w.refusals && w.refused >= lo && w.refused < hi);
+}
+
+// The weights of element i, exact (or rounded once) in 64 bits. some: refused tokens to look for.
 template <bool DRAFT>
-__device__ __forceinline__ Pair weigh(const Row& w, int i, float p, float q) {
+__device__ __forceinline__ Pair weigh(const Row& w, uint64_t some, int i, float p, float q) {
   Pair x;
   x.whole = kept(double(p));
   x.rest = DRAFT ? kept(double(p) - double(q)) : x.whole;
   if (!DRAFT)
-    for (int k = 0; k < w.refusals; ++k)
-      if (w.refused[k] == i) x.rest = 0.0;
+    for (uint64_t m = some; m != 0; m &= m - 1)
+      if (__builtin_amdgcn_readlane(w.refused, __builtin_ctzll(m)) == i) x.rest = 0.0;
   return x;
 }
 
-// Sums of the weights from lo + first on, `step` apart in groups of four neighbours.
-template <bool DRAFT>
-__device__ __forceinline__ Pair sum_run(const Row& w, int lo, int hi, int first, int step) {
-  Pair s{0.0, 0.0};
-  int i = lo + first;
-  constexpr int U = 4;     // groups in flight
-  for (; i + (U - 1) * step + 4 <= hi; i += U * step) {
-    quad p[U], q[U];
+// N elements from i on (zeros at and past hi) in groups of four, `step` apart.
+template <bool DRAFT, int N>
+__device__ __forceinline__ void load_run(const Row& w, int i, int step, int hi, float (&p)[N], float (&q)[N]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      p[u] = *reinterpret_cast<const quad*>(w.target + i + u * step);
-      if (DRAFT) q[u] = *reinterpret_cast<const quad*>(w.draft + i + u * step);
+  for (int u = 0; u < N / 4; ++u) {
+    const int at = i + u * step;
+    quad a = {0.f, 0.f, 0.f, 0.f}, b = {0.f, 0.f, 0.f, 0.f};
+    if (at + 4 <= hi) {
+      a = *reinterpret_cast<const quad*>(w.target + at);
+      if (DRAFT) b = *reinterpret_cast<const quad*>(w.draft + at);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (at + e < hi) {
+          a[e] = w.target[at + e];
+          if (DRAFT) b[e] = w.draft[at + e];
+        }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const Pair x = weigh<DRAFT>(w, i + u * step + e, p[u][e], DRAFT ? q[u][e] : 0.f);
-        s.rest += x.rest;
-        s.whole += x.whole;
-      }
+    for (int e = 0; e < 4; ++e) {
+      p[4 * u + e] = a[e];
+      q[4 * u + e] = b[e];
+    }
   }
-  for (; i < hi; i += step)
-    for (int e = 0; e < 4 && i + e < hi; ++e) {
-      const Pair x = weigh<DRAFT>(w, i + e, w.target[i + e], DRAFT ? w.draft[i + e] : 0.f);
+}
+
+// The sums of a wave's run [lo, hi), of this lane's elements.
+template <bool DRAFT>
+__device__ __forceinline__ Pair sum_run(const Row& w, int lo, int hi) {
+  const uint64_t some = refused_in(w, lo, hi);
+  Pair s{0.0, 0.0};
+  constexpr int N = 16;   // elements in flight a lane: 32 or non-temporal loads gained nothing
+  for (int i = lo + 4 * int(threadIdx.x & 63); i < hi; i += 64 * N) {
+    float p[N], q[N];
+    load_run<DRAFT>(w, i, 256, hi, p, q);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const Pair x = weigh<DRAFT>(w, some, i + e / 4 * 256 + e % 4, p[e], q[e]);
       s.rest += x.rest;
       s.whole += x.whole;
     }
+  }
   return s;
 }
 
@@ -97,19 +115,21 @@ __device__ __forceinline__ double lane_value(double x, int lane) {   // lane: th
   return __longlong_as_double((long long)(uint64_t(hi) << 32 | lo));
 }
 
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
-  return x;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double shifted(double x) {   // zero where there is no lane to take from
+  const uint64_t v = uint64_t(__double_as_longlong(x));
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, uint32_t(v), CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, uint32_t(v >> 32), CTRL, ROWS, 0xF, false);
+  return __longlong_as_double((long long)(uint64_t(hi) << 32 | lo));
 }
 
 __device__ __forceinline__ double wave_scan(double x) {   // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const double y = __shfl_up(x, o);
-    if (lane >= o) x += y;
-  }
+  x += shifted<0x111, 0xF>(x);   // row_shr 1, 2, 4, 8
+  x += shifted<0x112, 0xF>(x);
+  x += shifted<0x114, 0xF>(x);
+  x += shifted<0x118, 0xF>(x);
+  x += shifted<0x142, 0xA>(x);   // the row before's last, rows 1 and 3
+  x += shifted<0x143, 0xC>(x);   // the first half's last, rows 2 and 3
   return x;
 }
 
@@ -141,9 +161,9 @@ __device__ __forceinline__ Decision decide_chain(const VerifyCall& a, int64_t b,
   return d;
 }
 
-// A tree, by one wave: lane c decides node c. refused and path are LDS arrays.
-__device__ __forceinline__ Decision decide_tree(const VerifyCall& a, int64_t b, int& n, int* refused, int* path,
-                                                int* refusals) {
+// A tree, by one wave: lane c holds node c. path is an LDS array; the tokens refused at the last
+// node go to the row.
+__device__ __forceinline__ Decision decide_tree(const VerifyCall& a, int64_t b, int& n, int* path, Row& w) {
   const int lane = threadIdx.x & 63;
   int parent = -1, token = -1;
   double mass = 0.0, u = 0.0;
@@ -155,33 +175,31 @@ __device__ __forceinline__ Decision decide_tree(const VerifyCall& a, int64_t b, 
   n = count_of(a.count, b, a.nodes);
   if (lane >= n || parent < 0 || parent >= lane || token < 0 || token >= a.vocab) parent = -1;
   if (parent >= 0) mass = kept(double(a.target[(b * a.nodes + parent) * a.vocab + token]));
-  // siblings in node order: lane s is final when its turn comes
-  double left = 1.0;
-  bool again = false, taken = false;
-  for (int s = 1; s < n; ++s) {
-    const int ps = __builtin_amdgcn_readlane(parent, s), ts = __builtin_amdgcn_readlane(token, s);
-    const bool stood = (__ballot(!again && u * left < mass) >> s) & 1;
-    const double ms = lane_value(again ? 0.0 : mass, s);
-    if (ps >= 0 && ps == parent && lane > s) {
-      again |= ts == token;
-      left -= ms;
-      taken |= stood;
-    }
-  }
-  const bool chosen = parent >= 0 && !again && !taken && u * left < mass;
   Decision d{0, 0, false};
   if (lane == 0) path[0] = 0;
   while (true) {
-    const uint64_t next = __ballot(chosen && parent == d.row);   // parents are before their children
-    if (next == 0) break;
-    d.row = __builtin_ctzll(next);
-    ++d.accepted;
-    if (lane == 0) path[d.accepted] = d.row;
+    uint64_t children = __ballot(parent == d.row);   // after their parent: the walk ends
+    double left = 1.0;
+    bool stands = false;
+    w.refusals = 0;
+    for (; children != 0; children &= children - 1) {
+      const int c = __builtin_ctzll(children), x = __builtin_amdgcn_readlane(token, c);
+      const bool again = __ballot(lane < w.refusals && w.refused == x) != 0;
+      const double p = again ? 0.0 : lane_value(mass, c);
+      stands = lane_value(u, c) * left < p;
+      if (stands) {
+        d.row = c;
+        ++d.accepted;
+        if (lane == 0) path[d.accepted] = c;
+        break;
+      }
+      left -= p;
+      if (lane == w.refusals) w.refused = x;
+      ++w.refusals;
+    }
+    if (!stands) break;
   }
-  const uint64_t tried = __ballot(parent == d.row);   // all refused
-  if (parent == d.row) refused[__builtin_popcountll(tried & ((1ull << lane) - 1))] = token;
-  if (lane == 0) *refusals = __builtin_popcountll(tried);
-  d.stopped = tried != 0;
+  d.stopped = w.refusals > 0;
   return d;
 }
 
@@ -194,78 +212,86 @@ struct Target {
 };
 
 __device__ __forceinline__ Target find_part(const Pair (&x)[4], double u) {
-  const int lane = threadIdx.x & 63;
-  double r[4], run[4];
-  double sum = wave_sum((x[0].rest + x[1].rest) + (x[2].rest + x[3].rest));
+  const double rest = (x[0].rest + x[1].rest) + (x[2].rest + x[3].rest);
+  const double whole = (x[0].whole + x[1].whole) + (x[2].whole + x[3].whole);
+  const double scan_rest = wave_scan(rest), scan_whole = wave_scan(whole);
   Target t;
-  t.plain = !(sum > 0.0);
+  t.plain = !(lane_value(scan_rest, 63) > 0.0);
+  const double mine = t.plain ? whole : rest, scan = t.plain ? scan_whole : scan_rest;
+  double r[4], run[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) r[j] = t.plain ? x[j].whole : x[j].rest;
-  const double mine = (r[0] + r[1]) + (r[2] + r[3]);
-  const double scan = wave_scan(mine);
   run[0] = (scan - mine) + r[0];
 #pragma unroll
   for (int j = 1; j < 4; ++j) run[j] = run[j - 1] + r[j];
   t.threshold = u * lane_value(scan, 63);
-  uint64_t past[4], any[4];
   int first = 4 * 64, top = -1;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    past[j] = __ballot(r[j] > 0.0 && run[j] > t.threshold);
-    any[j] = __ballot(r[j] > 0.0);
-    if (past[j] != 0) first = min(first, 4 * __builtin_ctzll(past[j]) + j);
-    if (any[j] != 0) top = max(top, 4 * (63 - __builtin_clzll(any[j])) + j);
+    const uint64_t past = __ballot(r[j] > 0.0 && run[j] > t.threshold), any = __ballot(r[j] > 0.0);
+    if (past != 0) first = min(first, 4 * __builtin_ctzll(past) + j);
+    if (any != 0) top = max(top, 4 * (63 - __builtin_clzll(any)) + j);
   }
   // rounding may leave no part past the threshold: then the last that has any weight
   t.part = first < 4 * 64 ? first : max(top, 0);
   const int at = t.part >> 2, j = t.part & 3;
-  const double upto = j == 0 ? run[0] - r[0] : j == 1 ? run[0] : j == 2 ? run[1] : run[2];
+  const double upto = j == 0 ? scan - mine : j == 1 ? run[0] : j == 2 ? run[1] : run[2];
   t.before = lane_value(upto, at);
   return t;
 }
 
-// The first index of the part whose running sum passes the threshold, by the workgroup: a
-// thread sums a few neighbours, and those that reach past it walk theirs.
+// The first index of the part whose running sum passes the threshold, by the workgroup, 16
+// neighbours a thread at a time; else (rounding took the threshold past the last sum) the last
+// index with any weight; -1 if none has. found, last: LDS, 0x7FFFFFFF and -1 on entry.
 template <bool DRAFT>
-__device__ __forceinline__ void walk(const Row& w, const Target& t, int lo, int hi, double* parts, int* found, int* last) {
-  const int tid = threadIdx.x, wave = tid >> 6;
-  const int each = ((hi - lo + kThreads - 1) / kThreads + 3) & ~3;   // a thread's neighbours
-  const int i0 = min(hi, lo + tid * each), i1 = min(hi, i0 + each);
-  const Pair s = sum_run<DRAFT>(w, i0, i1, 0, 4);
-  const double mine = t.plain ? s.whole : s.rest;
-  const double scan = wave_scan(mine);
-  if ((tid & 63) == 63) parts[wave] = scan;
-  __syncthreads();
+__device__ __forceinline__ int walk(const Row& w, const Target& t, int lo, int hi, double* parts, int* found, int* last) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint64_t some = refused_in(w, lo, hi);
   double before = t.before;
-  for (int x = 0; x < wave; ++x) before += parts[x];
-  if (mine > 0.0 && before + scan > t.threshold) {
-    double run = before + (scan - mine);
-    for (int i = i0; i < i1; ++i) {
-      const Pair x = weigh<DRAFT>(w, i, w.target[i], DRAFT ? w.draft[i] : 0.f);
-      const double v = t.plain ? x.whole : x.rest;
-      run += v;
-      if (v > 0.0 && run > t.threshold) {
-        atomicMin(found, i);
-        break;
+  for (int block = lo; block < hi; block += 16 * kThreads) {
+    const int i0 = block + 16 * tid;
+    float p[16], q[16];
+    load_run<DRAFT>(w, i0, 4, hi, p, q);
+    double v[16], mine = 0.0;
+    int top = -1;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const Pair x = weigh<DRAFT>(w, some, i0 + e, p[e], q[e]);
+      v[e] = t.plain ? x.whole : x.rest;
+      mine += v[e];
+      if (v[e] > 0.0) top = i0 + e;
+    }
+    const double scan = wave_scan(mine);
+    if (lane == 63) parts[wave] = scan;
+    __syncthreads();
+    double run = before, all = 0.0;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) {
+      if (x < wave) run += parts[x];
+      all += parts[x];
+    }
+    if (run + scan > t.threshold) {
+      run += scan - mine;
+      int hit = -1;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        run += v[e];
+        if (hit < 0 && v[e] > 0.0 && run > t.threshold) hit = i0 + e;
       }
+      if (hit >= 0) atomicMin(found, hit);
     }
+    if (before + all <= t.threshold || block + 16 * kThreads >= hi)
+      if (top >= 0) atomicMax(last, top);   // perhaps none passes it
+    __syncthreads();
+    if (*found != 0x7FFFFFFF) return *found;
+    before += all;
   }
-  __syncthreads();
-  if (*found != 0x7FFFFFFF || !(mine > 0.0)) return;
-  // rounding took the threshold past the last sum: the last index with any weight
-  for (int i = i1 - 1; i >= i0; --i) {
-    const Pair x = weigh<DRAFT>(w, i, w.target[i], DRAFT ? w.draft[i] : 0.f);
-    if ((t.plain ? x.whole : x.rest) > 0.0) {
-      atomicMax(last, i);
-      break;
-    }
-  }
+  return *last;
 }
 
 __global__ __launch_bounds__(kThreads) void verify_kernel(VerifyCall a, VerifySplit sp) {
   __shared__ double parts[2][kWaves];
-  __shared__ int refused[kMaxNodes], path[kMaxNodes];
-  __shared__ int refusals, found, last;
+  __shared__ int path[kMaxNodes], found, last;
   __shared__ uint32_t arrived;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t b = blockIdx.y;
@@ -276,25 +302,22 @@ __global__ __launch_bounds__(kThreads) void verify_kernel(VerifyCall a, VerifySp
   const double u0 = a.uniforms[b * a.nodes];
   int n;
   Decision d;
+  Row w{nullptr, nullptr, -1, 0};
   if (a.parents == nullptr) {
     d = decide_chain(a, b, n);
+    if (d.stopped) w.draft = a.draft + (b * (a.nodes - 1) + d.row) * a.vocab;
   } else {
-    d = decide_tree(a, b, n, refused, path, &refusals);   // every wave writes the same
-    __syncthreads();
+    d = decide_tree(a, b, n, path, w);   // every wave writes the same path
   }
-  Row w{a.target + (b * a.nodes + d.row) * a.vocab, nullptr, refused, 0};
-  if (a.parents != nullptr)
-    w.refusals = refusals;
-  else if (d.stopped)
-    w.draft = a.draft + (b * (a.nodes - 1) + d.row) * a.vocab;
+  w.target = a.target + (b * a.nodes + d.row) * a.vocab;
 
   // this wave's run of the row
   const int each = ((a.vocab + sp.chunks * kWaves - 1) / (sp.chunks * kWaves) + 3) & ~3;
   const int64_t lo64 = int64_t(int(blockIdx.x) * kWaves + wave) * each;
   int lo = int(lo64 < a.vocab ? lo64 : a.vocab), hi = min(a.vocab, lo + each);
-  Pair s = w.draft != nullptr ? sum_run<true>(w, lo, hi, 4 * lane, 256) : sum_run<false>(w, lo, hi, 4 * lane, 256);
-  s.rest = wave_sum(s.rest);
-  s.whole = wave_sum(s.whole);
+  Pair s = w.draft != nullptr ? sum_run<true>(w, lo, hi) : sum_run<false>(w, lo, hi);
+  s.rest = lane_value(wave_scan(s.rest), 63);
+  s.whole = lane_value(wave_scan(s.whole), 63);
   Pair x[4] = {};
   if (sp.chunks > 1) {
     __amdgpu_buffer_rsrc_t buf = coherent_buffer(sp.sums + b * kMaxParts * 2, kMaxParts * 16);
@@ -330,12 +353,8 @@ __global__ __launch_bounds__(kThreads) void verify_kernel(VerifyCall a, VerifySp
   const Target t = find_part(x, u0);
   lo = int(min(int64_t(a.vocab), int64_t(t.part) * each));
   hi = min(a.vocab, lo + each);
-  if (w.draft != nullptr)
-    walk<true>(w, t, lo, hi, parts[0], &found, &last);
-  else
-    walk<false>(w, t, lo, hi, parts[0], &found, &last);
-  __syncthreads();
-  const int token = found != 0x7FFFFFFF ? found : last;
+  const int token = w.draft != nullptr ? walk<true>(w, t, lo, hi, parts[0], &found, &last)
+                                       : walk<false>(w, t, lo, hi, parts[0], &found, &last);
   if (tid == 0) a.accepted[b] = d.accepted;
   if (tid < a.nodes) {
     int32_t* out = a.out_tokens + b * a.nodes;
@@ -345,7 +364,8 @@ __global__ __launch_bounds__(kThreads) void verify_kernel(VerifyCall a, VerifySp
   }
 }
 
-// Chunks of a row: enough workgroups to fill the GPU twice over.
+// Chunks of a row: two workgroups a CU. (64 rows of 128256, us at 1, 2, 4, 8 a CU: 25.2, 21.4,
+// 23.6, 31.4: each makes the decisions for itself.)
 int chunks_of(int64_t batch, int64_t vocab, const DeviceInfo& dev) {
   if (batch > NM_DECODE_COUNTER_BYTES / 4) return 1;
   int64_t c = 2 * int64_t(dev.cu_count) / batch;
