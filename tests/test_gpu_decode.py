@@ -740,3 +740,69 @@ def test_calls_run_on_the_current_stream():
     torch.cuda.current_stream().wait_stream(s)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------------------ more ranges
+@pytest.mark.parametrize("form", list(FORMATS))
+def test_attend_uneven_batches(form):
+    """One long sequence among short and empty ones, an odd number of key heads, and one key head
+    alone over a long context (more chunks than a join takes): the chunks' search and caps."""
+    rng = np.random.default_rng(86)
+    context = [0, 9000] + rng.integers(0, 70, 40).tolist()
+    p = Paged(rng, 42, -(-9004 // 64), 64, 3, 64, form)
+    attend_case(rng, p, context, 2, 6, tag="one long")
+    p = Paged(rng, 1, -(-40009 // 128), 128, 1, 128, form)
+    attend_case(rng, p, [40000], 1, 1, tag="one head")
+    attend_case(rng, p, [39990], 9, 16, tag="one head, 144 rows")
+
+
+@pytest.mark.parametrize("form", ["int8", "fp16"])
+def test_cache_beyond_four_gigabytes(form):
+    """Offsets past 32 bits: the same tokens in the last blocks of a cache of more than 4 GiB a
+    side and in the first blocks give the same bits."""
+    rng = np.random.default_rng(87)
+    kv, page, dim = 8, 64, 128
+    blocks = 2 ** 32 // (kv * page * dim * (1 if form == "int8" else 2)) + 40
+    c = nm.kv_cache(blocks, page, kv, dim, FORMATS[form], device=device())
+    k, v = up(halves(rng, 2, 300, kv, dim)), up(halves(rng, 2, 300, kv, dim))
+    q = up(halves(rng, 2, 4, 32, dim))
+    results = []
+    for first in (0, blocks - 12):
+        table = i32(first + rng.permutation(12).reshape(2, 6))
+        nm.nm_kv_append(c, k, v, table, i32([7, 0]))
+        read = nm.nm_kv_read(c, table, i32([7, 0]), 300)
+        out = nm.nm_tree_attention(q, c, table, i32([300, 296]), workspace=nm.tree_attention_workspace(q, c, table))
+        results.append((*read, out[1:]))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert results[0][0].float().abs().sum() > 0
+
+
+def test_verify_with_a_small_workspace_runs_unsplit():
+    rng = np.random.default_rng(88)
+    target, draft, tokens, u = chain_case(rng, 3, 4, 20000)
+    want = nm.nm_verify_chain(up(target), up(draft), i32(tokens), up(u))
+    got = nm.nm_verify_chain(up(target), up(draft), i32(tokens), up(u),
+                             workspace=torch.zeros(70000, dtype=torch.uint8, device=device()))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_verify_rows_of_large_vocabularies_end_anywhere():
+    """Thresholds in the first and last elements of every workgroup's run."""
+    rng = np.random.default_rng(89)
+    vocab = 50021
+    target = np.zeros((64, 1, vocab), np.float32)
+    at = np.unique(np.concatenate([[0, vocab - 1], rng.integers(0, vocab, 61), [1024]]))[:64]
+    for b in range(64):
+        target[b, 0, at[b % len(at)]] = 0.25 + b
+    check_chain(target, np.zeros((64, 0, vocab), np.float32), np.zeros((64, 1), np.int32),
+                rng.random((64, 1)).astype(np.float32))
+
+
+@pytest.mark.parametrize("form", list(FORMATS))
+def test_example_gives_the_same_text(form):
+    """Decoding with draft trees gives the text of plain decoding, in fewer steps."""
+    from examples import speculative_decode as ex
+    plain, tree, steps = ex.main(["--tokens", "64", "--format", form])
+    assert plain == tree
+    assert steps < 64
