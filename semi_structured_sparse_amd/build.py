@@ -1,4 +1,5 @@
-"""Build libnmsparse.so in place with hipcc for gfx950.
+"""Build libnmsparse.so in place with hipcc for gfx950, and _nmtorch.so, the quick way from torch
+tensors to its decoding calls, with the host compiler.
 
 Usage: ``python -m semi_structured_sparse_amd.build`` (or call ``build()``).
 """
@@ -9,12 +10,14 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libnmsparse.so"
+EXT_NAME = "_nmtorch.so"
 ARCH = os.environ.get("NM_OFFLOAD_ARCH", "gfx950")
 
 HIP_FLAGS = [
@@ -40,7 +43,48 @@ def sources() -> list:
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
 
 
+def extension_command(out: str) -> list:
+    """The host compiler's command for csrc/nm_torch.cpp, against the installed torch."""
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(base, "include"), os.path.join(base, "lib")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DUSE_ROCM",
+            "-D__HIP_PLATFORM_AMD__", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f"-I{INCLUDE}", "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(rocm, "include"), "-isystem", sysconfig.get_paths()["include"],
+            os.path.join(CSRC, "nm_torch.cpp"), "-o", out, f"-L{lib}", "-lc10", "-lc10_hip", "-ltorch_cpu",
+            "-ltorch_python", f"-Wl,-rpath,{lib}"]
+
+
+def build_extension(verbose: bool = False) -> str:
+    """Compile csrc/nm_torch.cpp into PKG_DIR/_nmtorch.so (always recompiles)."""
+    out = os.path.join(PKG_DIR, EXT_NAME)
+    tmp = out + ".tmp"
+    cmd = extension_command(tmp)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 def build(verbose: bool = False) -> str:
+    """Compile every HIP source into PKG_DIR/libnmsparse.so, and the torch extension beside it
+    (always recompiles)."""
+    with ThreadPoolExecutor(1) as pool:      # the extension while hipcc works
+        extension = pool.submit(build_extension, verbose)
+        out = build_library(verbose)
+        extension.result()
+    return out
+
+
+def build_library(verbose: bool = False) -> str:
     """Compile every HIP source into PKG_DIR/libnmsparse.so (always recompiles)."""
     out = os.path.join(PKG_DIR, LIB_NAME)
     tmp = out + ".tmp"

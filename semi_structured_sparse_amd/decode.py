@@ -2,7 +2,9 @@
 speculative decoding step. Rotary positions, a paged key/value cache in fp16, int8 or e4m3,
 the attention of drafted trees, chains or single tokens over it, and the verification of the
 drafts. Argument marshalling only, as in the rest of the package; every step runs in the HIP
-kernels of libnmsparse.so.
+kernels of libnmsparse.so. A call goes through _nmtorch.so (csrc/nm_torch.cpp), which does the
+same in a fifth of the time; what that does not take (a refusal, tensors of a device that is not
+the current one) goes through the checks here, which raise or make the call.
 """
 from __future__ import annotations
 
@@ -129,6 +131,8 @@ def _cache_arg(cache, device):
     import torch
     k, v, k_scale, v_scale = cache
     form = _formats().get(k.dtype)
+    if not form:
+        k_scale = v_scale = None
     if form is None:
         raise ValueError(f"a cache is fp16, int8 or float8_e4m3fn, not {k.dtype}")
     if k.dim() != 4:
@@ -154,6 +158,19 @@ def _paging(table, first, first_name, count, batch, device):
 
 
 _functions = {}   # of the loaded library, by name
+_quick = None     # _nmtorch, bound to that library on the first call
+_QUICK = ("nm_rope", "nm_kv_append", "nm_rope_kv_append", "nm_kv_read", "nm_kv_compact", "nm_tree_attention",
+          "nm_verify_chain", "nm_verify_tree")
+
+
+def _bound():
+    global _quick
+    if _quick is None:
+        from . import _nmtorch
+        lib = _nm().lib()
+        _nmtorch.bind(*(_c.cast(getattr(lib, name), _c.c_void_p).value for name in _QUICK))
+        _quick = _nmtorch
+    return _quick
 
 
 def _run(name, device, *args):
@@ -204,6 +221,9 @@ def nm_rope(x, positions, turns, layout: str = "half", scale: float = 1.0, out=N
     """Rotary positions on x fp16 [tokens, heads, head_dim] (a slice of a fused projection's
     output will do): the first 2 * len(turns) elements of each head turned by positions int32
     [tokens], the rest copied. out: fp16 of x's shape, x itself included; made if not given."""
+    done = (_quick or _bound()).nm_rope(x, positions, turns, LAYOUTS.get(layout, -1), scale, out)
+    if done is not NotImplemented:
+        return done
     import torch
     device = _device_of(x, "x")
     xp, xs = _rows(x, "x", 3, device)
@@ -223,6 +243,9 @@ def nm_kv_append(cache: KVCache, k, v, block_table, start, count=None) -> None:
     """Writes k, v fp16 [batch, tokens, kv_heads, head_dim] into the cache at positions
     start[b] + t of sequences whose pages block_table int32 [batch, pages] lists, for t below
     count[b] (int32, None: all)."""
+    done = (_quick or _bound()).nm_kv_append(*cache, k, v, block_table, start, count)
+    if done is not NotImplemented:
+        return done
     device = _device_of(k, "k")
     c = _cache_arg(cache, device)
     kp, ks = _rows(k, "k", 4, device)
@@ -239,6 +262,10 @@ def nm_rope_kv_append(cache: KVCache, q, k, v, positions, turns, block_table, st
     """nm_rope on q and k and nm_kv_append in one launch: returns q turned, fp16 [batch, tokens,
     heads, head_dim] (zeros for tokens at or past count; out may be q). positions int32 [batch,
     tokens]. q None: k and v only, returns None."""
+    done = (_quick or _bound()).nm_rope_kv_append(*cache, q, k, v, positions, turns, block_table, start, count,
+                                                  LAYOUTS.get(layout, -1), scale, out)
+    if done is not NotImplemented:
+        return done
     import torch
     device = _device_of(k, "k")
     c = _cache_arg(cache, device)
@@ -269,6 +296,9 @@ def nm_rope_kv_append(cache: KVCache, q, k, v, positions, turns, block_table, st
 def nm_kv_read(cache: KVCache, block_table, start, tokens: int, count=None, out=None):
     """(k, v) fp16 [batch, tokens, kv_heads, head_dim]: the values at positions start[b] + t, zeros
     for t at or past count[b]. out: a pair of such tensors."""
+    done = (_quick or _bound()).nm_kv_read(*cache, block_table, start, tokens, count, *((None, None) if out is None else out))
+    if done is not NotImplemented:
+        return done
     import torch
     device = _device_of(block_table, "block_table")
     c = _cache_arg(cache, device)
@@ -285,6 +315,9 @@ def nm_kv_read(cache: KVCache, block_table, start, tokens: int, count=None, out=
 def nm_kv_compact(cache: KVCache, block_table, start, path, accepted) -> None:
     """Moves the rows at start[b] + path[b, d] to start[b] + d for 1 <= d <= accepted[b]: path
     int32 [batch, nodes] and accepted int32 [batch] as nm_verify_tree returns them."""
+    done = (_quick or _bound()).nm_kv_compact(*cache, block_table, start, path, accepted)
+    if done is not NotImplemented:
+        return done
     import torch
     device = _device_of(block_table, "block_table")
     c = _cache_arg(cache, device)
@@ -321,6 +354,9 @@ def nm_tree_attention(q, cache: KVCache, block_table, context, mask=None, count=
     allows by bits (None: a chain). count int32 [batch]: nodes of each sequence. scale: 1/sqrt of
     head_dim if None. workspace: from tree_attention_workspace, or None (long contexts are then
     not split over the GPU)."""
+    done = (_quick or _bound()).nm_tree_attention(q, *cache, block_table, context, mask, count, scale, workspace, out)
+    if done is not NotImplemented:
+        return done
     import torch
     device = _device_of(q, "q")
     c = _cache_arg(cache, device)
@@ -366,6 +402,9 @@ def nm_verify_chain(target, draft, tokens, uniforms, count=None, workspace=None)
     """Rejection sampling of a drafted chain: target fp32 [batch, nodes, vocab], draft fp32 [batch,
     nodes-1, vocab], tokens int32 and uniforms fp32 [batch, nodes]. Returns (accepted int32 [batch],
     out_tokens int32 [batch, nodes]: the accepted drafts, the token drawn after them, then -1)."""
+    done = (_quick or _bound()).nm_verify_chain(target, draft, tokens, uniforms, count, workspace)
+    if done is not NotImplemented:
+        return done
     import torch
     device, tp, (kp, up, np_), (accepted, out), rest = _verify_args(target, tokens, uniforms, count, workspace)
     batch, nodes, vocab = target.shape
@@ -378,6 +417,9 @@ def nm_verify_tree(target, tokens, parents, uniforms, count=None, workspace=None
     """Verification of a tree of chosen tokens: parents int32 [batch, nodes], the rest as
     nm_verify_chain. Returns (accepted, out_tokens, path int32 [batch, nodes]: the nodes reached,
     from node 0 on, then -1)."""
+    done = (_quick or _bound()).nm_verify_tree(target, parents, tokens, uniforms, count, workspace)
+    if done is not NotImplemented:
+        return done
     import torch
     device, tp, (kp, up, np_), (accepted, out), rest = _verify_args(target, tokens, uniforms, count, workspace)
     batch, nodes, _ = target.shape
