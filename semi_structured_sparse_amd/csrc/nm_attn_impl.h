@@ -632,8 +632,11 @@ struct AttnWave {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float y = exp2_fast(x[n][e] - m[n]);
-        l[n] = FMT == NM_KV_FP16 ? l[n] + y : fmaf(y, t.iz[e], l[n]);
+        // fp16: the sum is of the weights as rounded, so that a weighted mean of equal values is
+        // exact; with 8-bit codes, whose own rounding is coarser, that took 4% longer at 64 nodes
+        if constexpr (FMT != NM_KV_FP16) l[n] = fmaf(y, t.iz[e], l[n]);
         w[n][e] = _Float16(y);   // to nearest even: 2^-11 of the weight
+        if constexpr (FMT == NM_KV_FP16) l[n] += float(w[n][e]);
       }
       if constexpr (FMT == NM_KV_INT8) {
         const f16x2 ones = {_Float16(1.0f), _Float16(1.0f)};
