@@ -109,8 +109,9 @@ int nm_rope(const uint16_t* x, uint16_t* y, const int32_t* positions, const doub
  * Tokens whose position is outside 0 .. table_width * page - 1 or whose table entry is outside
  * 0 .. blocks - 1 are skipped (an entry of -1 is the usual filler). Two tokens of one call must
  * not share a slot. NM_ERR_SHAPE: batch outside 1 .. 65535, tokens outside 1 .. 2^24, batch * tokens
- * above 2^30, batch * tokens times the call's heads above 2^31 - 1, table_width outside 1 .. 2^24 or table_width * page above 2^30, kv_heads outside
- * 1 .. 4096, blocks outside 1 .. 2^31 - 1, a stride below the heads' size or above 2^40. */
+ * above 2^30, the call's q, k and v together (k alone, where it reads) above 2^35 elements,
+ * table_width outside 1 .. 2^24 or table_width * page above 2^30, kv_heads outside 1 .. 4096,
+ * blocks outside 1 .. 2^31 - 1, a stride below the heads' size or above 2^40. */
 int nm_kv_append(const nm_kv_cache* cache, const uint16_t* k, const uint16_t* v, int64_t k_stride,
                  int64_t v_stride, const int32_t* table, int64_t table_width, const int32_t* start,
                  const int32_t* count, int64_t batch, int64_t tokens, void* stream);
@@ -138,8 +139,9 @@ int nm_kv_read(const nm_kv_cache* cache, uint16_t* k_out, uint16_t* v_out, const
 /* Moves an accepted tree path's rows together: for 1 <= d <= accepted[b], position
  * start[b] + d gets the k, v and scales of position start[b] + path[b][d], all read before
  * any is written. path  int32 [batch][nodes] and accepted  int32 [batch], as nm_verify_tree
- * gives them (accepted is clamped to 0 .. nodes - 1). Entries outside 0 .. nodes - 1 and positions that
- * nm_kv_append would skip are left alone. nodes 1 .. 64; other limits as nm_kv_append. */
+ * gives them (accepted is clamped to 0 .. nodes - 1). Entries outside 0 .. nodes - 1 and
+ * positions that nm_kv_append would skip are left alone. nodes 1 .. 64; other limits as
+ * nm_kv_append. */
 int nm_kv_compact(const nm_kv_cache* cache, const int32_t* table, int64_t table_width, const int32_t* start,
                   const int32_t* path, const int32_t* accepted, int64_t batch, int64_t nodes, void* stream);
 
@@ -149,10 +151,10 @@ int nm_kv_compact(const nm_kv_cache* cache, const int32_t* table, int64_t table_
  * where bit i of mask[b][t] is set and i < count[b] (mask NULL: a chain, node t sees nodes
  * 0 .. t). Query head h reads key head h / (heads / kv_heads). A node that sees no key, and
  * nodes at or past count, get zeros. Keys that a node does not see do not touch its result,
- * whatever they hold (NaN and infinities too). A draft whose v row has an infinity or
- * NaN in it makes the results of the nodes that see it NaN. fp16 products of exact codes, fp32 sums; the
- * weights times v's scale are rounded to fp16 (relative 2^-11) for the second product. Bit-identical from run
- * to run for the same lengths and workspace.
+ * whatever they hold (NaN and infinities too). A draft whose v row has an infinity or NaN in
+ * it makes the results of the nodes that see it NaN. fp16 products of exact codes, fp32 sums;
+ * the weights times v's scale are rounded to fp16 (relative 2^-11) for the second product.
+ * Bit-identical from run to run for the same arguments, lengths and size of workspace.
  *   q     fp16, token (b, t)'s head h at [(b * tokens + t) * q_stride + h * head_dim]; 16-byte
  *         aligned, q_stride a multiple of 8;  out  fp16 [batch][tokens][heads][head_dim], 16-byte
  *         aligned
@@ -165,7 +167,8 @@ int nm_kv_compact(const nm_kv_cache* cache, const int32_t* table, int64_t table_
  * nm_tree_attention and nm_verify calls in stream order. Fewer bytes than
  * nm_tree_attention_workspace_bytes run as NULL does. Calls that overlap on one workspace
  * race. NM_ERR_SHAPE: tokens outside 1 .. 64, heads not a multiple of kv_heads or above 16
- * times kv_heads or 65536, batch outside 1 .. 65535, a scale that is not finite, others as nm_kv_append. */
+ * times kv_heads or 65536, batch outside 1 .. 65535, batch * kv_heads above 2^23, a scale that
+ * is not finite, others as nm_kv_append. */
 #define NM_DECODE_COUNTER_BYTES 65536u
 int nm_tree_attention(const nm_kv_cache* cache, const uint16_t* q, uint16_t* out, int64_t heads,
                       int64_t q_stride, const int32_t* table, int64_t table_width, const int32_t* context,

@@ -92,7 +92,6 @@ hipError_t launch_attention(const AttnCall& c, int head_dim, int format, void* w
   // Row tiles of one chunk read the same keys: a grid width that is a multiple of the 8 XCDs
   // puts them on one XCD's L2.
   const int64_t wide = (int64_t(p.slots ? p.slots : c.batch) * c.cache.kv_heads + 7) / 8 * 8;
-  if (wide > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   const Kernel k = kernel_of(format, head_dim, p.nr);
   return launch(k.f, dim3(uint32_t(wide), uint32_t(p.row_tiles)), dim3(kAttnThreads), args, size_t(k.lds), stream, dev);
 }

@@ -9,7 +9,9 @@ namespace nm {
 namespace {
 
 constexpr int64_t kMaxStride = int64_t(1) << 40;
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;   // (token, head) rows of a cache call
+// Elements of a cache call, 16 a thread: a grid has fewer than 2^32 threads across.
+constexpr int64_t kMaxElements = int64_t(1) << 35;
+constexpr int64_t kMaxAttnHeads = int64_t(1) << 23;   // key heads of an attention call's sequences, likewise
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -72,7 +74,7 @@ int append(const nm_kv_cache* cache, const uint16_t* q, uint16_t* q_out, int64_t
   if (!stride_ok(k_stride, row) || !stride_ok(v_stride, row)) return NM_ERR_SHAPE;
   if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 != 0 || v_stride % 8 != 0) return NM_ERR_ALIGN;
   if (!aligned(start, 4) || !aligned(count, 4)) return NM_ERR_ALIGN;
-  if (batch * tokens * (q_heads + 2 * cache->kv_heads) > kMaxRows) return NM_ERR_SHAPE;
+  if (batch * tokens * (q_heads + 2 * cache->kv_heads) > kMaxElements / cache->head_dim) return NM_ERR_SHAPE;
   if (q_heads > 0) {
     if (!q || !q_out) return NM_ERR_NULL;
     if (!stride_ok(q_stride, q_heads * cache->head_dim) || !stride_ok(q_out_stride, q_heads * cache->head_dim))
@@ -91,7 +93,8 @@ int attention_check(const nm_kv_cache* cache, int64_t heads, const int32_t* tabl
                     int64_t tokens) {
   const int st = cache_check(cache, table, table_width, batch, tokens);
   if (st != NM_OK) return st;
-  if (tokens > kMaxNodes || !within(heads, 1, 65536) || heads % cache->kv_heads != 0 || heads / cache->kv_heads > 16)
+  if (tokens > kMaxNodes || !within(heads, 1, 65536) || heads % cache->kv_heads != 0 || heads / cache->kv_heads > 16 ||
+      batch * cache->kv_heads > kMaxAttnHeads)
     return NM_ERR_SHAPE;
   return NM_OK;
 }
@@ -181,7 +184,7 @@ int nm_kv_read(const nm_kv_cache* cache, uint16_t* k_out, uint16_t* v_out, const
   const int st = cache_check(cache, table, table_width, batch, tokens);
   if (st != NM_OK) return st;
   if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(start, 4) || !aligned(count, 4)) return NM_ERR_ALIGN;
-  if (batch * tokens * cache->kv_heads > kMaxRows) return NM_ERR_SHAPE;
+  if (batch * tokens * cache->kv_heads > kMaxElements / cache->head_dim) return NM_ERR_SHAPE;
   DeviceInfo dev;
   const hipError_t e = current_device_info(&dev);
   if (e != hipSuccess) return finish(e);

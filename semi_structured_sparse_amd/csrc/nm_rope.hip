@@ -1,4 +1,5 @@
 // Rotary positions (nm_rope) and the host table of their frequencies (nm_rope_turns).
+#include <algorithm>
 #include <cmath>
 
 #include "nm_decode_internal.h"
@@ -7,6 +8,7 @@ namespace nm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kGridThreads = int64_t(1) << 31;
 
 // Any head size, stride and alignment: one pair (or, past the rotated part, two elements) per
 // thread.
@@ -66,6 +68,21 @@ __global__ __launch_bounds__(kThreads) void rope_wide_kernel(RopeCall a, int uni
   }
 }
 
+// Launches `most` tokens at a time: a grid has fewer than 2^32 threads across.
+template <class F>
+hipError_t by_tokens(RopeCall& a, int64_t most, F&& launch_some) {
+  const RopeCall all = a;
+  for (int64_t t = 0; t < all.tokens; t += most) {
+    a.tokens = std::min(most, all.tokens - t);
+    a.x = all.x + t * all.x_stride;
+    a.y = all.y + t * all.y_stride;
+    a.rope.positions = all.rope.positions + t;
+    const hipError_t e = launch_some();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
@@ -84,14 +101,17 @@ hipError_t launch_rope(const RopeCall& c, hipStream_t stream, const DeviceInfo& 
     if (split < (passes + kPasses - 1) / kPasses) split = (passes + kPasses - 1) / kPasses;
     int each = (passes + split - 1) / split * step;
     void* args[] = {&a, &units, &step, &each};
-    return launch(reinterpret_cast<const void*>(rope_wide_kernel), dim3(uint32_t(c.tokens), (c.heads + each - 1) / each),
-                  dim3(kThreads), args, 0, stream, dev);
+    return by_tokens(a, kGridThreads / kThreads, [&] {
+      return launch(reinterpret_cast<const void*>(rope_wide_kernel),
+                    dim3(uint32_t(a.tokens), (c.heads + each - 1) / each), dim3(kThreads), args, 0, stream, dev);
+    });
   }
-  const int64_t n = c.tokens * c.heads * ((c.head_dim + 1) / 2);
-  const int64_t grid = (n + kThreads - 1) / kThreads;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const int64_t per_token = c.heads * int64_t((c.head_dim + 1) / 2);
   void* args[] = {&a};
-  return launch(reinterpret_cast<const void*>(rope_kernel), dim3(uint32_t(grid)), dim3(kThreads), args, 0, stream, dev);
+  return by_tokens(a, kGridThreads / per_token, [&] {
+    return launch(reinterpret_cast<const void*>(rope_kernel), dim3(uint32_t((a.tokens * per_token + kThreads - 1) / kThreads)),
+                  dim3(kThreads), args, 0, stream, dev);
+  });
 }
 
 }  // namespace nm

@@ -294,3 +294,14 @@ def test_oracle_tree_keeps_the_target_distribution():
         _, out, _ = ref.verify_tree_ref(target, [0, 1, 1, 3], [-1, 0, 0, 0], u, 4)
         got[out[0]] += 1 / 20000
     assert np.allclose(got, target[0], atol=0.02)
+
+
+@pytest.mark.parametrize("name,base,kw", [
+    ("nm_kv_append", "APPEND", dict(batch=1 << 6, tokens=1 << 24, cache_kv_heads=32, k_stride=32 * 128, v_stride=32 * 128)),
+    ("nm_rope_kv_append", "ROPE_APPEND", dict(batch=1 << 6, tokens=1 << 22, q_heads=1024, q_stride=1 << 17, q_out_stride=1 << 17)),
+    ("nm_kv_read", "READ", dict(batch=1 << 6, tokens=1 << 24, cache_kv_heads=32)),
+    ("nm_tree_attention", "ATTEND", dict(batch=4096, cache_kv_heads=4096, heads=4096, q_stride=4096 * 128)),
+])
+def test_calls_past_a_grid_are_refused(name, base, kw):
+    """One grid has fewer than 2^32 threads across; nm_rope takes several, these calls refuse."""
+    assert _call(name, globals()[base], kw) == nm.NM_ERR_SHAPE

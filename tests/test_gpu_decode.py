@@ -806,3 +806,105 @@ def test_example_gives_the_same_text(form):
     plain, tree, steps = ex.main(["--tokens", "64", "--format", form])
     assert plain == tree
     assert steps < 64
+
+
+class _Refuses:
+    """Stands for the quick way and takes nothing, so that decode.py's own checks make the call."""
+
+    def __getattr__(self, name):
+        return lambda *args: NotImplemented
+
+
+class _Counts:
+    """The quick way, counting the calls that it took."""
+
+    def __init__(self, inner):
+        self.inner, self.took, self.left = inner, [], []
+
+    def __getattr__(self, name):
+        def call(*args):
+            done = getattr(self.inner, name)(*args)
+            (self.left if done is NotImplemented else self.took).append(name)
+            return done
+        return call
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", [torch.float16, torch.int8, torch.float8_e4m3fn])
+def test_both_ways_to_the_library(form, monkeypatch):
+    from semi_structured_sparse_amd import decode
+
+    def calls():
+        g = torch.Generator().manual_seed(7)
+        dev = torch.device("cuda")
+        batch, nodes, heads, kv, dim, vocab = 2, 5, 4, 2, 64, 1001
+        cache = nm.kv_cache(12, 16, kv, dim, dtype=form)
+        table = torch.arange(12, dtype=torch.int32, device=dev).view(batch, 6).contiguous()
+        start = torch.tensor([30, 7], dtype=torch.int32, device=dev)
+        count = torch.tensor([5, 3], dtype=torch.int32, device=dev)
+        fused = torch.randn(batch, nodes, (heads + 2 * kv) * dim, generator=g).half().to(dev)
+        q = fused[..., : heads * dim].unflatten(-1, (heads, dim))
+        k = fused[..., heads * dim: (heads + kv) * dim].unflatten(-1, (kv, dim))
+        v = fused[..., (heads + kv) * dim:].unflatten(-1, (kv, dim))
+        turns = nm.rope_turns(dim, device=dev)
+        pos = start[:, None] + torch.arange(nodes, dtype=torch.int32, device=dev)
+        made = [nm.nm_rope(q.reshape(-1, heads, dim), pos.reshape(-1).contiguous(), turns)]
+        past = torch.randn(batch, 30, kv, dim, generator=g).half().to(dev)
+        nm.nm_kv_append(cache, past, past, table, torch.zeros_like(start))
+        turned = nm.nm_rope_kv_append(cache, q, k, v, pos, turns, table, start, count, layout="interleaved")
+        assert nm.nm_rope_kv_append(cache, None, k, v, pos, turns, table, start, count, layout="interleaved") is None
+        mask = torch.tensor([[1, 3, 5, 11, 21]] * batch, dtype=torch.int64, device=dev)
+        work = nm.tree_attention_workspace(turned, cache, table)
+        made += [turned, nm.nm_tree_attention(turned, cache, table, start, mask, count, workspace=work)]
+        p = torch.rand(batch, nodes, vocab, generator=g).to(dev)
+        p /= p.sum(-1, keepdim=True)
+        tokens = torch.randint(0, vocab, (batch, nodes), generator=g).int().to(dev)
+        u = torch.rand(batch, nodes, generator=g).to(dev)
+        parents = torch.tensor([[-1, 0, 0, 1, 2]] * batch, dtype=torch.int32, device=dev)
+        ws = nm.verify_workspace(batch, vocab)
+        made += nm.nm_verify_chain(p, p[:, 1:].contiguous(), tokens, u, count, ws)
+        made += nm.nm_verify_tree(p, tokens, parents, u, count, ws)
+        path = torch.tensor([[0, 2, 4, -1, -1]] * batch, dtype=torch.int32, device=dev)
+        nm.nm_kv_compact(cache, table, start, path, torch.tensor([2, 1], dtype=torch.int32, device=dev))
+        made += nm.nm_kv_read(cache, table, torch.zeros_like(start), 40, start + 5)
+        return made
+
+    counts = _Counts(decode._bound())
+    monkeypatch.setattr(decode, "_quick", counts)
+    quick = calls()
+    assert not counts.left and set(counts.took) == set(decode._QUICK)
+    monkeypatch.setattr(decode, "_quick", _Refuses())
+    for a, b in zip(quick, calls(), strict=True):
+        assert a.dtype == b.dtype and a.shape == b.shape and a.stride() == b.stride()
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dim", [16, 2])
+def test_rope_of_more_tokens_than_a_grid(dim):
+    """2^23 tokens and more in wide rows take a second grid (the narrow form's limit is further
+    off); tokens around the border and at both ends are checked."""
+    tokens = 2 ** 23 + 5
+    x = torch.arange(tokens * dim, dtype=torch.int32, device=device()).remainder_(1013).half().view(tokens, 1, dim)
+    pos = torch.arange(tokens, dtype=torch.int32, device=device())
+    turns = ref.rope_turns_ref(dim)
+    got = nm.nm_rope(x, pos, up(turns))
+    for at in (0, 2 ** 23 - 4, tokens - 4):
+        part = slice(at, at + 4)
+        want, size = ref.rope_ref(x[part].cpu().numpy(), pos[part].cpu().numpy(), turns)
+        close(got[part], want, HALF * np.abs(want) + 2.0 ** -18 * size + TINY, f"from {at}")
+
+
+@pytest.mark.parametrize("context", [0, 5, 700, 9000])
+def test_attend_equal_values_are_exact(context):
+    """In an fp16 cache the weights' sum is of the weights as they multiply v: where all v are
+    3, so is the result, but for fp32 sums ((keys + 8) 2^-24 each) and the last rounding."""
+    rng = np.random.default_rng(context)
+    cache = nm.kv_cache(160, 64, 2, 128)
+    cache.k.copy_(up(halves(rng, 160, 2, 64, 128)))
+    cache.v.fill_(3.0)
+    table = i32(np.arange(160)[None])
+    q = up(halves(rng, 1, 3, 8, 128))
+    for work in (None, nm.tree_attention_workspace(q, cache, table)):
+        got = nm.nm_tree_attention(q, cache, table, i32([context]), workspace=work)
+        want = np.full(got.shape, 3.0)
+        close(got, want, 3.0 * (HALF + 2 * (context + 8) * 2.0 ** -24) + 0 * want, f"{context}")
