@@ -11,7 +11,10 @@
 // e.g. 64 x 128256 x 8 bytes. A single workgroup reads a row at the rate of one CU, so a row
 // goes to several: each sums a chunk, the last to arrive finds the run of it that the threshold
 // falls in and walks that one alone. The decisions cost a chain of dependent loads (tokens,
-// probabilities), so every workgroup makes them for itself rather than wait for another.
+// probabilities), so every workgroup makes them for itself rather than wait for another. Measured:
+// 64 chains of 8, vocabulary 128256 (66 MB) 16.1 us, 4.1 TB/s; 16 trees of 32, 151936 9.1 us; 8
+// chains of 5, 32000 6.8 us, most of it the chain of loads (decisions about 2, a run 1.5, the sums'
+// hand-off 2, the walk 1).
 #include "nm_decode_internal.h"
 
 namespace nm {
@@ -23,10 +26,11 @@ constexpr int kMaxChunks = 64;                     // workgroups of a row
 constexpr int kMaxParts = kMaxChunks * kWaves;     // its waves' runs: four a lane of the joining wave
 constexpr int kMinChunk = 1024;                    // elements: one load of 16 bytes a lane
 
-// Where a row's waves leave the sums of their runs: {with the draft (or the refused tokens)
-// taken off, the target alone} for every sequence and run.
+// Where a row's waves leave the sums of their runs, and each sequence's counter: apart, since
+// additions to one line wait for each other.
 struct VerifySplit {
   int chunks;
+  int counter_step;
   uint32_t* counters;
   double* sums;
 };
@@ -43,25 +47,24 @@ typedef float quad __attribute__((ext_vector_type(4), aligned(4)));   // rows st
 // Positive and finite, else zero.
 __device__ __forceinline__ double kept(double x) { return x > 0.0 && x < __builtin_inf() ? x : 0.0; }
 
-struct Pair {
-  double rest, whole;      // weights with what is taken off, and of the target alone
-};
-
 // The refused tokens (lanes, a bit each) in [lo, hi): mostly none.
 __device__ __forceinline__ uint64_t refused_in(const Row& w, int lo, int hi) {
   return __ballot(int(threadIdx.x & 63) < w.refusals && w.refused >= lo && w.refused < hi);
 }
 
-// The weights of element i, exact (or rounded once) in 64 bits. some: refused tokens to look for.
-template <bool DRAFT>
-__device__ __forceinline__ Pair weigh(const Row& w, uint64_t some, int i, float p, float q) {
-  Pair x;
-  x.whole = kept(double(p));
-  x.rest = DRAFT ? kept(double(p) - double(q)) : x.whole;
-  if (!DRAFT)
-    for (uint64_t m = some; m != 0; m &= m - 1)
-      if (__builtin_amdgcn_readlane(w.refused, __builtin_ctzll(m)) == i) x.rest = 0.0;
-  return x;
+// The weights of N elements in groups of four from i on, `step` apart, exact (or rounded once) in
+// 64 bits. some: refused tokens to look for.
+template <bool DRAFT, int N>
+__device__ __forceinline__ void weigh(const Row& w, uint64_t some, int i, int step, const float (&p)[N], const float (&q)[N],
+                                      double (&v)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = kept(DRAFT ? double(p[e]) - double(q[e]) : double(p[e]));
+  for (uint64_t m = some; m != 0; m &= m - 1) {
+    const int x = __builtin_amdgcn_readlane(w.refused, __builtin_ctzll(m)) - i;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (x == e / 4 * step + e % 4) v[e] = 0.0;
+  }
 }
 
 // N elements from i on (zeros at and past hi) in groups of four, `step` apart.
@@ -90,25 +93,6 @@ __device__ __forceinline__ void load_run(const Row& w, int i, int step, int hi, 
   }
 }
 
-// The sums of a wave's run [lo, hi), of this lane's elements.
-template <bool DRAFT>
-__device__ __forceinline__ Pair sum_run(const Row& w, int lo, int hi) {
-  const uint64_t some = refused_in(w, lo, hi);
-  Pair s{0.0, 0.0};
-  constexpr int N = 16;   // elements in flight a lane: 32 or non-temporal loads gained nothing
-  for (int i = lo + 4 * int(threadIdx.x & 63); i < hi; i += 64 * N) {
-    float p[N], q[N];
-    load_run<DRAFT>(w, i, 256, hi, p, q);
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const Pair x = weigh<DRAFT>(w, some, i + e / 4 * 256 + e % 4, p[e], q[e]);
-      s.rest += x.rest;
-      s.whole += x.whole;
-    }
-  }
-  return s;
-}
-
 __device__ __forceinline__ double lane_value(double x, int lane) {   // lane: the same in all lanes
   const uint64_t v = uint64_t(__double_as_longlong(x));
   const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(v), lane), hi = __builtin_amdgcn_readlane(uint32_t(v >> 32), lane);
@@ -131,6 +115,36 @@ __device__ __forceinline__ double wave_scan(double x) {   // inclusive
   x += shifted<0x142, 0xA>(x);   // the row before's last, rows 1 and 3
   x += shifted<0x143, 0xC>(x);   // the first half's last, rows 2 and 3
   return x;
+}
+
+// The sum of a wave's run [lo, hi). Weights that are infinite, and refused tokens, are looked for
+// only where the plain sum is not finite, and where a token is in the run.
+template <bool DRAFT>
+__device__ __forceinline__ double sum_run(const Row& w, int lo, int hi) {
+  const uint64_t some = refused_in(w, lo, hi);
+  const int first = lo + 4 * int(threadIdx.x & 63);
+  constexpr int N = 16;   // elements in flight a lane: 32 or non-temporal loads gained nothing
+  double s = 0.0;
+  if (some == 0) {
+    for (int i = first; i < hi; i += 64 * N) {
+      float p[N], q[N];
+      load_run<DRAFT>(w, i, 256, hi, p, q);
+#pragma unroll
+      for (int e = 0; e < N; ++e) s += fmax(DRAFT ? double(p[e]) - double(q[e]) : double(p[e]), 0.0);
+    }
+    s = lane_value(wave_scan(s), 63);
+    if (s < __builtin_inf()) return s;
+  }
+  s = 0.0;
+  for (int i = first; i < hi; i += 64 * N) {
+    float p[N], q[N];
+    double v[N];
+    load_run<DRAFT>(w, i, 256, hi, p, q);
+    weigh<DRAFT>(w, some, i, 256, p, q, v);
+#pragma unroll
+    for (int e = 0; e < N; ++e) s += v[e];
+  }
+  return lane_value(wave_scan(s), 63);
 }
 
 struct Decision {
@@ -207,28 +221,23 @@ __device__ __forceinline__ Decision decide_tree(const VerifyCall& a, int64_t b, 
 // runs' sums, four a lane.
 struct Target {
   int part;
-  bool plain;                 // nothing is left but the target itself
+  bool any;                   // the row has a weight
   double before, threshold;   // the running sum before the part; what the draw's has to exceed
 };
 
-__device__ __forceinline__ Target find_part(const Pair (&x)[4], double u) {
-  const double rest = (x[0].rest + x[1].rest) + (x[2].rest + x[3].rest);
-  const double whole = (x[0].whole + x[1].whole) + (x[2].whole + x[3].whole);
-  const double scan_rest = wave_scan(rest), scan_whole = wave_scan(whole);
+__device__ __forceinline__ Target find_part(const double (&x)[4], double u) {
+  const double mine = (x[0] + x[1]) + (x[2] + x[3]), scan = wave_scan(mine), sum = lane_value(scan, 63);
+  double run[4];
+  run[0] = (scan - mine) + x[0];
+#pragma unroll
+  for (int j = 1; j < 4; ++j) run[j] = run[j - 1] + x[j];
   Target t;
-  t.plain = !(lane_value(scan_rest, 63) > 0.0);
-  const double mine = t.plain ? whole : rest, scan = t.plain ? scan_whole : scan_rest;
-  double r[4], run[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = t.plain ? x[j].whole : x[j].rest;
-  run[0] = (scan - mine) + r[0];
-#pragma unroll
-  for (int j = 1; j < 4; ++j) run[j] = run[j - 1] + r[j];
-  t.threshold = u * lane_value(scan, 63);
+  t.any = sum > 0.0;
+  t.threshold = u * sum;
   int first = 4 * 64, top = -1;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint64_t past = __ballot(r[j] > 0.0 && run[j] > t.threshold), any = __ballot(r[j] > 0.0);
+    const uint64_t past = __ballot(x[j] > 0.0 && run[j] > t.threshold), any = __ballot(x[j] > 0.0);
     if (past != 0) first = min(first, 4 * __builtin_ctzll(past) + j);
     if (any != 0) top = max(top, 4 * (63 - __builtin_clzll(any)) + j);
   }
@@ -240,65 +249,79 @@ __device__ __forceinline__ Target find_part(const Pair (&x)[4], double u) {
   return t;
 }
 
+// What a workgroup's waves tell each other.
+struct Shared {
+  double sum[kWaves];
+  int hit[kWaves], top[kWaves];
+  uint32_t arrived;
+  int path[kMaxNodes];
+};
+
+constexpr int kNone = 0x7FFFFFFF;
+
 // The first index of the part whose running sum passes the threshold, by the workgroup, 16
 // neighbours a thread at a time; else (rounding took the threshold past the last sum) the last
-// index with any weight; -1 if none has. found, last: LDS, 0x7FFFFFFF and -1 on entry.
+// index with any weight; -1 if none has.
 template <bool DRAFT>
-__device__ __forceinline__ int walk(const Row& w, const Target& t, int lo, int hi, double* parts, int* found, int* last) {
+__device__ __forceinline__ int walk(const Row& w, const Target& t, int lo, int hi, Shared& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const uint64_t some = refused_in(w, lo, hi);
   double before = t.before;
+  int last = -1;
   for (int block = lo; block < hi; block += 16 * kThreads) {
     const int i0 = block + 16 * tid;
     float p[16], q[16];
     load_run<DRAFT>(w, i0, 4, hi, p, q);
     double v[16], mine = 0.0;
+    weigh<DRAFT>(w, some, i0, 4, p, q, v);
     int top = -1;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const Pair x = weigh<DRAFT>(w, some, i0 + e, p[e], q[e]);
-      v[e] = t.plain ? x.whole : x.rest;
       mine += v[e];
       if (v[e] > 0.0) top = i0 + e;
     }
     const double scan = wave_scan(mine);
-    if (lane == 63) parts[wave] = scan;
+    if (lane == 63) sh.sum[wave] = scan;
     __syncthreads();
     double run = before, all = 0.0;
 #pragma unroll
     for (int x = 0; x < kWaves; ++x) {
-      if (x < wave) run += parts[x];
-      all += parts[x];
+      if (x < wave) run += sh.sum[x];
+      all += sh.sum[x];
     }
-    if (run + scan > t.threshold) {
+    // the wave's first thread whose neighbours take the sum past the threshold looks for the one
+    const uint64_t past = __ballot(top >= 0 && run + scan > t.threshold), any = __ballot(top >= 0);
+    if (lane == (past != 0 ? __builtin_ctzll(past) : 0)) {
+      int hit = past != 0 ? top : kNone;
       run += scan - mine;
-      int hit = -1;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         run += v[e];
-        if (hit < 0 && v[e] > 0.0 && run > t.threshold) hit = i0 + e;
+        if (v[e] > 0.0 && run > t.threshold) hit = min(hit, i0 + e);
       }
-      if (hit >= 0) atomicMin(found, hit);
+      sh.hit[wave] = hit;
     }
-    if (before + all <= t.threshold || block + 16 * kThreads >= hi)
-      if (top >= 0) atomicMax(last, top);   // perhaps none passes it
+    if (lane == (any != 0 ? 63 - __builtin_clzll(any) : 0)) sh.top[wave] = top;
     __syncthreads();
-    if (*found != 0x7FFFFFFF) return *found;
+    int found = kNone;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) {
+      found = min(found, sh.hit[x]);
+      last = max(last, sh.top[x]);
+    }
+    if (found != kNone) return found;
     before += all;
   }
-  return *last;
+  return last;
 }
 
+// A row's elements for each of `runs` waves, in whole quads.
+__device__ __forceinline__ int run_length(int vocab, int runs) { return ((vocab + runs - 1) / runs + 3) & ~3; }
+
 __global__ __launch_bounds__(kThreads) void verify_kernel(VerifyCall a, VerifySplit sp) {
-  __shared__ double parts[2][kWaves];
-  __shared__ int path[kMaxNodes], found, last;
-  __shared__ uint32_t arrived;
+  __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t b = blockIdx.y;
-  if (tid == 0) {
-    found = 0x7FFFFFFF;
-    last = -1;
-  }
   const double u0 = a.uniforms[b * a.nodes];
   int n;
   Decision d;
@@ -307,86 +330,100 @@ __global__ __launch_bounds__(kThreads) void verify_kernel(VerifyCall a, VerifySp
     d = decide_chain(a, b, n);
     if (d.stopped) w.draft = a.draft + (b * (a.nodes - 1) + d.row) * a.vocab;
   } else {
-    d = decide_tree(a, b, n, path, w);   // every wave writes the same path
+    d = decide_tree(a, b, n, sh.path, w);   // every wave writes the same path
   }
   w.target = a.target + (b * a.nodes + d.row) * a.vocab;
 
   // this wave's run of the row
-  const int each = ((a.vocab + sp.chunks * kWaves - 1) / (sp.chunks * kWaves) + 3) & ~3;
+  int each = run_length(a.vocab, sp.chunks * kWaves);
   const int64_t lo64 = int64_t(int(blockIdx.x) * kWaves + wave) * each;
   int lo = int(lo64 < a.vocab ? lo64 : a.vocab), hi = min(a.vocab, lo + each);
-  Pair s = w.draft != nullptr ? sum_run<true>(w, lo, hi) : sum_run<false>(w, lo, hi);
-  s.rest = lane_value(wave_scan(s.rest), 63);
-  s.whole = lane_value(wave_scan(s.whole), 63);
-  Pair x[4] = {};
+  double s = w.draft != nullptr ? sum_run<true>(w, lo, hi) : sum_run<false>(w, lo, hi);
+  double x[4] = {0.0, 0.0, 0.0, 0.0};
   if (sp.chunks > 1) {
-    __amdgpu_buffer_rsrc_t buf = coherent_buffer(sp.sums + b * kMaxParts * 2, kMaxParts * 16);
-    if (lane == 0) {
-      const uint64_t r = uint64_t(__double_as_longlong(s.rest)), t = uint64_t(__double_as_longlong(s.whole));
-      const u32x4 v = {uint32_t(r), uint32_t(r >> 32), uint32_t(t), uint32_t(t >> 32)};
-      __builtin_amdgcn_raw_buffer_store_b128(v, buf, (blockIdx.x * kWaves + wave) * 16, 0, kCoherent);
-    }
+    __amdgpu_buffer_rsrc_t buf = coherent_buffer(sp.sums + b * kMaxParts, kMaxParts * 8);
+    if (lane == 0)
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, s), buf, (blockIdx.x * kWaves + wave) * 8, 0, kCoherent);
     __builtin_amdgcn_s_waitcnt(0);   // the sums have reached the coherence point
     __syncthreads();
-    if (tid == 0) arrived = atomicAdd(sp.counters + b, 1u);
+    uint32_t* counter = sp.counters + b * sp.counter_step;
+    if (tid == 0) sh.arrived = atomicAdd(counter, 1u);
     __syncthreads();
-    if (arrived != uint32_t(sp.chunks - 1)) return;
-    if (tid == 0) atomicExch(sp.counters + b, 0u);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (4 * lane + j < sp.chunks * kWaves) {
-        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(buf, (4 * lane + j) * 16, 0, kCoherent);
-        x[j].rest = __longlong_as_double((long long)(uint64_t(v[1]) << 32 | v[0]));
-        x[j].whole = __longlong_as_double((long long)(uint64_t(v[3]) << 32 | v[2]));
-      }
-  } else {
-    if (lane == 0) {
-      parts[0][wave] = s.rest;
-      parts[1][wave] = s.whole;
+    if (sh.arrived != uint32_t(sp.chunks - 1)) return;
+    if (tid == 0) atomicExch(counter, 0u);
+    if (lane < sp.chunks) {   // a chunk's waves a lane
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(buf, lane * 32, 0, kCoherent);
+      const u32x4 z = __builtin_amdgcn_raw_buffer_load_b128(buf, lane * 32 + 16, 0, kCoherent);
+      x[0] = __builtin_bit_cast(double, u32x2{v[0], v[1]});
+      x[1] = __builtin_bit_cast(double, u32x2{v[2], v[3]});
+      x[2] = __builtin_bit_cast(double, u32x2{z[0], z[1]});
+      x[3] = __builtin_bit_cast(double, u32x2{z[2], z[3]});
     }
-    __syncthreads();
-    if (lane == 0)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = Pair{parts[0][j], parts[1][j]};
-    __syncthreads();
   }
-  const Target t = find_part(x, u0);
+  Target t;
+  bool alone = sp.chunks == 1;
+  while (true) {
+    if (alone) {
+      if (lane == 0) sh.sum[wave] = s;
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kWaves; ++j) x[j] = lane == 0 ? sh.sum[j] : 0.0;
+      __syncthreads();
+    }
+    t = find_part(x, u0);
+    if (t.any || (w.draft == nullptr && w.refusals == 0)) break;
+    // nothing is left but the target itself, whose sum this workgroup takes alone
+    w.draft = nullptr;
+    w.refusals = 0;
+    alone = true;
+    each = run_length(a.vocab, kWaves);
+    lo = min(a.vocab, wave * each);
+    s = sum_run<false>(w, lo, min(a.vocab, lo + each));
+  }
   lo = int(min(int64_t(a.vocab), int64_t(t.part) * each));
   hi = min(a.vocab, lo + each);
-  const int token = w.draft != nullptr ? walk<true>(w, t, lo, hi, parts[0], &found, &last)
-                                       : walk<false>(w, t, lo, hi, parts[0], &found, &last);
+  const int token = w.draft != nullptr ? walk<true>(w, t, lo, hi, sh) : walk<false>(w, t, lo, hi, sh);
   if (tid == 0) a.accepted[b] = d.accepted;
   if (tid < a.nodes) {
     int32_t* out = a.out_tokens + b * a.nodes;
-    const int next = tid < d.accepted ? (a.parents == nullptr ? tid + 1 : path[tid + 1]) : 0;
+    const int next = tid < d.accepted ? (a.parents == nullptr ? tid + 1 : sh.path[tid + 1]) : 0;
     out[tid] = n == 0 ? -1 : tid < d.accepted ? a.tokens[b * a.nodes + next] : tid == d.accepted ? token : -1;
-    if (a.path != nullptr) a.path[b * a.nodes + tid] = n > 0 && tid <= d.accepted ? path[tid] : -1;
+    if (a.path != nullptr) a.path[b * a.nodes + tid] = n > 0 && tid <= d.accepted ? sh.path[tid] : -1;
   }
 }
 
-// Chunks of a row: two workgroups a CU. (64 rows of 128256, us at 1, 2, 4, 8 a CU: 25.2, 21.4,
-// 23.6, 31.4: each makes the decisions for itself.)
+// Chunks of a row: four workgroups a CU. (us at 1, 2, 4, 8 a CU: 64 rows of 128256 with their
+// drafts 17.9, 16.0, 16.1, 17.5; 16 rows of 151936 11.1, 9.6, 9.1, 9.0: each makes the decisions
+// for itself.)
 int chunks_of(int64_t batch, int64_t vocab, const DeviceInfo& dev) {
   if (batch > NM_DECODE_COUNTER_BYTES / 4) return 1;
-  int64_t c = 2 * int64_t(dev.cu_count) / batch;
+  int64_t c = 4 * int64_t(dev.cu_count) / batch;
   if (c > kMaxChunks) c = kMaxChunks;
   if (c > vocab / kMinChunk) c = vocab / kMinChunk;
   return c < 1 ? 1 : int(c);
 }
 
+// From one sequence's counter to the next: a line where they are few (8 chains as above 6.7 us,
+// 8.9 with neighbouring counters; 16 trees 9.6 and 13.1).
+int counter_step(int64_t batch) {
+  const int64_t room = NM_DECODE_COUNTER_BYTES / 4 / batch;
+  return room > 32 ? 32 : int(room);
+}
+
 }  // namespace
 
 size_t verify_workspace_bytes(int64_t batch, int64_t vocab, const DeviceInfo& dev) {
-  return chunks_of(batch, vocab, dev) > 1 ? NM_DECODE_COUNTER_BYTES + size_t(batch) * kMaxParts * 16 : 0;
+  return chunks_of(batch, vocab, dev) > 1 ? NM_DECODE_COUNTER_BYTES + size_t(batch) * kMaxParts * sizeof(double) : 0;
 }
 
 hipError_t launch_verify(const VerifyCall& c, void* workspace, size_t workspace_bytes, hipStream_t stream,
                          const DeviceInfo& dev) {
   VerifyCall a = c;
-  VerifySplit sp{1, nullptr, nullptr};
+  VerifySplit sp{1, 0, nullptr, nullptr};
   const size_t need = verify_workspace_bytes(c.batch, c.vocab, dev);
   if (need > 0 && workspace != nullptr && workspace_bytes >= need) {
     sp.chunks = chunks_of(c.batch, c.vocab, dev);
+    sp.counter_step = counter_step(c.batch);
     sp.counters = static_cast<uint32_t*>(workspace);
     sp.sums = reinterpret_cast<double*>(static_cast<char*>(workspace) + NM_DECODE_COUNTER_BYTES);
   }

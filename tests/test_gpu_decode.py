@@ -908,3 +908,28 @@ def test_attend_equal_values_are_exact(context):
         got = nm.nm_tree_attention(q, cache, table, i32([context]), workspace=work)
         want = np.full(got.shape, 3.0)
         close(got, want, 3.0 * (HALF + 2 * (context + 8) * 2.0 ** -24) + 0 * want, f"{context}")
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+def test_verify_rows_with_nothing_left(workspace):
+    """A wide vocabulary whose rest is empty (drawn from the target after all), with infinities
+    and NaN in some runs of the row, and with refused tokens in the first and the last."""
+    rng = np.random.default_rng(91)
+    vocab = 150001
+    target, draft, tokens, u = chain_case(rng, 4, 2, vocab)
+    draft[0, 0] = target[0, 0]                       # equal, refused by its token
+    tokens[:, 1] = -1
+    draft[1, 0] = 1.0                                # more than the target has anywhere
+    target[2, 0, [5, 70000, 149999]] = np.inf, np.nan, -np.inf
+    draft[2, 0, [6, 70001]] = -np.inf, np.nan
+    target[3, 0], draft[3, 0] = 0.0, 0.0
+    check_chain(target, draft, tokens, u, workspace=workspace)
+    target, tokens, parents, u = tree_case(rng, 3, 5, vocab)
+    parents[:, 1:] = 0
+    target[0, 0] = 0.0                               # the first child's token holds it all, and is refused
+    target[0, 0, vocab - 1] = 0.25
+    tokens[:, 1:] = np.array([vocab - 1, 0, 1, 2])
+    u[0, 1:] = 0.5
+    target[1, 0, [3, 149998]] = np.inf
+    u[1:, 1:] = 0.999
+    check_tree(target, tokens, parents, u, workspace=workspace)
