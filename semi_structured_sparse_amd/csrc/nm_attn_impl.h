@@ -1078,12 +1078,14 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
       }
     }
   };
-  // (16 loads: 32 need more registers than there are. 20 rows of 64, 2 x 16384 tokens: 27.7 us with
-  // 1 x 16, 30.7 with 4 x 4; 16 rows of 256, 4 x 16384: 44.9 and 40.6.)
+  // (What fits the registers. us with 1 x 16, 4 x 4 and all of a thread's units, 24 loads: 20 rows
+  // of 64, 2 x 16384 tokens 27.7, 30.7 and -; 40 rows of 128, 2 x 131071 tokens -, 109 and 103.5; 16
+  // rows of 256, 4 x 16384 tokens 44.9, 40.5 and 41.0.)
+  constexpr int kUnits = D > 128 ? 4 : NR * D / 64 > 1 ? NR * D / 64 : 2;   // of a thread, if all rows are live
   if (units <= 2 * kAttnThreads)
     join(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
   else
-    join(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+    join(std::integral_constant<int, kUnits>{}, std::integral_constant<int, (D > 128 ? 16 : 24) / kUnits>{});
   __syncthreads();
   for (int u = tid; u < live * (D / 8); u += kAttnThreads) {
     const int r = u / (D / 8), d = u % (D / 8) * 8, at = rt * NR * 16 + r, node = at / a.group;
