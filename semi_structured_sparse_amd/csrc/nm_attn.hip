@@ -12,6 +12,7 @@ struct Plan {
   int row_tiles;   // workgroups of rows
   int slots;       // chunks over all sequences; 0: one a sequence
   uint32_t part_bytes;
+  float join;      // what a partial result costs in the join, in tiles
 };
 
 struct Kernel {
@@ -58,6 +59,8 @@ Plan plan_of(const AttnCall& c, int head_dim, int format, const DeviceInfo& dev)
   p.row_tiles = (tiles + most_tiles - 1) / most_tiles;
   p.nr = (tiles + p.row_tiles - 1) / p.row_tiles;
   p.part_bytes = uint32_t(head_dim / 16 * p.nr * 1024 + p.nr * 128);
+  const int live = std::min(rows, 16 * p.nr), code_bytes = format == NM_KV_FP16 ? 2 : 1;
+  p.join = 2.0f * float(live * 4) / float(2 * kTileKeys * code_bytes);   // twice its bytes over a tile's
   const int64_t items = int64_t(c.batch) * c.cache.kv_heads * p.row_tiles;
   const int64_t most = int64_t(c.cache.table_width) << c.cache.page_shift;
   // Slots for as many workgroups as the GPU holds at once (once more for every two thirds of
@@ -87,7 +90,7 @@ hipError_t launch_attention(const AttnCall& c, int head_dim, int format, void* w
   Plan p = plan_of(c, head_dim, format, dev);
   if (workspace == nullptr || workspace_bytes < plan_bytes(c, p)) p.slots = 0;
   AttnSplit sp{p.slots, p.row_tiles, static_cast<uint32_t*>(workspace),
-               p.slots ? static_cast<char*>(workspace) + NM_DECODE_COUNTER_BYTES : nullptr, p.part_bytes};
+               p.slots ? static_cast<char*>(workspace) + NM_DECODE_COUNTER_BYTES : nullptr, p.part_bytes, p.join};
   void* args[] = {&a, &sp};
   // Row tiles of one chunk read the same keys: a grid width that is a multiple of the 8 XCDs
   // puts them on one XCD's L2.

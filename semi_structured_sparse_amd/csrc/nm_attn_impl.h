@@ -50,6 +50,7 @@ struct AttnSplit {
   uint32_t* counters;
   char* parts;
   uint32_t part_bytes;
+  float join;      // what a partial result costs in the join, in tiles
 };
 
 // What a kernel variant holds: registers and LDS set the waves of a SIMD (the workgroups of a
@@ -706,10 +707,16 @@ __device__ __forceinline__ void attn_lengths(const AttnCall& a, int b, uint32_t&
   keys = uint32_t(min(int64_t(context) + count, most));
 }
 
-// Tiles of a sequence's chunk: `per`, more where that would make more than `most` chunks.
-__device__ __forceinline__ uint32_t chunk_tiles(uint32_t tiles, uint32_t per, uint32_t most) {
+// Tiles of a sequence's chunk: `per`, more where that would make more than `most` chunks, or where
+// the last of c chunks would spend longer on the partial results (c of them) than on its tiles (a
+// c-th of the sequence's): join is what a partial costs in tiles. (us without, with join at half,
+// once, twice a partial's bytes over a tile's, and at 4 times: 4 x 4 nodes over 16384 e4m3 tokens
+// of 256 40.8, 37.9, 38.1, 33.0, 34.2; 2 x 5 over 16384 int8 tokens of 64 26.8, 23.3, 23.0, 22.6,
+// 26.1; 2 x 8 over 131071 int8 tokens 104, 104, 104, 103 to 105, 120. It is set at twice.)
+__device__ __forceinline__ uint32_t chunk_tiles(uint32_t tiles, uint32_t per, uint32_t most, float join) {
   const uint32_t least = (tiles + most * kAttnWaves - 1) / (most * kAttnWaves) * kAttnWaves;
-  return per > least ? per : least;
+  const uint32_t even = uint32_t(__builtin_amdgcn_sqrtf(float(tiles) * join) * (1.0f / kAttnWaves) + 0.999f) * kAttnWaves;
+  return max(max(per, least), even);
 }
 __device__ __forceinline__ uint32_t chunks_of(uint32_t tiles, uint32_t per) {
   return tiles <= per ? 1u : (tiles + per - 1) / per;
@@ -728,7 +735,7 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
 
 // Every wave works this out for itself: 64 sequences a pass, one a lane; the first 64 stay in
 // registers.
-__device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, int slot, uint32_t most) {
+__device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, int slot, uint32_t most, float join) {
   const int lane = threadIdx.x & 63;
   struct Lengths {
     uint32_t context, keys, tiles;   // tiles: at most 2^25
@@ -776,7 +783,7 @@ __device__ __forceinline__ AttnChunk find_chunk(const AttnCall& a, int slots, in
     int n = 0;
     if (b0 + lane < a.batch) {
       if (slots > a.batch) {   // as many chunks as `per` asks for, of even size
-        n = int(chunks_of(x.tiles, chunk_tiles(x.tiles, per, most)));
+        n = int(chunks_of(x.tiles, chunk_tiles(x.tiles, per, most, join)));
         mine = max((x.tiles + n * kAttnWaves - 1) / (n * kAttnWaves), 1u) * kAttnWaves;
       }
       n = int(chunks_of(x.tiles, mine));
@@ -810,7 +817,7 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int head = int(blockIdx.x) % a.cache.kv_heads, slot = int(blockIdx.x) / a.cache.kv_heads;
   const int rt = blockIdx.y;
-  AttnChunk ck = find_chunk(a, sp.slots, slot, S::kMaxChunks);
+  AttnChunk ck = find_chunk(a, sp.slots, slot, S::kMaxChunks, sp.join);
   const int b = __builtin_amdgcn_readfirstlane(ck.b);
   if (b < 0) return;
   const int chunks = __builtin_amdgcn_readfirstlane(ck.chunks), first = __builtin_amdgcn_readfirstlane(ck.first);
