@@ -52,6 +52,7 @@ def extension_command(out: str) -> list:
     base = os.path.dirname(torch.__file__)
     inc, lib = os.path.join(base, "include"), os.path.join(base, "lib")
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    # the HIP headers, under a host compiler, have to be told the platform
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DUSE_ROCM",
             "-D__HIP_PLATFORM_AMD__", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             f"-I{INCLUDE}", "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),

@@ -166,8 +166,12 @@ _QUICK = ("nm_rope", "nm_kv_append", "nm_rope_kv_append", "nm_kv_read", "nm_kv_c
 def _bound():
     global _quick
     if _quick is None:
-        from . import _nmtorch
         lib = _nm().lib()
+        try:
+            from . import _nmtorch
+        except ImportError as e:
+            raise RuntimeError(f"_nmtorch.so does not load ({e}); build it with "
+                               "python -m semi_structured_sparse_amd.build") from e
         _nmtorch.bind(*(_c.cast(getattr(lib, name), _c.c_void_p).value for name in _QUICK))
         _quick = _nmtorch
     return _quick
