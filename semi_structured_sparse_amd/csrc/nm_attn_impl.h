@@ -859,7 +859,9 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
     const bool live = r < rows && t < count;
     uint64_t mk = 0;
     if (live) mk = a.mask != nullptr ? a.mask[int64_t(b) * a.tokens + t] : t >= 63 ? ~0ull : (2ull << t) - 1;
-    w.mask[n] = count >= 64 ? mk : mk & ((1ull << count) - 1);
+    // nodes past the page table's end are not there: their tile may reach further than the keys
+    const uint32_t held = w.keys - w.context;
+    w.mask[n] = held >= 64 ? mk : mk & ((1ull << held) - 1);
     w.m[n] = kLowest;
     w.l[n] = 0.f;
 #pragma unroll

@@ -1,0 +1,72 @@
+"""GPU tests of the attention where its range ends: tables, weights, scales, sums and workspaces.
+Bounds are those of tests/attend_bounds.py, derived there."""
+import numpy as np
+import pytest
+import torch
+
+import semi_structured_sparse_amd as nm
+from oracle import decode_oracle as ref
+from tests.attend_bounds import HALF, TINY, attend_exact, markers
+from tests.gpu_helpers import device, say
+from tests.test_gpu_decode import FORMATS, Paged, close, halves, i32, tree_masks, up
+
+pytestmark = pytest.mark.gpu
+LARGEST = {"int8": 127.0, "e4m3": 448.0}
+
+
+def cache_of(k, v, form, page=16, k_scale=None, v_scale=None):
+    """A cache of one sequence whose tokens are k, v [keys, kv, dim] (codes where a scale [keys, kv]
+    is given), in consecutive pages; its table."""
+    keys, kv, dim = k.shape
+    pages = -(-keys // page)
+
+    def paged(x, dtype):
+        full = np.zeros((pages * page,) + x.shape[1:], np.float32)
+        full[:keys] = x
+        full = full.reshape((pages, page) + x.shape[1:])
+        return torch.from_numpy(np.ascontiguousarray(full.swapaxes(1, 2))).to(dtype).to(device())
+
+    scales = [None if s is None else paged(s, torch.float32) for s in (k_scale, v_scale)]
+    return nm.KVCache(paged(k, FORMATS[form]), paged(v, FORMATS[form]), *scales), i32(np.arange(pages)[None])
+
+
+def attend(q, cache, table, context, workspace, **kw):
+    ws = nm.tree_attention_workspace(q, cache, table) if workspace else None
+    out = nm.nm_tree_attention(q, cache, table, i32(context), workspace=ws, **kw)
+    torch.cuda.synchronize()
+    return out.cpu().numpy().astype(np.float64)
+
+
+# --------------------------------------------------------------------- the end of the page table
+@pytest.mark.parametrize("form", list(FORMATS))
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("width", [1, 2, 3, 4, 129])
+def test_nodes_past_the_page_table_are_not_there(form, masked, width):
+    """context + count is clamped to the table's positions, which end inside a tile of 32 where
+    pages of 16 are odd in number: nodes past them see what fits, and are seen by none."""
+    say(f"table end {form} {width} {masked}")
+    rng = np.random.default_rng(width)
+    tokens, cap = 5, 16 * width
+    context = [cap - 3, cap, cap + 7, cap - 5, 2 ** 31 - 1]
+    p = Paged(rng, len(context), width, 16, 2, 128, form)
+    masks = tree_masks(rng, len(context), tokens) if masked else None
+    q = halves(rng, len(context), tokens, 4, 128)
+    counts = [5, 5, 5, 4, 5]
+    k, v = p.values()
+    for workspace in (True, False):
+        got = attend(up(q), p.cache, up(p.table), context, workspace, count=i32(counts),
+                     mask=None if masks is None else up(masks.view(np.int64)))
+        for b in range(len(context)):
+            held = min(context[b], cap)
+            keys = min(held + counts[b], cap)
+            seen = ref.tree_seen(held, counts[b], None if masks is None else masks[b])[:, :keys]
+            at = np.arange(keys)
+            z = None
+            if form != "fp16":
+                z = p.cache.v_scale.cpu().numpy()[p.table[b, at // 16], :, at % 16]
+            bias = 0.0
+            if form == "int8":
+                bias = 128.0 * p.cache.k_scale.cpu().numpy()[p.table[b, at // 16], :, at % 16].astype(np.float64)
+            want, bound = attend_exact(q[b, :counts[b]], p.rows(k, b, at), p.rows(v, b, at), seen, 128 ** -0.5, z, bias)
+            close(got[b, :counts[b]], want, bound, f"width {width} sequence {b}")
+            assert np.all(got[b, counts[b]:] == 0)
