@@ -719,7 +719,7 @@ __device__ __forceinline__ void attn_lengths(const AttnCall& a, int b, uint32_t&
   const int64_t c = a.context[b];
   count = count_of(a.count, b, a.tokens);
   context = uint32_t(c < 0 ? 0 : c > most ? most : c);
-  keys = uint32_t(min(int64_t(context) + count, most));
+  keys = uint32_t(c + count < 0 ? 0 : c + count > most ? most : c + count);
 }
 
 // Tiles of a sequence's chunk: `per`, more where that would make more than `most` chunks, or where

@@ -70,3 +70,14 @@ def test_nodes_past_the_page_table_are_not_there(form, masked, width):
             want, bound = attend_exact(q[b, :counts[b]], p.rows(k, b, at), p.rows(v, b, at), seen, 128 ** -0.5, z, bias)
             close(got[b, :counts[b]], want, bound, f"width {width} sequence {b}")
             assert np.all(got[b, counts[b]:] == 0)
+
+
+@pytest.mark.parametrize("form", list(FORMATS))
+def test_a_context_below_zero_shortens_the_nodes(form):
+    """context and context + count are both clamped to 0: of 5 nodes from -3 on, positions 0 and 1."""
+    rng = np.random.default_rng(7)
+    p = Paged(rng, 3, 2, 16, 2, 64, form)
+    q = up(halves(rng, 3, 5, 4, 64))
+    got = attend(q, p.cache, up(p.table), [-3, -5, -2 ** 31], False)
+    want = attend(q, p.cache, up(p.table), [0, 0, 0], False, mask=up(np.tile(np.array([1, 3, 3, 3, 3]), (3, 1))))
+    assert np.array_equal(got[0], want[0]) and not got[1:].any()
