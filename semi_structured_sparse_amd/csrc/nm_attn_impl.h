@@ -133,7 +133,11 @@ __device__ __forceinline__ float sum4(float x) {
 
 // Two fp16 of a word of codes: bytes 0, 1 (hi: 2, 3) of e4m3. int8 codes come with their sign
 // bit flipped, u = code + 128, and zero-extended to 16 bits they are the subnormals u 2^-24,
-// exact in the matrix instruction; the sums are corrected by 128 times the other side's sum.
+// exact in the matrix instruction. The scores' sums over a head's elements are corrected by 128
+// times the sum of q. The values' run over the keys, and 128 times a long sum of weights would
+// take the bits of a result that cancels: there the 128 comes off each pair of codes, exactly
+// (131072 keys in one chunk, values that nearly cancel: off by 240 times the bound with the sums
+// corrected; 32 sequences of one token 68.9 us then, 69.3 now, 2 of 8 nodes 100.8 and 100.7).
 constexpr float kCodeUnit = 0x1p24f;    // int8: the products come out in 2^-24
 constexpr float kCodeBias = 128.0f;
 
@@ -144,6 +148,12 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t codes, bool hi) {
               : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(codes), 1.0f, false));
   else
     return __builtin_amdgcn_perm(codes, codes, hi ? 0x0C030C02u : 0x0C010C00u);   // 0x0C: a zero byte
+}
+
+// Two flipped int8 codes, zero-extended, to code 2^-24.
+__device__ __forceinline__ uint32_t unbiased(uint32_t pair) {
+  const _Float16 bias = _Float16(-kCodeBias / kCodeUnit);
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, pair) + f16x2{bias, bias});
 }
 
 template <int FMT>
@@ -337,7 +347,7 @@ struct AttnWave {
   uint64_t mask[NR];
   f32x4 o[S::kJ][NR];
   float m[NR], l[NR];
-  float qs[NR], ws[NR];   // int8: -128 sum(q), and the sum of the weights, for the codes' bias
+  float qs[NR];           // int8: -128 sum(q), for the codes' bias
   uint32_t tile0, step, tiles;   // this wave's tiles: tile0 + i * step, i < tiles
   char* ring;                    // its LDS: kDepth slots of {keys, values, scales}
   uint32_t ring_at, q_at;        // LDS addresses of the same, and of this lane's piece of Q
@@ -519,10 +529,10 @@ struct AttnWave {
       } else {
         const uint32_t a = flipped<FMT>(t.v[2 * p][c]), b = flipped<FMT>(t.v[2 * p + 1][c]);
         if constexpr (FMT == NM_KV_INT8) {
-          w[0][p] = __builtin_amdgcn_perm(b, a, 0x0C040C00u);
-          w[1][p] = __builtin_amdgcn_perm(b, a, 0x0C050C01u);
-          w[2][p] = __builtin_amdgcn_perm(b, a, 0x0C060C02u);
-          w[3][p] = __builtin_amdgcn_perm(b, a, 0x0C070C03u);
+          w[0][p] = unbiased(__builtin_amdgcn_perm(b, a, 0x0C040C00u));
+          w[1][p] = unbiased(__builtin_amdgcn_perm(b, a, 0x0C050C01u));
+          w[2][p] = unbiased(__builtin_amdgcn_perm(b, a, 0x0C060C02u));
+          w[3][p] = unbiased(__builtin_amdgcn_perm(b, a, 0x0C070C03u));
         } else {
           const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x05010400u), hi = __builtin_amdgcn_perm(b, a, 0x07030602u);
           w[0][p] = pair_of<FMT>(lo, false);
@@ -590,10 +600,7 @@ struct AttnWave {
         sum[x % NR] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, __builtin_bit_cast(f16x8, q[x]), sum[x % NR], 0, 0, 0);
     }
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      qs[n] = sum[n][0] * (-kCodeBias / kCodeUnit);
-      ws[n] = 0.f;
-    }
+    for (int n = 0; n < NR; ++n) qs[n] = sum[n][0] * (-kCodeBias / kCodeUnit);
   }
 
   // Which of a tile's keys this lane's row n sees, a bit each.
@@ -638,7 +645,6 @@ struct AttnWave {
         const float f = exp2_fast(m[n] - next);
         m[n] = next;
         l[n] *= f;
-        if (FMT == NM_KV_INT8) ws[n] *= f;
 #pragma unroll
         for (int j = 0; j < S::kJ; ++j) o[j][n] *= f;
       }
@@ -653,11 +659,6 @@ struct AttnWave {
         if constexpr (FMT != NM_KV_FP16) l[n] = fmaf(y, t.iz[e], l[n]);
         w[n][e] = _Float16(y);   // to nearest even: 2^-11 of the weight
         if constexpr (FMT == NM_KV_FP16) l[n] += float(w[n][e]);
-      }
-      if constexpr (FMT == NM_KV_INT8) {
-        const f16x2 ones = {_Float16(1.0f), _Float16(1.0f)};
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) ws[n] = __builtin_amdgcn_fdot2(f16x2{w[n][e], w[n][e + 1]}, ones, ws[n], false);
       }
     }
   }
@@ -932,10 +933,9 @@ __global__ __launch_bounds__(kAttnThreads, (AttnShape<FMT, D, NR>::kWaves)) void
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     w.l[n] = sum4(w.l[n]);
-    if constexpr (FMT == NM_KV_INT8) {   // O in its own unit, without the codes' bias
-      const float bias = w.tiles > 0 ? sum4(w.ws[n]) * kCodeBias : 0.f;
+    if constexpr (FMT == NM_KV_INT8) {   // O in its own unit
 #pragma unroll
-      for (int j = 0; j < S::kJ; ++j) w.o[j][n] = w.o[j][n] * kCodeUnit - bias;
+      for (int j = 0; j < S::kJ; ++j) w.o[j][n] *= kCodeUnit;
     }
     if (w.g == 0) {
       stat_m[wave][16 * n + w.li] = w.m[n];

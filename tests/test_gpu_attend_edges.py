@@ -81,3 +81,39 @@ def test_a_context_below_zero_shortens_the_nodes(form):
     got = attend(q, p.cache, up(p.table), [-3, -5, -2 ** 31], False)
     want = attend(q, p.cache, up(p.table), [0, 0, 0], False, mask=up(np.tile(np.array([1, 3, 3, 3, 3]), (3, 1))))
     assert np.array_equal(got[0], want[0]) and not got[1:].any()
+
+
+# ---------------------------------------------------------------------------------- long sums
+@pytest.mark.parametrize("form", list(FORMATS))
+@pytest.mark.parametrize("workspace", [False, True])
+def test_long_sums_of_values_that_cancel(form, workspace):
+    """131072 keys whose weights are fp16 numbers (scores log2 of 1 + r/1024, so that the rounding to
+    fp16 takes the exponential's error off) and whose weighted values, multiples of 2^-6, nearly
+    cancel in pairs: every partial sum of a wave stays below 2^18, exact in fp32. What is left are
+    the sum of the weights (8192 positive terms a lane, 2^-24 of the sum so far each, which is half
+    of the whole on average: 2^-12; 2^-20 for exponentials and joins) and the last rounding."""
+    say(f"cancel {form} {workspace}")
+    rng = np.random.default_rng(5)
+    keys, kv, dim = 131072, 1, 64
+    w = 1.0 + rng.integers(0, 1024, keys) / 1024.0
+    w[::32] = 2.0                                # the largest comes first in every tile
+    if form == "fp16":                           # the score is the key's own: held equal
+        w[:] = 2.0
+    k = np.zeros((keys, kv, dim))
+    k[:, 0, 0] = 1.0
+    codes = rng.integers(1, 8, (keys // 2, 1, dim)) * 16.0 * rng.choice([-1.0, 1.0], (keys // 2, 1, dim))
+    v = np.repeat(codes, 2, 0)
+    v[1::2] *= -1.0
+    ks = vs = None
+    if form == "fp16":
+        v[::2] += 0.5                            # what is left of each pair
+    else:
+        ks, vs = np.log2(w)[:, None].astype(np.float32), np.ones((keys, kv), np.float32)
+    parts = (w[:, None] * v[:, 0]).reshape(-1, 4, 32, dim)
+    assert np.abs(np.cumsum(parts.sum(2), 0)).max() + np.abs(parts).sum(2).max() < 2 ** 18
+    want = (parts.sum((0, 1, 2)) / w.sum())[None, None]
+    q = np.zeros((1, 1, 1, dim), np.float16)
+    q[..., 0] = 1.0
+    cache, table = cache_of(k, v, form, 128, ks, vs)
+    got = attend(up(q), cache, table, [keys - 1], workspace, scale=np.log(2.0))
+    close(got[0], want, np.abs(want) * (HALF + 2.0 ** -12 + 2.0 ** -20) + TINY, f"{form} {workspace}")
