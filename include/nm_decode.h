@@ -153,14 +153,16 @@ int nm_kv_compact(const nm_kv_cache* cache, const int32_t* table, int64_t table_
  * nodes at or past count, get zeros. Keys that a node does not see do not touch its result,
  * whatever they hold (NaN and infinities too). A draft whose v row has an infinity or NaN in
  * it makes the results of the nodes that see it NaN. fp16 products of exact codes, fp32 sums;
- * the weights times v's scale are rounded to fp16 (relative 2^-11) for the second product.
+ * the weights times v's scale are rounded to fp16 for the second product: relative 2^-11 down to
+ * 2^-21 of the largest in the row, below that 2^-32 of the largest.
  * Bit-identical from run to run for the same arguments, lengths and size of workspace.
  *   q     fp16, token (b, t)'s head h at [(b * tokens + t) * q_stride + h * head_dim]; 16-byte
  *         aligned, q_stride a multiple of 8;  out  fp16 [batch][tokens][heads][head_dim], 16-byte
  *         aligned
  *   mask  uint64 [batch][tokens], 8-byte aligned, or NULL;  context, count  int32 [batch]
- * context and context + count are clamped to 0 .. table_width * page; positions whose table
- * entry is outside 0 .. blocks - 1 have unspecified keys and values.
+ * context and context + count are clamped to 0 .. table_width * page (nodes past that end are
+ * seen by none, and see what lies before it); positions whose table entry is outside
+ * 0 .. blocks - 1 have unspecified keys and values.
  * workspace: device memory for the split of long contexts over the GPU, 16-byte aligned, or
  * NULL (no split). Its first NM_DECODE_COUNTER_BYTES are counters that must be zero before
  * the first call on it; every call leaves them zero, so one workspace serves any sequence of

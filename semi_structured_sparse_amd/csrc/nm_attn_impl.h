@@ -5,9 +5,11 @@
 // keys with a running maximum, and O^T = V^T P^T adds up. A value's scale z_j goes into the
 // exponent: with x_j = s_j + log2 z_j (scores in units of log2) the weight that the second
 // product takes in fp16 is 2^(x_j - m), and l = sum 2^(x_j - m) / z_j is kept in fp32. Each row's
-// reference m is the largest x_j so far, so the weights stay in fp16's range whatever the
-// scales of v; it moves only when it would grow by more than 8 (weights up to 2^8 are as exact
-// in fp16), which takes the maximum over lanes and the rescaling out of most tiles.
+// reference m is set 7 below the largest x_j so far, so the weights stay in fp16's range whatever
+// the scales of v; it moves only when it would grow by more than 8, which takes the maximum over
+// lanes and the rescaling out of most tiles. So the largest weight is 2^7 to 2^15, and fp16's
+// normal numbers hold what is down to 2^-21 of it to 2^-11, smaller ones to 2^-32 of it. (Without
+// the 7, 4096 keys 2^-22.5 below a leading one were off by 6%.)
 //
 // Work split. A workgroup of 4 waves takes one key head's rows (16 NR of them) and a chunk of
 // one sequence's keys; its waves take every fourth tile of 32 keys. Each wave loads its own tiles
@@ -53,6 +55,8 @@ constexpr int kTileKeys = 32;
 constexpr int kMinChunkTiles = 2 * kAttnWaves;   // two tiles a wave: a chunk more costs the join as much
 constexpr int kNonTemporal = 2;              // cache policy bit of a load
 constexpr float kLowest = -3e38f;            // the reference of a row that has seen nothing
+constexpr float kLift = 7.0f;                // from a row's reference, when it moves, to its largest score
+constexpr float kLag = 8.0f;                 // the score's growth until it moves: 2^(kLift + kLag) fits fp16
 // A value's scale counts as at least this (rows of zeros have scale 0, and codes 0): far below
 // what fp16 results can show, and its reciprocal times any number of keys is finite.
 constexpr float kLeastScale = 0x1p-100f;
@@ -636,12 +640,12 @@ struct AttnWave {
     for (int n = 0; n < NR; ++n) {
       top[n] = fmaxf(fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])),
                      fmaxf(fmaxf(x[n][4], x[n][5]), fmaxf(x[n][6], x[n][7])));
-      grows |= top[n] > m[n] + 8.0f;
+      grows |= top[n] > m[n] + (kLift + kLag);
     }
     if (__any(grows)) {
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
-        const float next = fmaxf(m[n], max4(top[n]));
+        const float next = fmaxf(m[n], max4(top[n]) - kLift);
         const float f = exp2_fast(m[n] - next);
         m[n] = next;
         l[n] *= f;

@@ -83,6 +83,36 @@ def test_a_context_below_zero_shortens_the_nodes(form):
     assert np.array_equal(got[0], want[0]) and not got[1:].any()
 
 
+# ------------------------------------------------------------------------------- small weights
+@pytest.mark.parametrize("form", list(FORMATS))
+@pytest.mark.parametrize("bits", [14.5, 18.5, 20.5, 22.5, 23.5])
+def test_long_tails_below_a_dominant_key_keep_their_share(form, bits):
+    """Four keys, one for each wave, lead and hold nothing; all that is left of the result is the
+    tail, 2^-bits of them each."""
+    say(f"tail {form} {bits}")
+    rng = np.random.default_rng(int(2 * bits))
+    keys, kv, dim = 4096, 1, 64
+    k, v = np.zeros((keys, kv, dim)), np.zeros((keys, kv, dim))
+    k[0:128:32, 0, 0] = 64.0
+    v[:, 0] = rng.integers(64, 128, (keys, dim)) if form != "e4m3" else rng.choice([64.0, 80.0, 96.0, 112.0], (keys, dim))
+    v[0:128:32] = 0.0
+    q = np.zeros((1, 1, 1, dim), np.float16)
+    q[..., 0] = 1.0
+    ks = vs = None
+    if form != "fp16":
+        ks, vs = np.full((keys, kv), 1 / 64, np.float32), np.full((keys, kv), 8.0 if form == "int8" else 2.0, np.float32)
+    cache, table = cache_of(k, v, form, 64, ks, vs)
+    scale = bits * np.log(2.0) / (64.0 if form == "fp16" else 1.0)
+    values = v * (1.0 if vs is None else vs[..., None].astype(np.float64))
+    keyed = k * (1.0 if ks is None else ks[..., None].astype(np.float64))
+    want, bound = attend_exact(q[0], keyed, values, np.ones((1, keys), bool), np.float64(np.float32(scale)), vs,
+                               0.0 if form != "int8" else 128.0 * ks)
+    assert np.abs(want).min() > 2.0 ** -14
+    for workspace in (False, True):
+        got = attend(up(q), cache, table, [keys - 1], workspace, scale=scale)
+        close(got[0], want, bound, f"{form} {bits} bits, workspace {workspace}")
+
+
 # ---------------------------------------------------------------------------------- long sums
 @pytest.mark.parametrize("form", list(FORMATS))
 @pytest.mark.parametrize("workspace", [False, True])
