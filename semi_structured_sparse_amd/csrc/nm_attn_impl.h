@@ -58,8 +58,11 @@ constexpr float kLowest = -3e38f;            // the reference of a row that has 
 constexpr float kLift = 7.0f;                // from a row's reference, when it moves, to its largest score
 constexpr float kLag = 8.0f;                 // the score's growth until it moves: 2^(kLift + kLag) fits fp16
 // A value's scale counts as at least this (rows of zeros have scale 0, and codes 0): far below
-// what fp16 results can show, and its reciprocal times any number of keys is finite.
-constexpr float kLeastScale = 0x1p-100f;
+// what fp16 results can show, its reciprocal times any number of keys is finite, and a key's term
+// of the sum, 2^(x - m) before the reciprocal, stays in fp32's range down to 2^-60 of the largest
+// beside values up to fp16's. (With 2^-100 it did not: 65535 rows of zeros 2^-18.5 below one of
+// 61440 were left out: the result was 18% too large.)
+constexpr float kLeastScale = 0x1p-60f;
 
 // How the host cuts a call up: `slots` chunks over all sequences (0: one a sequence), row_tiles
 // workgroups of rows, and where the chunks' partial results go.

@@ -113,6 +113,29 @@ def test_long_tails_below_a_dominant_key_keep_their_share(form, bits):
         close(got[0], want, bound, f"{form} {bits} bits, workspace {workspace}")
 
 
+@pytest.mark.parametrize("form", ["int8", "e4m3"])
+@pytest.mark.parametrize("bits", [18.5, 24.5])
+def test_rows_of_zeros_keep_their_weight_in_the_sum(form, bits):
+    """One key of large values over a long tail whose values are zeros (scale 0): they shrink the
+    result by their share, whatever lies between the scales."""
+    keys, kv, dim = 65536, 1, 64
+    k, v = np.zeros((keys, kv, dim)), np.zeros((keys, kv, dim))
+    k[5, 0, 0], v[5, 0] = 1.0, np.arange(64, 128) // 8 * 8
+    q = np.zeros((1, 1, 1, dim), np.float16)
+    q[..., 0] = 1.0
+    ks, vs = np.ones((keys, kv), np.float32), np.zeros((keys, kv), np.float32)
+    vs[5] = 512.0 if form == "int8" else 128.0
+    cache, table = cache_of(k, v, form, 128, ks, vs)
+    scale = float(np.float32(bits * np.log(2.0)))
+    share = 1.0 / (1.0 + (keys - 1) * np.exp(-scale))
+    want = v[5] * np.float64(vs[5, 0]) * share
+    # the exponentials 2^-20 together, the sum in fp32 over 65536 keys, both weights' rounding
+    bound = np.abs(want) * (2 * HALF + 2.0 ** -19 + keys * 2.0 ** -24 * (1.0 - share)) + HALF * np.abs(want)
+    for workspace in (False, True):
+        got = attend(up(q), cache, table, [keys - 1], workspace, scale=scale)
+        close(got[0, 0], want, bound, f"{form} workspace {workspace}")
+
+
 # ---------------------------------------------------------------------------------- long sums
 @pytest.mark.parametrize("form", list(FORMATS))
 @pytest.mark.parametrize("workspace", [False, True])
@@ -147,3 +170,28 @@ def test_long_sums_of_values_that_cancel(form, workspace):
     cache, table = cache_of(k, v, form, 128, ks, vs)
     got = attend(up(q), cache, table, [keys - 1], workspace, scale=np.log(2.0))
     close(got[0], want, np.abs(want) * (HALF + 2.0 ** -12 + 2.0 ** -20) + TINY, f"{form} {workspace}")
+
+
+@pytest.mark.parametrize("form", ["int8", "e4m3"])
+@pytest.mark.parametrize("factor", [2.0 ** -5, 1.0, 2.0 ** 6])
+def test_small_and_uneven_value_scales_keep_their_bits(form, factor):
+    """Results that fp16 holds in full, of values whose scales differ by 2^6 from page to page."""
+    rng = np.random.default_rng(82)
+    p = Paged(rng, 2, 20, 16, 2, 64, form)
+    p.cache.v.view(torch.uint8).bitwise_and_(0x7F)             # positive: nothing cancels
+    p.cache.v_scale.mul_(factor)
+    p.cache.v_scale[::2].mul_(2.0 ** -6)
+    p.cache.v_scale[3] = 0.0
+    q = halves(rng, 2, 2, 4, 64)
+    context = [300, 17]
+    k, v = p.values()
+    for workspace in (True, False):
+        got = attend(up(q), p.cache, up(p.table), context, workspace)
+        for b, ctx in enumerate(context):
+            at = np.arange(ctx + 2)
+            pick = (p.table[b, at // 16], slice(None), at % 16)
+            z, ks = p.cache.v_scale.cpu().numpy()[pick], p.cache.k_scale.cpu().numpy()[pick]
+            want, bound = attend_exact(q[b], p.rows(k, b, at), p.rows(v, b, at), ref.tree_seen(ctx, 2, None), 1 / 8, z,
+                                       0.0 if form != "int8" else 128.0 * ks.astype(np.float64))
+            assert np.abs(want).min() > 2.0 ** -14
+            close(got[b], want, bound, f"{form} {factor} sequence {b}")
