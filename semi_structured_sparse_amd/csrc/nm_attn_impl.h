@@ -173,9 +173,13 @@ __device__ __forceinline__ f16x8 as_half8(const uint32_t (&w)[4]) {
   return __builtin_bit_cast(f16x8, v);
 }
 
-// Bits 15 and 31: whether the two fp16 of a word are infinite or NaN.
+// Nonzero where one of a word's two fp16 is infinite or NaN, or one of its four e4m3 codes is NaN
+// (0x7F with either sign; there are no infinities). int8 codes are numbers.
+template <int FMT>
 __device__ __forceinline__ uint32_t non_finite(uint32_t v) {
-  return ((v & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+  if constexpr (FMT == NM_KV_FP16) return ((v & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+  if constexpr (FMT == NM_KV_E4M3) return ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  return 0;
 }
 
 // The 16-byte pieces of a row in LDS are permuted by its number, so that the 8 lanes that read
@@ -671,16 +675,17 @@ struct AttnWave {
   }
 
   // Values of an edge tile: those past the end, which were never written and may be NaN, become
-  // 0, since 0 times them is not; so does a draft's fp16 row with an infinity or NaN in it, whose
-  // key is returned as a bit: the rows that see it are NaN, the others must not be.
+  // 0, since 0 times them is not; so does a draft's row with an infinity or NaN in it (an fp16, or
+  // an e4m3 code, which no append writes but a caller's own tensor may hold), whose key is returned
+  // as a bit: the rows that see it are NaN, the others must not be.
   __device__ __forceinline__ uint32_t edge_values(AttnTile<FMT, D>& t, uint32_t key0) const {
     uint32_t bad = 0;
-    if constexpr (FMT == NM_KV_FP16) {
+    if constexpr (FMT != NM_KV_INT8) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         uint32_t any = 0;
 #pragma unroll
-        for (int c = 0; c < S::kWordsV; ++c) any |= non_finite(t.v[e][c]);
+        for (int c = 0; c < S::kWordsV; ++c) any |= non_finite<FMT>(t.v[e][c]);
         bad |= uint32_t(any != 0 && key0 + e >= context) << e;
       }
 #pragma unroll

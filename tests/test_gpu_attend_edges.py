@@ -136,6 +136,26 @@ def test_rows_of_zeros_keep_their_weight_in_the_sum(form, bits):
         close(got[0, 0], want, bound, f"{form} workspace {workspace}")
 
 
+# ---------------------------------------------------------------------------------- odd values
+def test_codes_that_are_not_numbers_stay_with_the_nodes_that_see_them():
+    """e4m3 codes of NaN in a draft's value row, whose scale is a number: the nodes that see the
+    draft get NaN, the others what they had."""
+    rng = np.random.default_rng(80)
+    context, tokens = [37, 0, 20, 95], 6
+    p = Paged(rng, 4, 8, 16, 2, 128, "e4m3")
+    masks = np.tile(np.array([1, 3, 5, 9, 17, 33], np.uint64), (4, 1))
+    args = (up(halves(rng, 4, tokens, 4, 128)), p.cache, up(p.table), context)
+    mask = up(masks.view(np.int64))
+    clean = attend(*args, False, mask=mask)
+    for b in range(4):
+        j = context[b] + 3
+        p.cache.v.view(torch.uint8)[p.table[b, j // 16], :, j % 16, 5 + b] = 0x7F if b % 2 else 0xFF
+    got = attend(*args, False, mask=mask)
+    keep = [0, 1, 2, 4, 5]
+    assert np.array_equal(got[:, keep], clean[:, keep])
+    assert np.isnan(got[:, 3]).all()
+
+
 # ---------------------------------------------------------------------------------- long sums
 @pytest.mark.parametrize("form", list(FORMATS))
 @pytest.mark.parametrize("workspace", [False, True])
