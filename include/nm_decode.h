@@ -167,7 +167,7 @@ int nm_kv_compact(const nm_kv_cache* cache, const int32_t* table, int64_t table_
  * NULL (no split). Its first NM_DECODE_COUNTER_BYTES are counters that must be zero before
  * the first call on it; every call leaves them zero, so one workspace serves any sequence of
  * nm_tree_attention and nm_verify calls in stream order. Fewer bytes than
- * nm_tree_attention_workspace_bytes run as NULL does. Calls that overlap on one workspace
+ * nm_tree_attention_workspace_bytes split as far as they go. Calls that overlap on one workspace
  * race. NM_ERR_SHAPE: tokens outside 1 .. 64, heads not a multiple of kv_heads or above 16
  * times kv_heads or 65536, batch outside 1 .. 65535, batch * kv_heads above 2^23, a scale that
  * is not finite, others as nm_kv_append. */

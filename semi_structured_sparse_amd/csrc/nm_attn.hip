@@ -73,9 +73,13 @@ Plan plan_of(const AttnCall& c, int head_dim, int format, const DeviceInfo& dev)
   return p;
 }
 
+// A slot's partial results.
+size_t slot_bytes(const AttnCall& c, const Plan& p) {
+  return size_t(unsigned(c.cache.kv_heads)) * unsigned(p.row_tiles) * p.part_bytes;
+}
+
 size_t plan_bytes(const AttnCall& c, const Plan& p) {
-  if (p.slots == 0) return 0;
-  return NM_DECODE_COUNTER_BYTES + size_t(p.slots) * unsigned(c.cache.kv_heads) * unsigned(p.row_tiles) * p.part_bytes;
+  return p.slots == 0 ? 0 : NM_DECODE_COUNTER_BYTES + p.slots * slot_bytes(c, p);
 }
 
 }  // namespace
@@ -88,7 +92,10 @@ hipError_t launch_attention(const AttnCall& c, int head_dim, int format, void* w
                             hipStream_t stream, const DeviceInfo& dev) {
   AttnCall a = c;
   Plan p = plan_of(c, head_dim, format, dev);
-  if (workspace == nullptr || workspace_bytes < plan_bytes(c, p)) p.slots = 0;
+  // fewer slots where the workspace holds no more; one a sequence needs none
+  const size_t room = workspace == nullptr || workspace_bytes < NM_DECODE_COUNTER_BYTES
+                          ? 0 : (workspace_bytes - NM_DECODE_COUNTER_BYTES) / slot_bytes(c, p);
+  if (size_t(p.slots) > room) p.slots = room > size_t(c.batch) ? int(room) : 0;
   AttnSplit sp{p.slots, p.row_tiles, static_cast<uint32_t*>(workspace),
                p.slots ? static_cast<char*>(workspace) + NM_DECODE_COUNTER_BYTES : nullptr, p.part_bytes, p.join};
   void* args[] = {&a, &sp};

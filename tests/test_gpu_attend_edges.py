@@ -215,3 +215,45 @@ def test_small_and_uneven_value_scales_keep_their_bits(form, factor):
                                        0.0 if form != "int8" else 128.0 * ks.astype(np.float64))
             assert np.abs(want).min() > 2.0 ** -14
             close(got[b], want, bound, f"{form} {factor} sequence {b}")
+
+
+# --------------------------------------------------------------------------------- workspaces
+def steps(rng, kv, heads, dim, form, width, page=64, batch=1):
+    cache = nm.kv_cache(batch * width, page, kv, dim, FORMATS[form], device=device())
+    rows = up(halves(rng, batch, page * width, kv, dim))
+    table = i32(np.arange(batch * width).reshape(batch, width))
+    nm.nm_kv_append(cache, rows, rows.flip(1).contiguous(), table, i32([0] * batch))
+    return cache, table
+
+
+@pytest.mark.parametrize("form", list(FORMATS))
+@pytest.mark.parametrize("share", [0.9, 0.5, 0.2, 0.02])
+def test_a_small_workspace_splits_as_far_as_it_goes(form, share):
+    """Less than the query's bytes split over fewer workgroups, with the result of the whole to the
+    order of its sums; the partial results stay within what was given."""
+    rng = np.random.default_rng(4)
+    heads, kv, dim, width = 64, 8, 128, 128
+    cache, table = steps(rng, kv, heads, dim, form, width)
+    q = up(halves(rng, 1, 6, heads, dim))
+    full = nm.tree_attention_workspace(q, cache, table)
+    want = nm.nm_tree_attention(q, cache, table, i32([8000]), workspace=full)
+    room = 65536 + int((full.numel() - 65536) * share) // 16 * 16
+    guarded = torch.full((full.numel() + 4096,), 0xA5, dtype=torch.uint8, device=device())
+    guarded[:65536] = 0
+    small = guarded[:room]
+    got = nm.nm_tree_attention(q, cache, table, i32([8000]), workspace=small)
+    torch.cuda.synchronize()
+    assert not guarded[:65536].any() and bool((guarded[room:] == 0xA5).all())
+    assert bool((small[65536:] != 0xA5).any()) == (share > 0.1)
+    alone = nm.nm_tree_attention(q, cache, table, i32([8000]))
+    # both within the roundings of the definition: twice the weights' and the result's half steps,
+    # where values of about one in magnitude cancel
+    worst = 4 * HALF * cache_size(cache)
+    for other in (got, alone):
+        assert (other.float() - want.float()).abs().max().item() <= worst
+
+
+def cache_size(cache):
+    top = cache.v.float().abs().amax((1, 2, 3)) if cache.v_scale is None else \
+        (cache.v.float().abs().amax(-1) * cache.v_scale).amax((1, 2))
+    return float(top.max())
