@@ -177,8 +177,9 @@ int nm_tree_attention(const nm_kv_cache* cache, const uint16_t* q, uint16_t* out
                       const uint64_t* mask, const int32_t* count, int64_t batch, int64_t tokens, float scale,
                       void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace nm_tree_attention uses for these arguments on the current device (0: it
- * takes no split, or the arguments are invalid, or no device). */
+/* Bytes of workspace nm_tree_attention uses at most for these arguments, or for fewer tokens, on
+ * the current device (0: it takes no split, or the arguments are invalid, or no device). So one
+ * workspace, made for the most tokens, serves every step of these sequences. */
 size_t nm_tree_attention_workspace_bytes(const nm_kv_cache* cache, int64_t heads, int64_t table_width,
                                          int64_t batch, int64_t tokens);
 
@@ -222,7 +223,8 @@ int nm_verify_tree(const float* target, const int32_t* tokens, const int32_t* pa
                    const int32_t* count, int32_t* accepted, int32_t* out_tokens, int32_t* path, int64_t batch,
                    int64_t nodes, int64_t vocab, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace the nm_verify calls use for these sizes on the current device (0: none). */
+/* Bytes of workspace the nm_verify calls use at most for these sizes, or for fewer sequences, on
+ * the current device (0: none). */
 size_t nm_verify_workspace_bytes(int64_t batch, int64_t vocab);
 
 #ifdef __cplusplus

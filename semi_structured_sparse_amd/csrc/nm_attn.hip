@@ -84,8 +84,14 @@ size_t plan_bytes(const AttnCall& c, const Plan& p) {
 
 }  // namespace
 
+// The most that a step of as many nodes or fewer takes: fewer nodes may make for smaller row tiles,
+// or fewer of them, and more slots (64 / 8 heads of 128 over 16384 tokens: 8 nodes 8.6 MB, 5 or 6
+// 12.8).
 size_t attention_workspace_bytes(const AttnCall& c, int head_dim, int format, const DeviceInfo& dev) {
-  return plan_bytes(c, plan_of(c, head_dim, format, dev));
+  size_t most = 0;
+  AttnCall a = c;
+  for (a.tokens = 1; a.tokens <= c.tokens; ++a.tokens) most = std::max(most, plan_bytes(a, plan_of(a, head_dim, format, dev)));
+  return most;
 }
 
 hipError_t launch_attention(const AttnCall& c, int head_dim, int format, void* workspace, size_t workspace_bytes,

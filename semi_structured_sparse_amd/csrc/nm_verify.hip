@@ -410,17 +410,22 @@ int counter_step(int64_t batch) {
   return room > 32 ? 32 : int(room);
 }
 
+size_t split_bytes(int64_t batch, int64_t vocab, const DeviceInfo& dev) {
+  return chunks_of(batch, vocab, dev) > 1 ? NM_DECODE_COUNTER_BYTES + size_t(batch) * kMaxParts * sizeof(double) : 0;
+}
+
 }  // namespace
 
+// The most that as many sequences or fewer take: more than two a CU have a workgroup each, unsplit.
 size_t verify_workspace_bytes(int64_t batch, int64_t vocab, const DeviceInfo& dev) {
-  return chunks_of(batch, vocab, dev) > 1 ? NM_DECODE_COUNTER_BYTES + size_t(batch) * kMaxParts * sizeof(double) : 0;
+  return split_bytes(batch < 2 * int64_t(dev.cu_count) ? batch : 2 * int64_t(dev.cu_count), vocab, dev);
 }
 
 hipError_t launch_verify(const VerifyCall& c, void* workspace, size_t workspace_bytes, hipStream_t stream,
                          const DeviceInfo& dev) {
   VerifyCall a = c;
   VerifySplit sp{1, 0, nullptr, nullptr};
-  const size_t need = verify_workspace_bytes(c.batch, c.vocab, dev);
+  const size_t need = split_bytes(c.batch, c.vocab, dev);
   if (need > 0 && workspace != nullptr && workspace_bytes >= need) {
     sp.chunks = chunks_of(c.batch, c.vocab, dev);
     sp.counter_step = counter_step(c.batch);

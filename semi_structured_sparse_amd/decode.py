@@ -334,8 +334,9 @@ def nm_kv_compact(cache: KVCache, block_table, start, path, accepted) -> None:
 
 
 def tree_attention_workspace(q, cache: KVCache, block_table):
-    """A zeroed workspace for nm_tree_attention of these shapes (None where it takes none); it
-    serves any later call that needs no more, and the nm_verify calls, in stream order."""
+    """A zeroed workspace for nm_tree_attention of these shapes (None where it takes none), made once
+    for the largest step: it serves steps of fewer nodes, sequences or pages too, and the nm_verify
+    calls, in stream order (a call that would take more splits as far as it goes)."""
     import torch
     device = _device_of(q, "q")
     c = _cache_arg(cache, device)
@@ -380,7 +381,8 @@ def nm_tree_attention(q, cache: KVCache, block_table, context, mask=None, count=
 
 
 def verify_workspace(batch: int, vocab: int, device=None):
-    """A zeroed workspace for the nm_verify calls of these sizes (None where they take none)."""
+    """A zeroed workspace for the nm_verify calls of these sizes, or fewer sequences (None where they
+    take none)."""
     import torch
     device = torch.device("cuda" if device is None else device)
     with torch.cuda.device(device):

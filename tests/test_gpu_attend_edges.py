@@ -227,6 +227,27 @@ def steps(rng, kv, heads, dim, form, width, page=64, batch=1):
 
 
 @pytest.mark.parametrize("form", list(FORMATS))
+@pytest.mark.parametrize("heads,kv,dim", [(64, 8, 128), (32, 8, 64), (16, 1, 256), (5, 5, 128)])
+def test_a_workspace_serves_every_smaller_step(form, heads, kv, dim):
+    """What a step of 64 nodes over the widest table asks for is enough for steps of fewer nodes,
+    sequences or pages."""
+    wide = nm.kv_cache(4, 64, kv, dim, FORMATS[form], device=device())
+
+    def need(tokens, width, batch):
+        q = torch.empty(batch, tokens, heads, dim, dtype=torch.float16, device=device())
+        ws = nm.tree_attention_workspace(q, wide, torch.zeros(batch, width, dtype=torch.int32, device=device()))
+        return 0 if ws is None else ws.numel()
+
+    for batch, width in ((1, 256), (3, 64), (8, 2048)):
+        most = 0
+        for tokens in range(1, 65):
+            now = need(tokens, width, batch)
+            assert now >= most, f"{tokens} nodes need {now}, fewer {most}"
+            most = now
+        assert need(64, width // 2, batch) <= most and need(64, width, max(1, batch // 2)) <= most
+
+
+@pytest.mark.parametrize("form", list(FORMATS))
 @pytest.mark.parametrize("share", [0.9, 0.5, 0.2, 0.02])
 def test_a_small_workspace_splits_as_far_as_it_goes(form, share):
     """Less than the query's bytes split over fewer workgroups, with the result of the whole to the
@@ -257,3 +278,25 @@ def cache_size(cache):
     top = cache.v.float().abs().amax((1, 2, 3)) if cache.v_scale is None else \
         (cache.v.float().abs().amax(-1) * cache.v_scale).amax((1, 2))
     return float(top.max())
+
+
+def test_a_verification_workspace_serves_fewer_sequences():
+    def need(batch):
+        ws = nm.verify_workspace(batch, 32000)
+        return 0 if ws is None else ws.numel()
+
+    sizes = [need(b) for b in (1, 7, 64, 500, 512, 513, 4000)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    assert nm.verify_workspace(4, 100) is None
+
+
+def test_a_step_takes_the_workspace_of_a_larger_one():
+    """6 nodes with the workspace of 8 and of 64: the same bits as with their own."""
+    rng = np.random.default_rng(6)
+    cache, table = steps(rng, 8, 64, 128, "int8", 256)
+    q = up(halves(rng, 1, 64, 64, 128))
+    few = q[:, :6].contiguous()
+    want = nm.nm_tree_attention(few, cache, table, i32([16000]), workspace=nm.tree_attention_workspace(few, cache, table))
+    for nodes in (8, 64):
+        ws = nm.tree_attention_workspace(q[:, :nodes].contiguous(), cache, table)
+        assert torch.equal(nm.nm_tree_attention(few, cache, table, i32([16000]), workspace=ws), want)
