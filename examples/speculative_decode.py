@@ -49,7 +49,10 @@ class Model:
         self.page, pages = 16, 64
         self.table = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)[None]
         self.caches = [nm.kv_cache(pages, self.page, kv, dim, FORMATS[form]) for _ in range(layers)]
-        self.workspace = None
+        # made once, for the largest step; steps of fewer nodes (the prompt's tokens) use them too
+        step = torch.empty(1, nodes, heads, dim, dtype=torch.float16, device="cuda")
+        self.workspace = nm.tree_attention_workspace(step, self.caches[0], self.table)
+        self.verify_workspace = nm.verify_workspace(1, vocab)
 
     def __call__(self, tokens, positions, context, mask):
         """Probabilities fp32 [1, nodes, vocab] after each node; its k and v go into the caches."""
@@ -59,8 +62,6 @@ class Model:
             fused = layer["qkv"](norm(x)).view(1, nodes, self.heads + 2 * self.kv, self.dim)
             q, k, v = fused.split([self.heads, self.kv, self.kv], dim=2)
             q = nm.nm_rope_kv_append(cache, q, k, v, positions, self.turns, self.table, context)
-            if self.workspace is None:
-                self.workspace = nm.tree_attention_workspace(q, cache, self.table)
             o = nm.nm_tree_attention(q, cache, self.table, context, mask=mask, workspace=self.workspace)
             x = x + layer["out"](o.view(nodes, -1))
             x = x + layer["down"](torch.relu(layer["up"](norm(x))))
@@ -109,7 +110,8 @@ def generate(model, prompt, count, nodes):
         start, tokens = device([context]), device([tokens])
         target = model(tokens, device([[context + d for d in depth]]), start, device([sees], torch.int64))
         uniforms = torch.full((1, nodes), 0.5, device="cuda")
-        accepted, out, path = nm.nm_verify_tree(target, tokens, device([parents]), uniforms)
+        accepted, out, path = nm.nm_verify_tree(target, tokens, device([parents]), uniforms,
+                                                workspace=model.verify_workspace)
         for cache in model.caches:
             nm.nm_kv_compact(cache, model.table, start, path, accepted)
         text += out[0, :int(accepted[0]) + 1].tolist()

@@ -300,3 +300,16 @@ def test_a_step_takes_the_workspace_of_a_larger_one():
     for nodes in (8, 64):
         ws = nm.tree_attention_workspace(q[:, :nodes].contiguous(), cache, table)
         assert torch.equal(nm.nm_tree_attention(few, cache, table, i32([16000]), workspace=ws), want)
+
+
+def test_the_example_makes_its_workspaces_for_its_trees():
+    """What the example hands to the calls is what its largest step asks for."""
+    from examples import speculative_decode as ex
+    nodes = 12
+    model = ex.Model(nodes, "int8")
+    q = torch.empty(1, nodes, model.heads, model.dim, dtype=torch.float16, device=device())
+    need = nm.tree_attention_workspace(q, model.caches[0], model.table)
+    text, _ = ex.generate(model, [1, 5, 9, 1, 5], 8, nodes)
+    assert len(text) == 13 and model.workspace.numel() >= need.numel()
+    few = nm.verify_workspace(1, model.vocab)
+    assert few is None or model.verify_workspace.numel() >= few.numel()
