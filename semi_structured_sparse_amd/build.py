@@ -1,5 +1,6 @@
 """Build libnmsparse.so in place with hipcc for gfx950, and _nmtorch.so, the quick way from torch
-tensors to its decoding calls, with the host compiler.
+tensors to its decoding calls, with the host compiler where that and torch are there (the calls do
+without it, in more time).
 
 Usage: ``python -m semi_structured_sparse_amd.build`` (or call ``build()``).
 """
@@ -10,6 +11,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -43,20 +46,43 @@ def sources() -> list:
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
 
 
+def _host_compiler() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def _rocm() -> str:
+    return os.environ.get("ROCM_PATH", "/opt/rocm")
+
+
+def extension_obstacle() -> str | None:
+    """What the extension would need and is not here; None: it can be built."""
+    try:
+        import torch
+    except ImportError:
+        return "torch is not importable"
+    if shutil.which(_host_compiler()) is None:
+        return f"no host compiler {_host_compiler()}"
+    base = os.path.dirname(torch.__file__)
+    for path in (os.path.join(base, "include", "torch", "csrc", "autograd", "python_variable.h"),
+                 os.path.join(base, "lib", "libc10_hip.so"),
+                 os.path.join(_rocm(), "include", "hip", "hip_runtime_api.h"),
+                 os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(path):
+            return f"no {path}"
+    return None
+
+
 def extension_command(out: str) -> list:
     """The host compiler's command for csrc/nm_torch.cpp, against the installed torch."""
-    import sysconfig
-
     import torch
 
     base = os.path.dirname(torch.__file__)
     inc, lib = os.path.join(base, "include"), os.path.join(base, "lib")
-    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     # the HIP headers, under a host compiler, have to be told the platform
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DUSE_ROCM",
+    return [_host_compiler(), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DUSE_ROCM",
             "-D__HIP_PLATFORM_AMD__", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             f"-I{INCLUDE}", "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-            "-isystem", os.path.join(rocm, "include"), "-isystem", sysconfig.get_paths()["include"],
+            "-isystem", os.path.join(_rocm(), "include"), "-isystem", sysconfig.get_paths()["include"],
             os.path.join(CSRC, "nm_torch.cpp"), "-o", out, f"-L{lib}", "-lc10", "-lc10_hip", "-ltorch_cpu",
             "-ltorch_python", f"-Wl,-rpath,{lib}"]
 
@@ -77,7 +103,16 @@ def build_extension(verbose: bool = False) -> str:
 
 def build(verbose: bool = False) -> str:
     """Compile every HIP source into PKG_DIR/libnmsparse.so, and the torch extension beside it
-    (always recompiles)."""
+    (always recompiles). Where the extension cannot be built here, an earlier one is taken away and
+    a warning says why; one that does not compile is an error."""
+    obstacle = extension_obstacle()
+    if obstacle is not None:
+        earlier = os.path.join(PKG_DIR, EXT_NAME)
+        if os.path.exists(earlier):
+            os.remove(earlier)
+        warnings.warn(f"_nmtorch.so is not built: {obstacle}; the decoding calls go through decode.py's own checks",
+                      RuntimeWarning, stacklevel=2)
+        return build_library(verbose)
     with ThreadPoolExecutor(1) as pool:      # the extension while hipcc works
         extension = pool.submit(build_extension, verbose)
         out = build_library(verbose)

@@ -4,13 +4,15 @@ the attention of drafted trees, chains or single tokens over it, and the verific
 drafts. Argument marshalling only, as in the rest of the package; every step runs in the HIP
 kernels of libnmsparse.so. A call goes through _nmtorch.so (csrc/nm_torch.cpp), which does the
 same in a fifth of the time; what that does not take (a refusal, tensors of a device that is not
-the current one) goes through the checks here, which raise or make the call.
+the current one, or all of them where the extension is not built) goes through the checks here,
+which raise or make the call.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
 import math
+import warnings
 from typing import NamedTuple, Optional
 
 _c = ctypes
@@ -163,6 +165,13 @@ _QUICK = ("nm_rope", "nm_kv_append", "nm_rope_kv_append", "nm_kv_read", "nm_kv_c
           "nm_verify_chain", "nm_verify_tree")
 
 
+class _Absent:
+    """Stands for the extension where it does not load, and takes no call."""
+
+    def __getattr__(self, name):
+        return lambda *args: NotImplemented
+
+
 def _bound():
     global _quick
     if _quick is None:
@@ -170,8 +179,10 @@ def _bound():
         try:
             from . import _nmtorch
         except ImportError as e:
-            raise RuntimeError(f"_nmtorch.so does not load ({e}); build it with "
-                               "python -m semi_structured_sparse_amd.build") from e
+            warnings.warn(f"_nmtorch.so does not load ({e}): the decoding calls take longer on the host; build it with "
+                          "python -m semi_structured_sparse_amd.build", RuntimeWarning, stacklevel=3)
+            _quick = _Absent()
+            return _quick
         _nmtorch.bind(*(_c.cast(getattr(lib, name), _c.c_void_p).value for name in _QUICK))
         _quick = _nmtorch
     return _quick
