@@ -192,6 +192,30 @@ def test_long_sums_of_values_that_cancel(form, workspace):
     close(got[0], want, np.abs(want) * (HALF + 2.0 ** -12 + 2.0 ** -20) + TINY, f"{form} {workspace}")
 
 
+@pytest.mark.parametrize("form", list(FORMATS))
+@pytest.mark.parametrize("keys,rows", [(20011, 1), (40001, 9), (131071, 16)])
+def test_every_tile_counts_once(form, keys, rows):
+    """Values that mark their tile: a tile of 32 keys left out, or taken twice, moves a result by one
+    over the number of tiles that share its dim, 10% where the bound is 0.4% at most."""
+    say(f"markers {form} {keys} {rows}")
+    rng = np.random.default_rng(keys)
+    kv, dim = 1, 128 if keys < 100000 else 256
+    k = rng.standard_normal((keys, kv, dim)).astype(np.float16).astype(np.float64)
+    v, ks, vs = markers(keys, kv, dim), None, None
+    if form != "fp16":
+        ks, vs = np.full((keys, kv), 2.0 ** -6, np.float32), np.full((keys, kv), 1 / 64, np.float32)
+        k, v = np.round(k * 16) * 4 % 64, v * 64.0     # whole numbers that e4m3 holds: multiples of 4 below 64
+    q = (halves(rng, 1, 1, rows, dim) * np.float16(0.125)).astype(np.float16)
+    values = v * (1.0 if vs is None else vs[..., None].astype(np.float64))
+    keyed = k * (1.0 if ks is None else ks[..., None].astype(np.float64))
+    want, bound = attend_exact(q[0], keyed, values, np.ones((1, keys), bool), dim ** -0.5, vs,
+                               0.0 if form != "int8" else 128.0 * ks)
+    cache, table = cache_of(k, v, form, 64, ks, vs)
+    for workspace in (False, True):
+        got = attend(up(q), cache, table, [keys - 1], workspace)
+        close(got[0], want, bound, f"{form} {keys} workspace {workspace}")
+
+
 @pytest.mark.parametrize("form", ["int8", "e4m3"])
 @pytest.mark.parametrize("factor", [2.0 ** -5, 1.0, 2.0 ** 6])
 def test_small_and_uneven_value_scales_keep_their_bits(form, factor):
