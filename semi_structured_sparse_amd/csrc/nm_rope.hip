@@ -1,10 +1,10 @@
 // Rotary positions (nm_rope) and the host table of their frequencies (nm_rope_turns).
 //
 // Mathematics: each pair of a head's rotated elements is turned by 2 pi pos turns_i. The product
-// and its fraction of a turn are worked out in 64 bits (a position near 2^20 times a rate in
-// fp32 would be off by 2^-4 of a turn), the cosine and sine of that fraction in fp32 by the
-// instructions that take one, the turn in fp32, rounded once. What bounds it: the copy, 4 bytes
-// an element; the angles are the costly part, one 64-bit product, rounding and difference each.
+// and its fraction of a turn are worked out in 64 bits, the cosine and sine of that fraction and
+// the turn in fp32, rounded once (rotation() in nm_decode_internal.h). What bounds it: the copy, 4
+// bytes an element; the angles are the costly part, five operations in 64 bits and some 25 in 32
+// each.
 #include <algorithm>
 #include <cmath>
 
