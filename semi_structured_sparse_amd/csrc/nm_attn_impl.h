@@ -31,11 +31,11 @@
 // What bounds it, with times on one GPU (a pure read of the same bytes reaches 7.0 TB/s, a large
 // copy 4.8):
 //   - few tokens over long contexts: reading the cache. 32 sequences of up to 8192 int8 tokens, 8
-//     key heads of 128, one token each of 32 heads (353 MB): 68.5 us, 5.2 TB/s. Three workgroups a
-//     CU hold 100 KB in flight there; the vector units are busy 28% of the time.
+//     key heads of 128, one token each of 32 heads (353 MB): 69.1 us, 5.1 TB/s. Three workgroups a
+//     CU hold 100 KB in flight there; the vector units are busy 30% of the time.
 //   - many rows: a tile's vector work (codes to fp16, scales, softmax) and its waits on LDS, at two
-//     workgroups a CU. 2 x 131071 int8 tokens, 8 nodes, 40 heads (450 MB, 33 GFLOP): 102.7 us; 4
-//     x 64 nodes over 8192 int8 tokens, 64 heads: 120 us, 375 TFLOP/s.
+//     workgroups a CU. 2 x 131071 int8 tokens, 8 nodes, 40 heads (450 MB, 33 GFLOP): 97 to 102 us; 4
+//     x 64 nodes over up to 8192 int8 tokens, 64 heads: 125 us, 360 TFLOP/s.
 //   - short work: the chain of dependent steps, lengths and page table 2, first tile 3, exchange
 //     0.5, partial and count 2.5, join 2 us. One token over 777 fp16 tokens: 11 us.
 #pragma once

@@ -181,7 +181,7 @@ __device__ __forceinline__ void rotation(int pos, double turns, float scale, flo
 // A unit of a head: 16 elements, as two runs of 8 that lie half of the rotated part, or half of
 // the rest, apart. So the pairs of NM_ROPE_HALF are the runs' elements (those of the other layout
 // are neighbours in a run), and neighbouring threads' loads and stores are neighbours in memory:
-// 8191 tokens of 72 heads turned in 54.1 us, 56.4 with runs that lie together.
+// with runs that lie together 8191 tokens of 72 heads took 2.3 us longer, of 55.
 struct HeadUnit {
   int first, second;   // where the runs start
   bool turned;

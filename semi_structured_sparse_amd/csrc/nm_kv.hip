@@ -70,9 +70,10 @@ __device__ __forceinline__ u32x2 codes_of(const float (&e)[8], float up) {
 // magnitude is a maximum over its lanes, its scale an exact division. What bounds it: the copy, 2
 // bytes an element in, 1 or 2 out, and behind it about as long in instructions, two divisions, a
 // maximum and a rounding for 16 elements a lane. 14337 of 16384 tokens, 8 + 8 heads of 128, to
-// int8 (89 MB): 19.6 us, 4.5 TB/s (24.0 with clamped conversions to integers and a comparison
-// an element for infinities, 1 of it by looking the page up only once the elements have come);
-// one rotated token of 16 sequences 3.4 us.
+// int8 (89 MB): 20.6 us, 4.3 TB/s (19.8 before the angles took registers of the eighth wave of
+// a SIMD; held to eight, turned prompts take 3% longer; 24.0 before with clamped conversions to
+// integers and a comparison an element for infinities, 1 of it by looking the page up only once the
+// elements have come); one rotated token of 16 sequences 3.9 us.
 template <int D, int FMT>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendCall a) {
   constexpr int kLanes = RowLanes<D>::kLanes;
@@ -154,7 +155,7 @@ __device__ __forceinline__ void decode4(uint32_t codes, float (&y)[4]) {
 }
 
 // D / 16 lanes per (token, head) row of k, then of v; a copy, widened to fp16: 16 bytes of codes
-// a lane in, 32 out. 14337 int8 tokens of 8 + 8 heads into 16384 (97 MB): 17.8 us, 5.4 TB/s.
+// a lane in, 32 out. 14337 int8 tokens of 8 + 8 heads into 16384 (97 MB): 17.6 us, 5.5 TB/s.
 template <int D, int FMT>
 __global__ __launch_bounds__(kThreads) void read_kernel(ReadCall a) {
   constexpr int kLanes = RowLanes<D>::kLanes;

@@ -17,7 +17,7 @@ constexpr int kThreads = 256;
 constexpr int64_t kGridThreads = int64_t(1) << 31;
 
 // Any head size, stride and alignment: one pair (or, past the rotated part, two elements) per
-// thread, which works out its angle: 189 us for the 8191 tokens of 72 heads below.
+// thread, which works out its angle: 184 us for the 8191 tokens of 72 heads below.
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeCall a) {
   const int units = (a.head_dim + 1) / 2, pairs = a.rope.rot_dim / 2;
   const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
@@ -44,9 +44,9 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeCall a) {
 // Heads of whole 16-element units with 16-byte alignment. A thread keeps one unit's cosines and
 // sines and turns that unit of every `step`-th head of its token, so that they are worked out
 // once for several heads; what is left is a copy, two 16-byte loads and stores a unit. 8191
-// tokens x 72 heads x 128 elements (302 MB read and written): 54.1 us, 5.6 TB/s, where a large
-// copy reaches 4.8; 8 tokens x 40 heads 2.8 us, an empty launch's time. Loads that bypass the
-// caches made the large one 57.8 us, such stores too 65.2.
+// tokens x 72 heads x 128 elements (302 MB read and written): 55.0 us, 5.5 TB/s, where a large
+// copy reaches 4.8; 8 tokens x 40 heads 3.1 us, where an empty launch takes 2.6. Loads that bypass
+// the caches made the large one 4 us longer, such stores too 11.
 __global__ __launch_bounds__(kThreads) void rope_wide_kernel(RopeCall a, int units, int step, int each) {
   const int unit = threadIdx.x % units, h0 = blockIdx.y * each + threadIdx.x / units;
   const int64_t token = blockIdx.x;

@@ -1,6 +1,7 @@
 // The quick way from torch tensors to the calls of nm_decode.h: a Python extension that checks
-// the arguments as decode.py does, makes the outputs and calls the library, in 1 to 2 us where
-// the same in Python takes 6 to 12 (a decoding step makes three such calls a layer). Each
+// the arguments as decode.py does, makes the outputs and calls the library, in 3 to 6 us of the
+// host where decode.py alone takes 9 to 16, launch and outputs' allocation included (4 is what
+// torch takes to fill an empty tensor; a decoding step makes three such calls a layer). Each
 // function returns NotImplemented where anything is not as it should be (a check that fails, a
 // tensor on another device than the current one, memory that runs out, a call that the library
 // refuses); decode.py then goes its own way, whose checks say what it is. Nothing here touches

@@ -3,9 +3,9 @@ speculative decoding step. Rotary positions, a paged key/value cache in fp16, in
 the attention of drafted trees, chains or single tokens over it, and the verification of the
 drafts. Argument marshalling only, as in the rest of the package; every step runs in the HIP
 kernels of libnmsparse.so. A call goes through _nmtorch.so (csrc/nm_torch.cpp), which does the
-same in a fifth of the time; what that does not take (a refusal, tensors of a device that is not
-the current one, or all of them where the extension is not built) goes through the checks here,
-which raise or make the call.
+same in a third to half of the host's time; what that does not take (a refusal, tensors of a
+device that is not the current one, all calls where the extension is not built) goes through the
+checks here, which raise or make the call.
 """
 from __future__ import annotations
 
