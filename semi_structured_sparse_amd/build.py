@@ -12,6 +12,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import tempfile
 import warnings
 from concurrent.futures import ThreadPoolExecutor
 
@@ -28,7 +29,6 @@ HIP_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # Packed-FP32 instructions are kept out of the generated code on this platform.
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -120,19 +120,33 @@ def build(verbose: bool = False) -> str:
     return out
 
 
+def _workers() -> int:
+    """Compilers at once: MAX_JOBS, else the CPUs of this process, up to 16."""
+    return max(1, min(16, int(os.environ.get("MAX_JOBS") or len(os.sched_getaffinity(0)))))
+
+
 def build_library(verbose: bool = False) -> str:
-    """Compile every HIP source into PKG_DIR/libnmsparse.so (always recompiles)."""
+    """Compile every HIP source into PKG_DIR/libnmsparse.so (always recompiles): a compiler for each
+    source, several at once, then the link."""
     out = os.path.join(PKG_DIR, LIB_NAME)
     tmp = out + ".tmp"
-    cmd = [hipcc(), *HIP_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", *sources(), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+
+    def run(cmd) -> str:
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        return res.stderr
+
+    with tempfile.TemporaryDirectory() as place, ThreadPoolExecutor(_workers()) as pool:
+        objects = {src: os.path.join(place, os.path.basename(src) + ".o") for src in sources()}
+        said = list(pool.map(lambda src: run([hipcc(), *HIP_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-c", src, "-o",
+                                              objects[src]]), objects))
+        said.append(run([hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared", *objects.values(), "-o", tmp]))
     # the host pass does not know the packed-fp32 target feature and says so; drop that noise
     noise = ("packed-fp32-ops", "is not a recognized feature", "--hip-link")
-    msgs = [l for l in res.stderr.splitlines() if l.strip() and not any(n in l for n in noise)]
+    msgs = [l for err in said for l in err.splitlines() if l.strip() and not any(n in l for n in noise)]
     if msgs and verbose:
         print("\n".join(msgs), file=sys.stderr)
     os.replace(tmp, out)
