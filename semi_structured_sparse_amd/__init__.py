@@ -3,8 +3,9 @@
 Argument marshalling only: every step runs in the HIP kernels of the library; torch
 provides device memory and the current stream. The names follow the C ABI in
 include/nm_sparse.h (nm_pack, nm_spmv, nm_gemv_dense, ...); decode.py binds what stands
-between the products of a decoding step (include/nm_decode.h). There is no CPU
-fallback: if the library is not built, every call raises.
+between the products of a decoding step (include/nm_decode.h), block.py what a transformer
+block does around them (include/nm_block.h). There is no CPU fallback: if the library is not
+built, every call raises.
 """
 from __future__ import annotations
 
@@ -12,6 +13,8 @@ import ctypes
 import os
 import threading
 
+from .block import (LogProbs, MAX_TOP, SIGNATURES as _BLOCK_SIGNATURES, gated_workspace, linear_workspace,  # noqa: F401
+                    logprobs_workspace, nm_block_norm, nm_gated, nm_linear, nm_logprobs, nm_norm)
 from .decode import (KVCache, MAX_NODES, NM_ERR_FORMAT, SIGNATURES as _DECODE_SIGNATURES, kv_cache,  # noqa: F401
                      nm_kv_append, nm_kv_compact, nm_kv_read, nm_rope, nm_rope_kv_append, nm_tree_attention,
                      nm_verify_chain, nm_verify_tree, rope_turns, tree_attention_workspace, verify_workspace)
@@ -70,6 +73,7 @@ SIGNATURES = {
                                         _c.c_int, _c.c_int, _c.c_void_p]),
     "nm_probe_copy": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     **_DECODE_SIGNATURES,
+    **_BLOCK_SIGNATURES,
 }
 
 _lib = None

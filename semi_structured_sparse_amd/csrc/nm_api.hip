@@ -102,10 +102,10 @@ bool prefill_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, cons
 // 25.9 and 16.7; 1024 x 8192 at 64 12.3 against 48.7 and 46.3; 4096 x 14336 4:8 at 64 30.7
 // against 97.2 and 106; 14336 x 4096 at 64 26.8 against 27.9. At 16 vectors and below one
 // skinny launch is as fast or faster (4096 x 4096 2:4: 9.2 against 11.9).
-bool colsplit_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev) {
+bool colsplit_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev, bool gated) {
   const bool size = batch > kSkinnyBatch || (N == 16 && batch >= kExpandColSplitMinBatch &&
-                                             rows <= kExpandColSplitMaxRows);
-  return size && prefill_pattern(N, M) && prefill_workspace_bytes(rows, cols, batch, N, dev) > 0;
+                                             (gated ? 2 * rows : rows) <= kExpandColSplitMaxRows);
+  return size && prefill_pattern(N, M) && prefill_workspace_bytes(rows, cols, batch, N, dev, gated) > 0;
 }
 
 // nm_spmm's argument checks, before any HIP call.
@@ -121,27 +121,41 @@ int spmm_check(const uint16_t* values, const uint32_t* masks, const uint16_t* X,
   return NM_OK;
 }
 
-// nm_spmm's dispatch, with an optional workspace for the skinny kernels' column splits.
+// nm_spmm's dispatch, with an optional workspace for the column splits; e: nm_linear's or nm_gated's
+// further arguments. A gated product takes the route of the rows of both matrices.
 int spmm_dispatch(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y, int64_t rows,
-                  int64_t cols, int64_t batch, int N, int M, void* stream, void* workspace, size_t workspace_bytes) {
+                  int64_t cols, int64_t batch, int N, int M, void* stream, void* workspace, size_t workspace_bytes,
+                  const BlockArgs* e) {
   const int st = spmm_check(values, masks, X, Y, rows, cols, batch, N, M);
   if (st != NM_OK) return st;
   if (!aligned(workspace, 16)) return NM_ERR_ALIGN;
   DeviceInfo dev;
-  hipError_t e = current_device_info(&dev);
-  if (e != hipSuccess) return hip_fail(e);
-  if (workspace != nullptr && colsplit_route(rows, cols, batch, N, M, dev) &&
-      workspace_bytes >= prefill_workspace_bytes(rows, cols, batch, N, dev)) {
+  hipError_t err = current_device_info(&dev);
+  if (err != hipSuccess) return hip_fail(err);
+  const bool gated = form_of(e) == kGatedForm;
+  const int64_t all = rows_read(rows, e);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  // launches of `count` vectors from b0 on
+  auto small = [&](int64_t b0, int64_t count) {
+    const BlockArgs part = e ? from_vector(*e, b0, rows) : BlockArgs{};
+    return launch_spmm(values, masks, X + b0 * cols, Y + b0 * rows, rows, cols, int(count), N, M, s, dev,
+                       e ? &part : nullptr);
+  };
+  auto skinny = [&](int64_t b0, int64_t count, void* ws, size_t ws_bytes) {
+    const BlockArgs part = e ? from_vector(*e, b0, rows) : BlockArgs{};
+    return launch_skinny_spmm(values, masks, X + b0 * cols, Y + b0 * rows, rows, cols, int(count), N, M, s, dev, ws,
+                              ws_bytes, e ? &part : nullptr);
+  };
+  if (workspace != nullptr && colsplit_route(rows, cols, batch, N, M, dev, gated) &&
+      workspace_bytes >= prefill_workspace_bytes(rows, cols, batch, N, dev, gated)) {
     // column-split prefill product (launch_prefill_spmm takes the split with this workspace)
-    e = launch_prefill_spmm(values, masks, X, Y, rows, cols, batch, N, M, static_cast<hipStream_t>(stream), dev,
-                            workspace, workspace_bytes);
-    return e == hipSuccess ? NM_OK : hip_fail(e);
+    err = launch_prefill_spmm(values, masks, X, Y, rows, cols, batch, N, M, s, dev, workspace, workspace_bytes, e);
+    return err == hipSuccess ? NM_OK : hip_fail(err);
   }
-  if (prefill_route(rows, cols, batch, N, M, dev)) {  // matrix-core prefill product
-    if (!prefill_fits(rows, cols, batch)) return NM_ERR_SHAPE;
-    e = launch_prefill_spmm(values, masks, X, Y, rows, cols, batch, N, M, static_cast<hipStream_t>(stream), dev,
-                            workspace, workspace_bytes);
-    return e == hipSuccess ? NM_OK : hip_fail(e);
+  if (prefill_route(all, cols, batch, N, M, dev)) {  // matrix-core prefill product
+    if (!prefill_fits(all, cols, batch)) return NM_ERR_SHAPE;
+    err = launch_prefill_spmm(values, masks, X, Y, rows, cols, batch, N, M, s, dev, workspace, workspace_bytes, e);
+    return err == hipSuccess ? NM_OK : hip_fail(err);
   }
   if (M != 2 * N && cols > max_cols_for(dev)) return NM_ERR_TOO_WIDE;  // 25%: single-vector kernel only
   if (N == 16 && M == 32 && batch >= kSkinnyMinBatch) {
@@ -150,57 +164,48 @@ int spmm_dispatch(const uint16_t* values, const uint32_t* masks, const uint16_t*
     // vectors at a time
     for (int64_t b0 = 0; b0 < batch; b0 += kSkinnyBatch) {
       const int64_t nb = batch - b0 < kSkinnyBatch ? batch - b0 : kSkinnyBatch;
-      if (skinny_expand_chunk(rows, cols, nb, dev)) {
-        e = launch_skinny_spmm(values, masks, X + b0 * cols, Y + b0 * rows, rows, cols, int(nb), N, M,
-                               static_cast<hipStream_t>(stream), dev);
-        if (e != hipSuccess) return hip_fail(e);
+      if (skinny_expand_chunk(all, cols, nb, dev)) {
+        err = skinny(b0, nb, nullptr, 0);
+        if (err != hipSuccess) return hip_fail(err);
         continue;
       }
       for (int64_t c0 = b0; c0 < b0 + nb; c0 += kSmallBatch) {
-        const int nc = int(b0 + nb - c0 < kSmallBatch ? b0 + nb - c0 : kSmallBatch);
-        e = launch_spmm(values, masks, X + c0 * cols, Y + c0 * rows, rows, cols, nc, N, M,
-                        static_cast<hipStream_t>(stream), dev);
-        if (e != hipSuccess) return hip_fail(e);
+        err = small(c0, b0 + nb - c0 < kSmallBatch ? b0 + nb - c0 : kSmallBatch);
+        if (err != hipSuccess) return hip_fail(err);
       }
     }
     return NM_OK;
   }
-  if (use_skinny(rows, cols, batch < kSkinnyBatch ? batch : kSkinnyBatch, N, M, dev)) {
+  if (use_skinny(all, cols, batch < kSkinnyBatch ? batch : kSkinnyBatch, N, M, dev)) {
     // 50% patterns at 5..31 vectors where measured faster: the matrix instructions, 16
     // vectors per launch (launches in stream order, so one workspace serves them all); a
     // last launch too small for them (17..20 vectors leave 1..4) runs on the small-batch kernel
     for (int64_t b0 = 0; b0 < batch; b0 += kSkinnyBatch) {
-      const int nb = int(batch - b0 < kSkinnyBatch ? batch - b0 : kSkinnyBatch);
-      if (use_skinny(rows, cols, nb, N, M, dev)) {
-        e = launch_skinny_spmm(values, masks, X + b0 * cols, Y + b0 * rows, rows, cols, nb, N, M,
-                               static_cast<hipStream_t>(stream), dev, workspace, workspace_bytes);
+      const int64_t nb = batch - b0 < kSkinnyBatch ? batch - b0 : kSkinnyBatch;
+      if (use_skinny(all, cols, nb, N, M, dev)) {
+        err = skinny(b0, nb, workspace, workspace_bytes);
       } else {
-        e = launch_spmm(values, masks, X + b0 * cols, Y + b0 * rows, rows, cols, nb < kSmallBatch ? nb : int(kSmallBatch),
-                        N, M, static_cast<hipStream_t>(stream), dev);
-        if (e == hipSuccess && nb > kSmallBatch)
-          e = launch_spmm(values, masks, X + (b0 + kSmallBatch) * cols, Y + (b0 + kSmallBatch) * rows, rows, cols,
-                          int(nb - kSmallBatch), N, M, static_cast<hipStream_t>(stream), dev);
+        err = small(b0, nb < kSmallBatch ? nb : kSmallBatch);
+        if (err == hipSuccess && nb > kSmallBatch) err = small(b0 + kSmallBatch, nb - kSmallBatch);
       }
-      if (e != hipSuccess) return hip_fail(e);
+      if (err != hipSuccess) return hip_fail(err);
     }
     return NM_OK;
   }
   // otherwise (fewer vectors, smaller layers, most 16:32 shapes): the small-batch kernel on consecutive
   // groups of kSmallBatch rows of X (X and Y rows are contiguous)
   for (int64_t b0 = 0; b0 < batch; b0 += kSmallBatch) {
-    const int nb = int(batch - b0 < kSmallBatch ? batch - b0 : kSmallBatch);
-    e = launch_spmm(values, masks, X + b0 * cols, Y + b0 * rows, rows, cols, nb, N, M,
-                    static_cast<hipStream_t>(stream), dev);
-    if (e != hipSuccess) return hip_fail(e);
+    err = small(b0, batch - b0 < kSmallBatch ? batch - b0 : kSmallBatch);
+    if (err != hipSuccess) return hip_fail(err);
   }
   return NM_OK;
 }
 
 // Workspace bytes spmm_dispatch can use for the product (0 when it would not use one).
-size_t spmm_workspace_bytes(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev) {
+size_t spmm_workspace_bytes(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev, bool gated) {
   if (!valid_shape(rows, cols) || !valid_pattern(N, M) || batch < 1 || batch > kPrefillMaxTokens) return 0;
-  if (colsplit_route(rows, cols, batch, N, M, dev)) return prefill_workspace_bytes(rows, cols, batch, N, dev);
-  if (prefill_route(rows, cols, batch, N, M, dev)) return 0;
+  if (colsplit_route(rows, cols, batch, N, M, dev, gated)) return prefill_workspace_bytes(rows, cols, batch, N, dev, gated);
+  if (gated || prefill_route(rows, cols, batch, N, M, dev)) return 0;
   if (!use_skinny(rows, cols, batch < kSkinnyBatch ? batch : kSkinnyBatch, N, M, dev)) return 0;
   return skinny_workspace_bytes(rows, cols, int(batch < kSkinnyBatch ? batch : kSkinnyBatch), N, dev);
 }
@@ -453,7 +458,7 @@ const char* nm_status_string(int status) {
     case NM_ERR_TOO_WIDE: return "cols too large: x does not fit in the LDS of one workgroup";
     case NM_ERR_HIP: return "a HIP runtime call failed";
     case NM_ERR_SCRATCH: return "the column split of this shape needs more than the library's static scratch";
-    case NM_ERR_FORMAT: return "unsupported cache format, rotary layout, head size or page size (nm_decode.h)";
+    case NM_ERR_FORMAT: return "unsupported cache format, rotary layout, head size or page size (nm_decode.h), activation or norm (nm_block.h)";
     default: return "unknown status";
   }
 }

@@ -28,6 +28,30 @@ void set_last_hip_error(hipError_t e);
 hipError_t launch(const void* kernel, dim3 grid, dim3 block, void** args, size_t lds,
                   hipStream_t stream, const DeviceInfo& dev);
 
+// What a product does with its sums before it rounds them (nm_linear), or the second matrix
+// that it multiplies and what it makes of both sums (nm_gated); the kernels' forms are in
+// nm_epilogue.h. NULL biases and residual are left out.
+enum BlockForm { kPlainForm = 0, kLinearForm = 1, kGatedForm = 2 };
+struct BlockArgs {
+  const uint16_t* up_values;   // nm_gated: the matrix whose product the activated one multiplies
+  const uint32_t* up_masks;
+  const uint16_t* bias;        // [rows] (nm_gated: the gate's)
+  const uint16_t* up_bias;
+  const uint16_t* residual;    // [batch][rows], may be Y
+  float scale;
+  int activation;
+};
+// e NULL: the plain product.
+inline int form_of(const BlockArgs* e) { return e == nullptr ? kPlainForm : e->up_values ? kGatedForm : kLinearForm; }
+// A gated product reads the rows of two matrices: the rows that the routing and the launch shapes go by.
+inline int64_t rows_read(int64_t rows, const BlockArgs* e) { return form_of(e) == kGatedForm ? 2 * rows : rows; }
+// The arguments for the vectors from b0 on.
+inline BlockArgs from_vector(const BlockArgs& e, int64_t b0, int64_t rows) {
+  BlockArgs r = e;
+  if (r.residual != nullptr) r.residual += b0 * rows;
+  return r;
+}
+
 // Kernel launchers (arguments already validated by the API layer).
 hipError_t launch_pack(const uint16_t* W, uint16_t* values, uint32_t* masks, int64_t rows,
                        int64_t cols, int N, int M, hipStream_t stream, const DeviceInfo& dev);
@@ -35,7 +59,7 @@ hipError_t launch_unpack(const uint16_t* values, const uint32_t* masks, uint16_t
                          int N, int M, hipStream_t stream, const DeviceInfo& dev);
 hipError_t launch_spmv(const uint16_t* values, const uint32_t* masks, const uint16_t* x,
                        uint16_t* y, int64_t rows, int64_t cols, int N, int M, hipStream_t stream,
-                       const DeviceInfo& dev);
+                       const DeviceInfo& dev, const BlockArgs* e = nullptr);
 hipError_t launch_gemv(const uint16_t* W, const uint16_t* x, uint16_t* y, int64_t rows,
                        int64_t cols, hipStream_t stream, const DeviceInfo& dev);
 
@@ -59,7 +83,7 @@ constexpr int64_t kSmallBatch = 8;
 constexpr int64_t kMatrixCoreMinBatch = 32;
 hipError_t launch_spmm(const uint16_t* values, const uint32_t* masks, const uint16_t* X,
                        uint16_t* Y, int64_t rows, int64_t cols, int batch, int N, int M,
-                       hipStream_t stream, const DeviceInfo& dev);
+                       hipStream_t stream, const DeviceInfo& dev, const BlockArgs* e = nullptr);
 hipError_t launch_gemm(const uint16_t* W, const uint16_t* X, uint16_t* Y, int64_t rows,
                        int64_t cols, int batch, hipStream_t stream, const DeviceInfo& dev);
 
@@ -96,10 +120,12 @@ bool prefill_pattern(int n, int m);
 // unsplit. The counters must be zero before the launch, which leaves them zero (the same
 // counter region as the skinny kernels' column splits, so one workspace serves both in
 // stream order). n: the pattern's N (the split kernels and their costs depend on it).
-size_t prefill_workspace_bytes(int64_t rows, int64_t cols, int64_t tokens, int n, const DeviceInfo& dev);
+size_t prefill_workspace_bytes(int64_t rows, int64_t cols, int64_t tokens, int n, const DeviceInfo& dev,
+                               bool gated = false);
 hipError_t launch_prefill_spmm(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y,
                                int64_t rows, int64_t cols, int64_t tokens, int n, int m, hipStream_t stream,
-                               const DeviceInfo& dev, void* workspace = nullptr, size_t workspace_bytes = 0);
+                               const DeviceInfo& dev, void* workspace = nullptr, size_t workspace_bytes = 0,
+                               const BlockArgs* e = nullptr);
 // Bytes at the start of a workspace that hold the column splits' per-tile counters (fixed
 // per device, so that every shape finds its counters where earlier launches left zeros).
 size_t counter_bytes(const DeviceInfo& dev);
@@ -121,7 +147,8 @@ bool skinny_fits(int64_t rows, int64_t cols, int64_t tokens, int n, int m, const
 size_t skinny_workspace_bytes(int64_t rows, int64_t cols, int tokens, int n, const DeviceInfo& dev);
 hipError_t launch_skinny_spmm(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y,
                               int64_t rows, int64_t cols, int tokens, int n, int m, hipStream_t stream,
-                              const DeviceInfo& dev, void* workspace = nullptr, size_t workspace_bytes = 0);
+                              const DeviceInfo& dev, void* workspace = nullptr, size_t workspace_bytes = 0,
+                              const BlockArgs* e = nullptr);
 // nm_spmm runs the skinny kernel, kSkinnyBatch vectors per launch, from kSkinnyMinBatch
 // vectors up to kMatrixCoreMinBatch, where the prefill kernels take over: on layers of at
 // least kSkinnyMinRows rows for 2:4, 4:8 and 8:16; on smaller layers (down to
@@ -172,8 +199,10 @@ int spmm_check(const uint16_t* values, const uint32_t* masks, const uint16_t* X,
 // skinny kernels split the columns of short layers, and batches of more than kSkinnyBatch
 // vectors take the column-split prefill kernel where colsplit_route says so.
 int spmm_dispatch(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y, int64_t rows,
-                  int64_t cols, int64_t batch, int N, int M, void* stream, void* workspace, size_t workspace_bytes);
-size_t spmm_workspace_bytes(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev);
+                  int64_t cols, int64_t batch, int N, int M, void* stream, void* workspace, size_t workspace_bytes,
+                  const BlockArgs* e = nullptr);
+size_t spmm_workspace_bytes(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev,
+                            bool gated = false);
 
 // Whether nm_spmm runs a batch on the prefill kernels (else on skinny or small-batch launches).
 bool prefill_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev);
@@ -183,7 +212,18 @@ int64_t prefill_min_batch(int N);
 // column-split prefill kernel: 50% batches of more than kSkinnyBatch vectors whose
 // small-tile grid leaves CUs idle or that split better over taller tiles, and the 16:32
 // batches above on small layers.
-bool colsplit_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev);
+bool colsplit_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev, bool gated = false);
+
+// The block products' kernels of a form, by the choices that the launchers make for the plain ones
+// (modes: 0 2:4 directly, 1 split, 2 expanded; gated: ci 1, tr even, no skinny column split).
+const void* block_spmv_kernel_for(int form, int N, int dec, int ci);
+const void* block_spmv_quarter_kernel_for(int form);
+const void* block_spmm_linear_kernel_for(int N, int batch, int ci);
+const void* block_spmm_gated_kernel_for(int N, int batch);
+const void* block_skinny_kernel_for(int form, int mode);
+const void* block_skinny_colsplit_kernel_for(int mode);
+const void* block_prefill_linear_kernel_for(int mode, int tr, int tt, bool colsplit);
+const void* block_prefill_gated_kernel_for(int mode, int tr, int tt, bool colsplit);
 
 // Name of the kernel configuration the prefill launchers pick (static string).
 // (sparse: n = the pattern's N, 2, 4, 8 or 16)

@@ -61,18 +61,20 @@ constexpr TileCost kExpandTiles[] = {{1, 4, 0.80, 0.51},  {1, 8, 0.963, 0.627}, 
 // the kernel family of a 50% pattern: 2:4 direct, 4:8 / 8:16 split, 16:32 expanded
 int pf_mode(int n) { return n == 2 ? kPfDirect : n == 16 ? kPfExpand : kPfSplit; }
 
-TileCost sparse_tile(int64_t rows, int64_t tokens, int mode, const DeviceInfo& dev) {
+// (gated: rows of both matrices, whose row tiles come in pairs: an even tr)
+TileCost sparse_tile(int64_t rows, int64_t tokens, int mode, const DeviceInfo& dev, bool gated = false) {
   const int64_t cus = dev.cu_count > 0 ? dev.cu_count : 256;
   const TileCost* c = mode == kPfDirect ? kDirectTiles : mode == kPfSplit ? kSplitTiles : kExpandTiles;
   const int n = mode == kPfDirect ? int(sizeof(kDirectTiles) / sizeof(TileCost))
               : mode == kPfSplit  ? int(sizeof(kSplitTiles) / sizeof(TileCost))
                                   : int(sizeof(kExpandTiles) / sizeof(TileCost));
   TileCost best = c[0];
-  double best_t = 0;
+  double best_t = -1.0;
   for (int i = 0; i < n; ++i) {
+    if (gated && c[i].tr % 2 != 0) continue;
     const int64_t grid = ceil_div(rows, 64 * c[i].tr) * ceil_div(tokens, 16 * c[i].tt);
     const double t = c[i].t1 + double(ceil_div(grid, cus) - 1) * c[i].tn;
-    if (i == 0 || t < best_t) {
+    if (best_t < 0.0 || t < best_t) {
       best = c[i];
       best_t = t;
     }
@@ -128,16 +130,18 @@ namespace {
 // (4096 x 4096 x 64, 2:4: 12.6 us at 4 splits against 14.7 at 8; 8192 x 8192 x 32: 23.1 us at
 // 4 against 27.6 at 2). Where one workgroup per CU allows no split, 2 splits if two fit.
 struct ColPlan {
-  int splits = 1, blocks = 0, tt = 4;
+  int splits = 1, blocks = 0, tr = 1, tt = 4;
   int64_t tiles = 0;
 };
 
-ColPlan colsplit_plan(int64_t rows, int64_t cols, int64_t tokens, const DeviceInfo& dev) {
+// (gated: rows of both matrices, in tiles of 128, 64 of each)
+ColPlan colsplit_plan(int64_t rows, int64_t cols, int64_t tokens, const DeviceInfo& dev, bool gated = false) {
   ColPlan p;
+  p.tr = gated ? 2 : 1;
   if (use_large<SparseLarge>(rows, tokens, dev)) return p;
   const int64_t cus = dev.cu_count > 0 ? dev.cu_count : 256;
   p.tt = tokens <= 32 ? 2 : 4;
-  p.tiles = ceil_div(rows, Small::kRows) * ceil_div(tokens, 16 * p.tt);
+  p.tiles = ceil_div(rows, Small::kRows * p.tr) * ceil_div(tokens, 16 * p.tt);
   const int64_t nblk = ceil_div(cols, kColBlock);
   const int64_t cap = p.tiles * nblk >= 4 * cus ? 2 * cus : cus;   // workgroups in the grid
   int s = 1;
@@ -151,7 +155,7 @@ ColPlan colsplit_plan(int64_t rows, int64_t cols, int64_t tokens, const DeviceIn
 
 size_t colsplit_bytes(const ColPlan& p, const DeviceInfo& dev) {
   if (p.splits == 1) return 0;
-  return counter_bytes(dev) + size_t(p.tiles) * size_t(p.splits) * size_t(kThreads) * size_t(p.tt) * 16u;
+  return counter_bytes(dev) + size_t(p.tiles) * size_t(p.splits) * size_t(kThreads) * size_t(p.tr) * size_t(p.tt) * 16u;
 }
 
 // Taller column splits for prompts of more than 128 tokens. There the 64-row tiles fill the
@@ -204,19 +208,19 @@ double split_estimate_us(int64_t steps, const TileCost& c, int64_t n, int units)
 // lane (a 64 x 64 tile's 8 splits make one unit, a 256 x 128 tile's S splits make S).
 int handoff_units(int tr, int tt, int splits) { return (splits * tr * tt + 31) / 32; }
 
-TallPlan tall_plan(int64_t rows, int64_t cols, int64_t tokens, int mode, const DeviceInfo& dev) {
+TallPlan tall_plan(int64_t rows, int64_t cols, int64_t tokens, int mode, const DeviceInfo& dev, bool gated = false) {
   TallPlan best;
   if (tokens <= kTallMinTokens) return best;
   const int64_t cus = dev.cu_count > 0 ? dev.cu_count : 256;
   const int64_t nblk = ceil_div(cols, kColBlock);
   double current;
-  const ColPlan p = colsplit_plan(rows, cols, tokens, dev);
-  const TileCost* small = mode_tile(mode, 1, p.tt);
+  const ColPlan p = colsplit_plan(rows, cols, tokens, dev, gated);
+  const TileCost* small = mode_tile(mode, p.tr, p.tt);
   if (p.splits > 1 && small != nullptr) {
     current = split_estimate_us(int64_t(p.blocks) * kStepsPerBlock, *small, ceil_div(p.tiles * p.splits, cus),
-                                handoff_units(1, p.tt, p.splits));
+                                handoff_units(p.tr, p.tt, p.splits));
   } else {
-    const TileCost u = sparse_tile(rows, tokens, mode, dev);
+    const TileCost u = sparse_tile(rows, tokens, mode, dev, gated);
     const int64_t grid = ceil_div(rows, 64 * u.tr) * ceil_div(tokens, 16 * u.tt);
     current = split_estimate_us(ceil_div(cols, 64), u, ceil_div(grid, cus), 1);
   }
@@ -270,44 +274,47 @@ const void* colsplit_kernel(int tt, int mode) {
 
 }  // namespace
 
-size_t prefill_workspace_bytes(int64_t rows, int64_t cols, int64_t tokens, int n, const DeviceInfo& dev) {
+size_t prefill_workspace_bytes(int64_t rows, int64_t cols, int64_t tokens, int n, const DeviceInfo& dev, bool gated) {
+  if (gated) rows *= 2;
   if (!prefill_fits(rows, cols, tokens)) return 0;
-  const TallPlan t = tall_plan(rows, cols, tokens, pf_mode(n), dev);
+  const TallPlan t = tall_plan(rows, cols, tokens, pf_mode(n), dev, gated);
   if (t.tiles > 0) return tall_bytes(t, dev);
-  return colsplit_bytes(colsplit_plan(rows, cols, tokens, dev), dev);
+  return colsplit_bytes(colsplit_plan(rows, cols, tokens, dev, gated), dev);
 }
 
 hipError_t launch_prefill_spmm(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y,
                                int64_t rows, int64_t cols, int64_t tokens, int n, int m, hipStream_t stream,
-                               const DeviceInfo& dev, void* workspace, size_t workspace_bytes) {
-  if (!prefill_fits(rows, cols, tokens) || !prefill_pattern(n, m)) return hipErrorInvalidValue;
+                               const DeviceInfo& dev, void* workspace, size_t workspace_bytes, const BlockArgs* e) {
+  const bool gated = form_of(e) == kGatedForm;
+  const int64_t all = rows_read(rows, e);   // what the tiles cover
+  if (!prefill_fits(all, cols, tokens) || !prefill_pattern(n, m)) return hipErrorInvalidValue;
   int r = int(rows), c = int(cols), t = int(tokens);
   const int mode = pf_mode(n);
-  if (workspace != nullptr) {
-    const TallPlan tp = tall_plan(rows, cols, tokens, mode, dev);
-    if (tp.tiles > 0 && workspace_bytes >= tall_bytes(tp, dev)) {
-      int sp = tp.splits, bl = tp.blocks;
-      unsigned* cnt = static_cast<unsigned*>(workspace);
-      float4* part = reinterpret_cast<float4*>(static_cast<char*>(workspace) + counter_bytes(dev));
-      void* cargs[] = {&values, &masks, &X, &Y, &r, &c, &t, &sp, &bl, &part, &cnt};
-      return launch(tall_kernel(tp, mode), dim3(unsigned(tp.tiles * tp.splits)), dim3(kThreads), cargs, 0, stream,
-                    dev);
-    }
-  }
-  const ColPlan p = colsplit_plan(rows, cols, tokens, dev);
-  const size_t need = colsplit_bytes(p, dev);
-  if (need > 0 && workspace != nullptr && workspace_bytes >= need) {
-    int sp = p.splits, bl = p.blocks;
+  auto kernel = [&](const void* plain, int tr, int tt, bool colsplit) {
+    return e == nullptr ? plain
+           : gated      ? block_prefill_gated_kernel_for(mode, tr, tt, colsplit)
+                        : block_prefill_linear_kernel_for(mode, tr, tt, colsplit);
+  };
+  auto split = [&](const void* k, int splits, int blocks, int64_t tiles) {
     unsigned* cnt = static_cast<unsigned*>(workspace);
     float4* part = reinterpret_cast<float4*>(static_cast<char*>(workspace) + counter_bytes(dev));
-    void* cargs[] = {&values, &masks, &X, &Y, &r, &c, &t, &sp, &bl, &part, &cnt};
-    return launch(colsplit_kernel(p.tt, mode), dim3(unsigned(p.tiles * p.splits)), dim3(kThreads), cargs, 0, stream,
-                  dev);
+    void* cargs[] = {&values, &masks, &X, &Y, &r, &c, &t, &splits, &blocks, &part, &cnt, const_cast<BlockArgs*>(e)};
+    return launch(k, dim3(unsigned(tiles * splits)), dim3(kThreads), cargs, 0, stream, dev);
+  };
+  if (workspace != nullptr) {
+    const TallPlan tp = tall_plan(all, cols, tokens, mode, dev, gated);
+    if (tp.tiles > 0 && workspace_bytes >= tall_bytes(tp, dev))
+      return split(kernel(tall_kernel(tp, mode), tp.tr, tp.tt, true), tp.splits, tp.blocks, tp.tiles);
   }
-  void* args[] = {&values, &masks, &X, &Y, &r, &c, &t};
-  const TileCost tc = sparse_tile(rows, tokens, mode, dev);
-  const int64_t grid = ceil_div(rows, 64 * tc.tr) * ceil_div(tokens, 16 * tc.tt);
-  return launch(sparse_kernel_of(tc, mode), dim3(unsigned(grid)), dim3(kThreads), args, 0, stream, dev);
+  const ColPlan p = colsplit_plan(all, cols, tokens, dev, gated);
+  const size_t need = colsplit_bytes(p, dev);
+  if (need > 0 && workspace != nullptr && workspace_bytes >= need)
+    return split(kernel(colsplit_kernel(p.tt, mode), p.tr, p.tt, true), p.splits, p.blocks, p.tiles);
+  void* args[] = {&values, &masks, &X, &Y, &r, &c, &t, const_cast<BlockArgs*>(e)};
+  const TileCost tc = sparse_tile(all, tokens, mode, dev, gated);
+  const int64_t grid = ceil_div(all, 64 * tc.tr) * ceil_div(tokens, 16 * tc.tt);
+  return launch(kernel(sparse_kernel_of(tc, mode), tc.tr, tc.tt, false), dim3(unsigned(grid)), dim3(kThreads), args, 0,
+                stream, dev);
 }
 
 hipError_t launch_prefill_gemm(const uint16_t* W, const uint16_t* X, uint16_t* Y, int64_t rows, int64_t cols,

@@ -46,6 +46,8 @@
 
 #include <type_traits>
 
+#include "nm_epilogue.h"
+
 namespace nm {
 namespace prefill_detail {
 
@@ -439,6 +441,71 @@ __device__ __forceinline__ void store_out(const f4_t (&acc)[TR][TT], uint16_t* _
     store_all(acc, Y, rows, tokens, wg_r0 + wave * 16 * TR, t0, lane);
 }
 
+// ---- block products (nm_epilogue.h) ----
+// Row tiles of a wave that are rows of Y: a gated product's wave holds TR / 2 of each matrix (tile a
+// of the first and tile TR / 2 + a of the second are the same rows).
+template <int TR, int FORM>
+constexpr int out_tiles() { return FORM == kGatedForm ? TR / 2 : TR; }
+
+// The workgroup's output of a block product. The fp32 sums go through LDS (the X buffers, free after
+// the main loop) in TR passes of kTokens / TR tokens, a token's sums in 16-byte chunks XOR-swizzled
+// by the token's low 4 bits, so that both sides are free of bank conflicts; then a thread takes 8
+// rows of a token, whose bias and residual it reads and whose outputs it writes in 16 bytes (one by
+// one where rows or the arrays do not allow that). The end of the product is thus one loop over
+// whole lines: applied where the sums lie it would be compiled TR * TT times over (two minutes of the
+// compiler for the linear kernels, erfcf and all) and read the residual in pieces of 8 bytes.
+template <int TR, int TT, int KS, int FORM>
+__device__ __forceinline__ void store_block(const f4_t (&acc)[TR][TT], uint16_t* Y, int rows, int tokens, int wg_r0,
+                                            int t0, int wave, int lane, char* buf, const BlockArgs& epi) {
+  using T = Tile<TR, TT, KS>;
+  constexpr int OT = out_tiles<TR, FORM>();
+  constexpr int kPassTok = T::kTokens / TR;
+  constexpr int kTokBytes = T::kRows * 4;
+  constexpr int kGroups = kWaves * 16 * OT / 8;   // 8-row groups of Y a token
+  constexpr int kItems = kPassTok * kGroups;
+  static_assert(T::kTokens % (16 * TR) == 0 && kPassTok * kTokBytes <= 2 * T::kXBytes, "a pass: whole token tiles that fit");
+  static_assert(kItems % kThreads == 0 || kItems < kThreads, "the groups of a pass split evenly over the workgroup");
+  const int q = lane >> 4, li = lane & 15;
+  const int tid = threadIdx.x;
+  const bool wide = wide_ok(epi, Y, rows);
+  __syncthreads();   // every wave's last reads of the X buffers are done
+#pragma unroll
+  for (int p = 0; p < TR; ++p) {
+#pragma unroll
+    for (int b = 0; b < TT; ++b) {
+      if (16 * b < p * kPassTok || 16 * b >= (p + 1) * kPassTok) continue;
+      const int tl = 16 * b + li - p * kPassTok;
+#pragma unroll
+      for (int a = 0; a < TR; ++a)
+        *reinterpret_cast<f4_t*>(buf + tl * kTokBytes + ((((wave * TR + a) * 4 + q) ^ (tl & 15)) << 4)) = acc[a][b];
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = tid; k < kItems; k += kThreads) {
+      const int tl = k / kGroups, g = k % kGroups;
+      const int tok = t0 + p * kPassTok + tl, row = wg_r0 + 8 * g;
+      if (tok >= tokens || row >= rows) continue;
+      // the group's first chunk among the token's: its wave, row tile and half of it
+      const int c = ((g / (2 * OT)) * TR + (g / 2) % OT) * 4 + 2 * (g & 1);
+      const char* from = buf + tl * kTokBytes;
+      float s[8], u[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f4_t v = *reinterpret_cast<const f4_t*>(from + (((c + h) ^ (tl & 15)) << 4));
+        f4_t w = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (FORM == kGatedForm) w = *reinterpret_cast<const f4_t*>(from + (((c + 4 * OT + h) ^ (tl & 15)) << 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[4 * h + e] = v[e];
+          u[4 * h + e] = w[e];
+        }
+      }
+      finish_rows<FORM, 8>(epi, s, u, row, rows, size_t(tok) * unsigned(rows) + unsigned(row), wide, Y);
+    }
+    if (p + 1 < TR) __syncthreads();
+  }
+}
+
 // Weight values of one step for the sparse product: per row tile and 64-column sub-step,
 // this lane's 8 kept values. (The mask words travel separately, a block of steps at a time.)
 template <int TR, int SUB>
@@ -636,20 +703,27 @@ constexpr uint32_t kPfAreaBytes = 16 * 64 + 64;
 // (lut: the pattern's table in LDS; area: EXPAND's per-wave value areas, TR per wave).
 // COLS: one of a tile's column splits (columns c_beg .. c_end - 1; the hand-off to the
 // tile's last workgroup in split_handoff), else the whole row (c_beg = 0, c_end = cols).
-template <int TR, int TT, int KS, int D, int MODE, bool COLS>
+// FORM: the plain product, or a block product's end (nm_epilogue.h); a gated product's workgroup
+// takes half as many rows, of both matrices.
+template <int TR, int TT, int KS, int D, int MODE, bool COLS, int FORM = kPlainForm>
 __device__ __forceinline__ void prefill_sparse_body(const uint16_t* __restrict__ values,
                                                     const uint32_t* __restrict__ masks,
-                                                    const uint16_t* __restrict__ X, uint16_t* __restrict__ Y,
+                                                    const uint16_t* __restrict__ X, uint16_t* Y,
                                                     int rows, int cols, int tokens,
                                                     char (*xs)[Tile<TR, TT, KS>::kXBytes], char* lut, char* area,
-                                                    TileCoord tc, int c_beg, int c_end, const ColSplit& cs) {
+                                                    TileCoord tc, int c_beg, int c_end, const ColSplit& cs,
+                                                    const BlockArgs& epi = BlockArgs{}) {
+  constexpr bool GATED = FORM == kGatedForm;
+  static_assert(!GATED || TR % 2 == 0, "a gated product's row tiles come in pairs");
+  constexpr int OT = out_tiles<TR, FORM>();
+  constexpr int kOutRows = kWaves * 16 * OT;
   constexpr bool SPLIT = MODE == kPfSplit, EXPAND = MODE == kPfExpand;
   using T = Tile<TR, TT, KS>;
   constexpr int SUB = T::kSub;
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = tid >> 6;
   const int q = lane >> 4, li = lane & 15;
-  const int r0 = tc.rx * T::kRows + wave * 16 * TR;
+  const int r0 = tc.rx * kOutRows + wave * 16 * OT;
   const int t0 = tc.ty * T::kTokens;
   const int words = cols >> 5;
 
@@ -676,14 +750,19 @@ __device__ __forceinline__ void prefill_sparse_body(const uint16_t* __restrict__
   xst.init(X, tokens, cols, t0, tid);
 
   // weight slices of the workgroup's rows; this lane's row in tile a is 16 a + li of its wave
-  const int wg_rows = min(T::kRows, rows - tc.rx * T::kRows);
-  const size_t wg_r0 = size_t(tc.rx) * T::kRows;
+  const int wg_rows = min(kOutRows, rows - tc.rx * kOutRows);
+  const size_t wg_r0 = size_t(tc.rx) * kOutRows;
   const __amdgpu_buffer_rsrc_t vr = make_rsrc(values + wg_r0 * unsigned(cols >> 1), int64_t(wg_rows) * cols);
   const __amdgpu_buffer_rsrc_t mr = make_rsrc(masks + wg_r0 * unsigned(words), int64_t(wg_rows) * words * 4);
+  // gated: the second matrix's, for row tiles OT .. TR - 1
+  const __amdgpu_buffer_rsrc_t vr2 =
+      GATED ? make_rsrc(epi.up_values + wg_r0 * unsigned(cols >> 1), int64_t(wg_rows) * cols) : vr;
+  const __amdgpu_buffer_rsrc_t mr2 =
+      GATED ? make_rsrc(epi.up_masks + wg_r0 * unsigned(words), int64_t(wg_rows) * words * 4) : mr;
   uint32_t voff[TR], moff[TR];
 #pragma unroll
   for (int a = 0; a < TR; ++a) {
-    const uint32_t rl = uint32_t(wave * 16 * TR + 16 * a + li);
+    const uint32_t rl = uint32_t(wave * 16 * OT + 16 * (a % OT) + li);
     voff[a] = rl * uint32_t(cols) + 16u * uint32_t(q);          // values 8q.. of the step
     moff[a] = rl * uint32_t(words) * 4u + 16u * uint32_t(q);     // mask words 4q .. 4q + 3 of a block
   }
@@ -696,7 +775,7 @@ __device__ __forceinline__ void prefill_sparse_body(const uint16_t* __restrict__
       const int c = c0 + 64 * u;
       const bool ok = c + qcol < cols;
 #pragma unroll
-      for (int a = 0; a < TR; ++a) f.v[a][u] = buf_load16(vr, ok ? voff[a] + uint32_t(c) : kOutOfRange);
+      for (int a = 0; a < TR; ++a) f.v[a][u] = buf_load16(a < OT ? vr : vr2, ok ? voff[a] + uint32_t(c) : kOutOfRange);
     }
   };
 
@@ -716,7 +795,7 @@ __device__ __forceinline__ void prefill_sparse_body(const uint16_t* __restrict__
   auto load_masks = [&](int blk) {   // blk counts from the range's first block
 #pragma unroll
     for (int a = 0; a < TR; ++a)
-      mnext[a] = buf_load16(mr, moff[a] + uint32_t(64 * (first_block + min(blk, last_block))));
+      mnext[a] = buf_load16(a < OT ? mr : mr2, moff[a] + uint32_t(64 * (first_block + min(blk, last_block))));
   };
   load_masks(0);
   auto hook = [&](auto pc, int s0) {
@@ -868,7 +947,9 @@ __device__ __forceinline__ void prefill_sparse_body(const uint16_t* __restrict__
   }
   // (the split kernels keep the direct stores: with the staged ones their 256 x 256 tile
   // measured 8% slower on 14336 x 4096 x 2048, the 2:4 and dense kernels 2-6% faster)
-  if constexpr (SPLIT)
+  if constexpr (FORM != kPlainForm)
+    store_block<TR, TT, KS, FORM>(acc, Y, rows, tokens, tc.rx * kOutRows, t0, wave, lane, xs[0], epi);
+  else if constexpr (SPLIT)
     store_all(acc, Y, rows, tokens, r0, t0, lane);
   else
     store_out<TR, TT, KS>(acc, Y, rows, tokens, tc.rx * T::kRows, t0, wave, lane, xs[0]);
@@ -967,6 +1048,48 @@ __global__ __launch_bounds__(kThreads) void prefill_colsplit_expand_kernel(const
   const int c_end = min(cols, c_beg + blocks * kColBlock);
   prefill_sparse_body<TR, TT, KS, D, kPfExpand, true>(values, masks, X, Y, rows, cols, tokens, xs, lut, area, tc,
                                                       c_beg, c_end, ColSplit{part, cnt, splits, tile, split, &flag});
+}
+
+// Block products (nm_epilogue.h), laid out as the kernels above. Y may be the residual.
+template <int MODE>
+constexpr uint32_t table_bytes() { return MODE == kPfSplit ? kSplitLutBytes : MODE == kPfExpand ? kExpandBytes : 16u; }
+
+template <int TR, int TT, int KS, int D, int MODE, int FORM>
+__global__ __launch_bounds__(kThreads) void block_prefill_kernel(const uint16_t* __restrict__ values,
+                                                                 const uint32_t* __restrict__ masks,
+                                                                 const uint16_t* __restrict__ X, uint16_t* Y, int rows,
+                                                                 int cols, int tokens, BlockArgs e) {
+  using T = Tile<TR, TT, KS>;
+  constexpr int kOutRows = kWaves * 16 * out_tiles<TR, FORM>();
+  __shared__ __attribute__((aligned(16))) char xs[2][T::kXBytes];
+  __shared__ __attribute__((aligned(16))) char lut[table_bytes<MODE>()];
+  __shared__ __attribute__((aligned(16))) char area[MODE == kPfExpand ? kWaves * TR * kPfAreaBytes : 16];
+  const TileCoord tc = tile_of(int(blockIdx.x), (rows + kOutRows - 1) / kOutRows, (tokens + T::kTokens - 1) / T::kTokens);
+  prefill_sparse_body<TR, TT, KS, D, MODE, false, FORM>(values, masks, X, Y, rows, cols, tokens, xs, lut, area, tc, 0,
+                                                        cols, ColSplit{}, e);
+}
+
+template <int TR, int TT, int KS, int D, int MODE, int FORM>
+__global__ __launch_bounds__(kThreads) void block_colsplit_kernel(const uint16_t* __restrict__ values,
+                                                                  const uint32_t* __restrict__ masks,
+                                                                  const uint16_t* __restrict__ X, uint16_t* Y, int rows,
+                                                                  int cols, int tokens, int splits, int blocks,
+                                                                  float4* __restrict__ part, unsigned* __restrict__ cnt,
+                                                                  BlockArgs e) {
+  using T = Tile<TR, TT, KS>;
+  constexpr int kOutRows = kWaves * 16 * out_tiles<TR, FORM>();
+  __shared__ __attribute__((aligned(16))) char xs[2][T::kXBytes];
+  __shared__ __attribute__((aligned(16))) char lut[table_bytes<MODE>()];
+  __shared__ __attribute__((aligned(16))) char area[MODE == kPfExpand ? kWaves * TR * kPfAreaBytes : 16];
+  __shared__ unsigned flag;
+  const int b = int(blockIdx.x);
+  const int tile = b / splits, split = b - tile * splits;
+  const int nrx = (rows + kOutRows - 1) / kOutRows;
+  const TileCoord tc{tile % nrx, tile / nrx};
+  const int c_beg = split * blocks * kColBlock;
+  const int c_end = min(cols, c_beg + blocks * kColBlock);
+  prefill_sparse_body<TR, TT, KS, D, MODE, true, FORM>(values, masks, X, Y, rows, cols, tokens, xs, lut, area, tc,
+                                                       c_beg, c_end, ColSplit{part, cnt, splits, tile, split, &flag}, e);
 }
 
 // Dense product: W [rows][cols] fp16.

@@ -61,15 +61,17 @@ int splits_for(int64_t tiles, int64_t cols, int tokens, int mode, const DeviceIn
 }
 
 SkinnyShape skinny_shape(int64_t rows, int64_t cols, int tokens, int mode, const DeviceInfo& dev,
-                         bool with_ws = false) {
+                         bool with_ws = false, bool gated = false) {
   const int64_t cus = dev.cu_count > 0 ? dev.cu_count : 256;
   const int64_t tiles = ceil_div(rows, 16);
-  const int64_t want = std::min<int64_t>(kMaxWaves, std::max<int64_t>(1, ceil_div(tiles, cus)));
+  // a gated product's row groups come in pairs, one of each matrix
+  const int64_t each = gated ? 2 : 1;
+  const int64_t want = std::min<int64_t>(kMaxWaves / each, std::max<int64_t>(1, ceil_div(tiles, cus)));
   SkinnyShape s;
-  s.rg = int(want);
+  s.rg = int(want * each);
   s.cs = kMaxWaves / s.rg;
   s.splits = with_ws && s.rg == 1 ? splits_for(tiles, cols, tokens, mode, dev) : 1;
-  s.grid = ceil_div(tiles, s.rg) * s.splits;
+  s.grid = ceil_div(tiles, want) * s.splits;
   // phases of whole 128-column lines (the loads of the 2:4 and split kernels cover lines)
   const int64_t pc_max = int64_t(x_budget(mode, dev) / (2 * size_t(tokens))) / 128 * 128;
   s.phase_cols = int(std::min<int64_t>(pc_max, ceil_div(cols, 128) * 128));
@@ -133,29 +135,28 @@ size_t skinny_workspace_bytes(int64_t rows, int64_t cols, int tokens, int n, con
 
 hipError_t launch_skinny_spmm(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y,
                               int64_t rows, int64_t cols, int tokens, int n, int m, hipStream_t stream,
-                              const DeviceInfo& dev, void* workspace, size_t workspace_bytes) {
+                              const DeviceInfo& dev, void* workspace, size_t workspace_bytes, const BlockArgs* e) {
   if (!skinny_fits(rows, cols, tokens, n, m, dev)) return hipErrorInvalidValue;
   const int mode = mode_of(n);
   const size_t need = skinny_workspace_bytes(rows, cols, tokens, n, dev);
-  const bool split = need > 0 && workspace != nullptr && workspace_bytes >= need;
-  const SkinnyShape s = skinny_shape(rows, cols, tokens, mode, dev, split);
+  const int form = form_of(e);
+  const bool split = need > 0 && workspace != nullptr && workspace_bytes >= need && form != kGatedForm;
+  const SkinnyShape s = skinny_shape(rows, cols, tokens, mode, dev, split, form == kGatedForm);
   int r = int(rows), c = int(cols), t = tokens, rg = s.rg, cs = s.cs, pc = s.phase_cols, sp = s.splits;
   unsigned* cnt = split ? static_cast<unsigned*>(workspace) : nullptr;
   float4* part = split ? reinterpret_cast<float4*>(static_cast<char*>(workspace) + counter_bytes(dev)) : nullptr;
-  if (mode == kModeExpand) {
-    void* args[] = {&values, &masks, &X, &Y, &r, &c, &t, &rg, &cs, &pc};
-    return launch(reinterpret_cast<const void*>(&skinny_expand_kernel<1>), dim3(unsigned(s.grid)),
-                  dim3(kThreadsFixed), args, s.lds, stream, dev);
-  }
   if (s.splits > 1) {
-    void* args[] = {&values, &masks, &X, &Y, &r, &c, &t, &cs, &pc, &sp, &part, &cnt};
-    const void* k = mode == kModeSplit ? reinterpret_cast<const void*>(&skinny_colsplit_kernel<true>)
-                                       : reinterpret_cast<const void*>(&skinny_colsplit_kernel<false>);
+    void* args[] = {&values, &masks, &X, &Y, &r, &c, &t, &cs, &pc, &sp, &part, &cnt, const_cast<BlockArgs*>(e)};
+    const void* k = e                    ? block_skinny_colsplit_kernel_for(mode)
+                    : mode == kModeSplit ? reinterpret_cast<const void*>(&skinny_colsplit_kernel<true>)
+                                         : reinterpret_cast<const void*>(&skinny_colsplit_kernel<false>);
     return launch(k, dim3(unsigned(s.grid)), dim3(kThreadsFixed), args, s.lds, stream, dev);
   }
-  void* args[] = {&values, &masks, &X, &Y, &r, &c, &t, &rg, &cs, &pc};
-  const void* k = mode == kModeSplit ? reinterpret_cast<const void*>(&skinny_spmm_kernel<1, true>)
-                                     : reinterpret_cast<const void*>(&skinny_spmm_kernel<1, false>);
+  void* args[] = {&values, &masks, &X, &Y, &r, &c, &t, &rg, &cs, &pc, const_cast<BlockArgs*>(e)};
+  const void* k = e                     ? block_skinny_kernel_for(form, mode)
+                  : mode == kModeExpand ? reinterpret_cast<const void*>(&skinny_expand_kernel<1>)
+                  : mode == kModeSplit  ? reinterpret_cast<const void*>(&skinny_spmm_kernel<1, true>)
+                                        : reinterpret_cast<const void*>(&skinny_spmm_kernel<1, false>);
   return launch(k, dim3(unsigned(s.grid)), dim3(kThreadsFixed), args, s.lds, stream, dev);
 }
 

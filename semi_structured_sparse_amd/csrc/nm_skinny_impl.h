@@ -72,15 +72,21 @@ __host__ __device__ constexpr uint32_t lead_bytes() {
 // The workgroup's view of the launch: its rows, the wave's place in them, and the buffer
 // resources of its slices of the packed matrix and of X. With `splits` > 1 the columns of
 // each group of row tiles are split over that many consecutive workgroups (split = which).
+//
+// Gated products (nm_epilogue.h): rg_count is even and the row groups come in pairs, rows of the
+// first matrix and the same rows of the second; rt is the pair's row tile.
 struct Tile {
   int lane, wave, q, li, rg, cs;
+  int rt;        // row tile within the workgroup (rg itself, but for gated products)
+  bool second;   // the wave's rows are the second matrix's
   bool active;   // the wave owns rows (rg < rg_count)
   int wg_r0, words;
   int tile0, split;   // first 16-row tile of the workgroup; its part of the columns
   __amdgpu_buffer_rsrc_t vr, mr, xr;
 
   __device__ __forceinline__ Tile(const uint16_t* values, const uint32_t* masks, const uint16_t* X, int rows,
-                                  int cols, int tokens, int rg_count, int cs_count, int splits = 1) {
+                                  int cols, int tokens, int rg_count, int cs_count, int splits = 1,
+                                  bool gated = false, const BlockArgs& e = BlockArgs{}) {
     const int tid = threadIdx.x;
     lane = tid & 63;
     // the wave index and everything derived from it are wave-uniform (scalar registers):
@@ -93,17 +99,20 @@ struct Tile {
     // waves past rg_count * cs_count (when 16 is not a multiple of cs_count) stage X and
     // meet the barriers but own no rows
     active = rg < rg_count;
-    const int wg_rows_max = rg_count * 16;
+    rt = gated ? rg >> 1 : rg;
+    second = gated && (rg & 1) != 0;
+    const int tiles = gated ? rg_count >> 1 : rg_count;
+    const int wg_rows_max = tiles * 16;
     // splits is 1, 2, 4 or 8: a shift, and none of it without a split
     const int sh = splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : 3;
     const int wg = int(blockIdx.x) >> sh;
     split = int(blockIdx.x) & (splits - 1);
-    tile0 = wg * rg_count;
+    tile0 = wg * tiles;
     wg_r0 = wg * wg_rows_max;
     const int wg_rows = min(wg_rows_max, rows - wg_r0);
     words = cols >> 5;
-    vr = make_rsrc(values + size_t(wg_r0) * unsigned(cols >> 1), int64_t(wg_rows) * cols);
-    mr = make_rsrc(masks + size_t(wg_r0) * unsigned(words), int64_t(wg_rows) * words * 4);
+    vr = make_rsrc((second ? e.up_values : values) + size_t(wg_r0) * unsigned(cols >> 1), int64_t(wg_rows) * cols);
+    mr = make_rsrc((second ? e.up_masks : masks) + size_t(wg_r0) * unsigned(words), int64_t(wg_rows) * words * 4);
     xr = make_rsrc(X, int64_t(tokens) * cols * 2);
   }
 };
@@ -157,21 +166,30 @@ struct SplitWs {
 // The CS partial tiles of each row group summed through LDS in a fixed order; the group's
 // first wave rounds once and stores (with column splits, the last split's first wave). D
 // layout of the instructions: lane (q, li) holds token li, rows 4q .. 4q+3 of the tile.
+template <int FORM>
 __device__ __forceinline__ void reduce_store(const Tile& w, f4_t acc, int cs_count, int rows, int tokens,
-                                             uint16_t* __restrict__ Y, char* lds_base,
-                                             const SplitWs& sw = SplitWs{nullptr, nullptr, 1}) {
+                                             uint16_t* Y, char* lds_base,
+                                             const SplitWs& sw = SplitWs{nullptr, nullptr, 1},
+                                             const BlockArgs& e = BlockArgs{}) {
   __syncthreads();
   float4* red = reinterpret_cast<float4*>(lds_base);
   red[w.wave * 64 + w.lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
   __syncthreads();
-  if (w.cs != 0 || !w.active) return;
+  if (w.cs != 0 || !w.active || w.second) return;
   float4 s = red[w.wave * 64 + w.lane];
   for (int k = 1; k < cs_count; ++k) {
     const float4 v = red[(w.wave + k) * 64 + w.lane];
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
+  float4 up = make_float4(0.f, 0.f, 0.f, 0.f);
+  if constexpr (FORM == kGatedForm) {   // the pair's other row group: the cs_count waves after these
+    for (int k = 0; k < cs_count; ++k) {
+      const float4 v = red[(w.wave + cs_count + k) * 64 + w.lane];
+      up.x += v.x; up.y += v.y; up.z += v.z; up.w += v.w;
+    }
+  }
   if (sw.splits > 1) {
-    const int tile = w.tile0 + w.rg;
+    const int tile = w.tile0 + w.rt;
     const __amdgpu_buffer_rsrc_t pr =
         make_rsrc(sw.part + size_t(tile) * unsigned(sw.splits) * 64u, int64_t(sw.splits) * 1024);
     coherent_store16(pr, uint32_t(w.split * 64 + w.lane) * 16u, s);
@@ -194,13 +212,18 @@ __device__ __forceinline__ void reduce_store(const Tile& w, f4_t acc, int cs_cou
     }
     if (w.lane == 0) atomicExch(sw.cnt + tile, 0u);
   }
-  const int row = w.wg_r0 + w.rg * 16 + 4 * w.q;
+  const int row = w.wg_r0 + w.rt * 16 + 4 * w.q;
   if (w.li >= tokens || row >= rows) return;
   uint16_t* out = Y + size_t(w.li) * unsigned(rows);
-  const float e[4] = {s.x, s.y, s.z, s.w};
+  const float sums[4] = {s.x, s.y, s.z, s.w};
+  if constexpr (FORM == kPlainForm) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (row + k < rows) out[row + k] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(e[k]));
+    for (int k = 0; k < 4; ++k)
+      if (row + k < rows) out[row + k] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(sums[k]));
+  } else {
+    const float ups[4] = {up.x, up.y, up.z, up.w};
+    finish_rows<FORM, 4>(e, sums, ups, row, rows, size_t(w.li) * unsigned(rows) + unsigned(row), wide_ok(e, Y, rows), Y);
+  }
 }
 
 // ---- 2:4 (DIRECT) and 4:8 / 8:16 (SPLIT): whole 128-byte lines per load.
@@ -234,18 +257,20 @@ constexpr int kMaskLines = 2;   // lines per mask block (8 words of each row)
 
 // COLS: the column-split form (skinny_colsplit_kernel); without it the split bookkeeping is
 // compiled out, so that the unsplit kernel is the same code as before the split existed.
-template <int MODE, bool COLS>
+template <int MODE, bool COLS, int FORM = kPlainForm>
 __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ values,
                                                  const uint32_t* __restrict__ masks,
-                                                 const uint16_t* __restrict__ X, uint16_t* __restrict__ Y,
+                                                 const uint16_t* __restrict__ X, uint16_t* Y,
                                                  int rows, int cols, int tokens, int rg_count, int cs_count,
-                                                 int phase_cols, const SplitWs& sw) {
+                                                 int phase_cols, const SplitWs& sw,
+                                                 const BlockArgs& e = BlockArgs{}) {
   constexpr bool SPLIT = MODE == kModeSplit;
   static_assert(MODE == kModeDirect || MODE == kModeSplit, "whole-line loads: 2:4 and the split patterns");
   extern __shared__ __attribute__((aligned(16))) char lds_base[];
   char* const lds = lds_base + lead_bytes<MODE>();   // SPLIT: the split tables first, X after them
   const int tid = threadIdx.x;
-  const Tile w(values, masks, X, rows, cols, tokens, rg_count, cs_count, COLS ? sw.splits : 1);
+  static_assert(!COLS || FORM != kGatedForm, "gated products have no column splits here");
+  const Tile w(values, masks, X, rows, cols, tokens, rg_count, cs_count, COLS ? sw.splits : 1, FORM == kGatedForm, e);
   const int q = w.q, li = w.li;
   // this workgroup's columns: lines [L s / S, L (s + 1) / S) of the row's L for split s of S
   // (lines <= 2^14 and splits <= 8: 32-bit products); without a split the whole row
@@ -257,10 +282,10 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
   }
   // value loads: lane l of load h reads row 8h + l % 8 of the row group, chunk kc of the line
   const int kc = 2 * q + ((w.lane >> 3) & 1);
-  const uint32_t voff0 = uint32_t(w.rg * 16 + (w.lane & 7)) * uint32_t(cols) + 16u * uint32_t(kc);
+  const uint32_t voff0 = uint32_t(w.rt * 16 + (w.lane & 7)) * uint32_t(cols) + 16u * uint32_t(kc);
   const uint32_t voff1 = voff0 + 8u * uint32_t(cols);
   // mask blocks: lane (q, li) holds words 2q, 2q+1 of the block for row li
-  const uint32_t moff = uint32_t(w.rg * 16 + li) * uint32_t(w.words) * 4u + 8u * uint32_t(q);
+  const uint32_t moff = uint32_t(w.rt * 16 + li) * uint32_t(w.words) * 4u + 8u * uint32_t(q);
   const bool lo8 = (w.lane & 8) == 0;
   const int xq = 4 * (q >> 1) + (q & 1);   // X chunk of lane q in product 0 of a line
   // token rows past the batch read the last token's X: their products are never stored
@@ -384,29 +409,30 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
     }
   }
   if constexpr (COLS)
-    reduce_store(w, acc, cs_count, rows, tokens, Y, lds_base, sw);
+    reduce_store<FORM>(w, acc, cs_count, rows, tokens, Y, lds_base, sw, e);
   else
-    reduce_store(w, acc, cs_count, rows, tokens, Y, lds_base);
+    reduce_store<FORM>(w, acc, cs_count, rows, tokens, Y, lds_base, SplitWs{nullptr, nullptr, 1}, e);
 }
 
 // ---- 16:32 (EXPAND): 64-column steps, each wave's values of a step through its own LDS area.
 constexpr int kMaskSteps = 4;   // 64-column steps per mask block
 constexpr int kDepth = 4;       // value loads in flight per wave
 
+template <int FORM = kPlainForm>
 __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ values,
                                                    const uint32_t* __restrict__ masks,
-                                                   const uint16_t* __restrict__ X, uint16_t* __restrict__ Y,
+                                                   const uint16_t* __restrict__ X, uint16_t* Y,
                                                    int rows, int cols, int tokens, int rg_count, int cs_count,
-                                                   int phase_cols) {
+                                                   int phase_cols, const BlockArgs& e = BlockArgs{}) {
   extern __shared__ __attribute__((aligned(16))) char lds_base[];
   // the expansion table and the waves' value areas, then X
   char* const lds = lds_base + lead_bytes<kModeExpand>();
   const int tid = threadIdx.x;
-  const Tile w(values, masks, X, rows, cols, tokens, rg_count, cs_count);
+  const Tile w(values, masks, X, rows, cols, tokens, rg_count, cs_count, 1, FORM == kGatedForm, e);
   const int q = w.q, li = w.li;
   // lane (q, li) loads values 8q .. 8q+7 of a 64-column step for row li, and words 2q, 2q+1
   // of a mask block
-  const uint32_t rl = uint32_t(w.rg * 16 + li);   // row within the workgroup
+  const uint32_t rl = uint32_t(w.rt * 16 + li);   // row within the workgroup
   const uint32_t voff = rl * uint32_t(cols) + 16u * uint32_t(q);
   const uint32_t moff = rl * uint32_t(w.words) * 4u + 8u * uint32_t(q);
   const int qcol = 32 * (q >> 1);
@@ -507,7 +533,7 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
       }
     }
   }
-  reduce_store(w, acc, cs_count, rows, tokens, Y, lds_base);
+  reduce_store<FORM>(w, acc, cs_count, rows, tokens, Y, lds_base, SplitWs{nullptr, nullptr, 1}, e);
 }
 
 // TR (row tiles per wave) is 1: one 16-row tile per wave; the parameter stays in the kernel
@@ -546,6 +572,33 @@ __global__ __launch_bounds__(kThreadsFixed) void skinny_expand_kernel(const uint
                                                                        int phase_cols) {
   static_assert(TR == 1, "one row tile per wave");
   skinny_expand_body(values, masks, X, Y, rows, cols, tokens, rg_count, cs_count, phase_cols);
+}
+
+// The kernels above with a block product's end (nm_epilogue.h): linear products in all three forms,
+// gated ones without column splits. Y may be the residual.
+template <int MODE, int FORM>
+__global__ __launch_bounds__(kThreadsFixed) void block_skinny_kernel(const uint16_t* __restrict__ values,
+                                                                      const uint32_t* __restrict__ masks,
+                                                                      const uint16_t* __restrict__ X, uint16_t* Y,
+                                                                      int rows, int cols, int tokens, int rg_count,
+                                                                      int cs_count, int phase_cols, BlockArgs e) {
+  if constexpr (MODE == kModeExpand)
+    skinny_expand_body<FORM>(values, masks, X, Y, rows, cols, tokens, rg_count, cs_count, phase_cols, e);
+  else
+    skinny_line_body<MODE, false, FORM>(values, masks, X, Y, rows, cols, tokens, rg_count, cs_count, phase_cols,
+                                        SplitWs{nullptr, nullptr, 1}, e);
+}
+
+template <int MODE>
+__global__ __launch_bounds__(kThreadsFixed) void block_skinny_colsplit_kernel(const uint16_t* __restrict__ values,
+                                                                               const uint32_t* __restrict__ masks,
+                                                                               const uint16_t* __restrict__ X,
+                                                                               uint16_t* Y, int rows, int cols,
+                                                                               int tokens, int cs_count,
+                                                                               int phase_cols, int splits, float4* part,
+                                                                               unsigned* cnt, BlockArgs e) {
+  skinny_line_body<MODE, true, kLinearForm>(values, masks, X, Y, rows, cols, tokens, 1, cs_count, phase_cols,
+                                            SplitWs{part, cnt, splits}, e);
 }
 
 }  // namespace skinny_detail

@@ -50,6 +50,17 @@ WorkgroupShape spmm_shape(int64_t rows, int64_t cols, const DeviceInfo& dev) {
   return spmm_shape_for(rows, cols, max_waves<N, B>(), dev);
 }
 
+// A gated product's workgroups: the rule's for the rows of both matrices, half (rounded up) of each.
+WorkgroupShape gated_shape(int64_t rows, int64_t cols, int maxw, const DeviceInfo& dev) {
+  WorkgroupShape s = spmm_shape_for(2 * rows, cols, maxw, dev);
+  s.ci = 1;
+  s.rpb = (s.rpb + 1) / 2;
+  s.row_groups = int(ceil_div(2 * s.rpb, 8));
+  s.cs = std::max(1, std::min(s.cs, maxw / s.row_groups));
+  s.grid = ceil_div(rows, s.rpb);
+  return s;
+}
+
 template <int N, int B, int DEC>
 const void* spmm_kernel_for(int ci) {
   switch (ci) {
@@ -61,27 +72,31 @@ const void* spmm_kernel_for(int ci) {
 
 template <int N, int B, int DEC>
 hipError_t launch_sparse(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y,
-                         int rows, int cols, hipStream_t stream, const DeviceInfo& dev) {
+                         int rows, int cols, hipStream_t stream, const DeviceInfo& dev, const BlockArgs* e) {
   // widest phase that fits, no wider than the row (rounded up to a whole step)
   const int cap = max_phase_cols<B, DEC>(size_t(dev.max_lds_per_block));
   if (cap < 128) return hipErrorInvalidValue;
   const int phase = int(std::min<int64_t>(cap, ceil_div(cols, 128) * 128));
-  const WorkgroupShape s = spmm_shape<N, B>(rows, cols, dev);
+  const int form = form_of(e);
+  const WorkgroupShape s = form == kGatedForm ? gated_shape(rows, cols, max_waves<N, B>(), dev) : spmm_shape<N, B>(rows, cols, dev);
   const uint4* v4 = reinterpret_cast<const uint4*>(values);
   int rpb = s.rpb, cs = s.cs;
-  void* args[] = {&v4, &masks, &X, &Y, &rows, &cols, &rpb, &cs, const_cast<int*>(&phase)};
-  return launch(spmm_kernel_for<N, B, DEC>(s.ci), dim3(unsigned(s.grid)), dim3(unsigned(64 * s.row_groups * s.cs)),
+  void* args[] = {&v4, &masks, &X, &Y, &rows, &cols, &rpb, &cs, const_cast<int*>(&phase), const_cast<BlockArgs*>(e)};
+  const void* k = form == kGatedForm    ? block_spmm_gated_kernel_for(N, B)
+                  : form == kLinearForm ? block_spmm_linear_kernel_for(N, B, s.ci)
+                                        : spmm_kernel_for<N, B, DEC>(s.ci);
+  return launch(k, dim3(unsigned(s.grid)), dim3(unsigned(64 * s.row_groups * s.cs)),
                 args, lds_bytes<B, DEC>(phase), stream, dev);
 }
 
 template <int B>
 hipError_t launch_sparse_b(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y,
-                           int rows, int cols, int N, hipStream_t stream, const DeviceInfo& dev) {
+                           int rows, int cols, int N, hipStream_t stream, const DeviceInfo& dev, const BlockArgs* e) {
   switch (N) {
-    case 2: return launch_sparse<2, B, kByteLut>(values, masks, X, Y, rows, cols, stream, dev);
-    case 4: return launch_sparse<4, B, kByteLut>(values, masks, X, Y, rows, cols, stream, dev);
-    case 8: return launch_sparse<8, B, kByteLut>(values, masks, X, Y, rows, cols, stream, dev);
-    case 16: return launch_sparse<16, B, kBitWalk>(values, masks, X, Y, rows, cols, stream, dev);
+    case 2: return launch_sparse<2, B, kByteLut>(values, masks, X, Y, rows, cols, stream, dev, e);
+    case 4: return launch_sparse<4, B, kByteLut>(values, masks, X, Y, rows, cols, stream, dev, e);
+    case 8: return launch_sparse<8, B, kByteLut>(values, masks, X, Y, rows, cols, stream, dev, e);
+    case 16: return launch_sparse<16, B, kBitWalk>(values, masks, X, Y, rows, cols, stream, dev, e);
     default: return hipErrorInvalidValue;
   }
 }
@@ -128,19 +143,19 @@ hipError_t launch_dense_b(const uint16_t* W, const uint16_t* X, uint16_t* Y, int
 
 hipError_t launch_spmm(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y,
                        int64_t rows, int64_t cols, int batch, int N, int M, hipStream_t stream,
-                       const DeviceInfo& dev) {
+                       const DeviceInfo& dev, const BlockArgs* e) {
   // one vector: the single-vector kernel (x staged whole) whenever x fits
-  if (batch == 1 && cols <= max_cols_for(dev)) return launch_spmv(values, masks, X, Y, rows, cols, N, M, stream, dev);
+  if (batch == 1 && cols <= max_cols_for(dev)) return launch_spmv(values, masks, X, Y, rows, cols, N, M, stream, dev, e);
   const int r = int(rows), c = int(cols);
   switch (batch) {
-    case 1: return launch_sparse_b<1>(values, masks, X, Y, r, c, N, stream, dev);
-    case 2: return launch_sparse_b<2>(values, masks, X, Y, r, c, N, stream, dev);
-    case 3: return launch_sparse_b<3>(values, masks, X, Y, r, c, N, stream, dev);
-    case 4: return launch_sparse_b<4>(values, masks, X, Y, r, c, N, stream, dev);
-    case 5: return launch_sparse_b<5>(values, masks, X, Y, r, c, N, stream, dev);
-    case 6: return launch_sparse_b<6>(values, masks, X, Y, r, c, N, stream, dev);
-    case 7: return launch_sparse_b<7>(values, masks, X, Y, r, c, N, stream, dev);
-    case 8: return launch_sparse_b<8>(values, masks, X, Y, r, c, N, stream, dev);
+    case 1: return launch_sparse_b<1>(values, masks, X, Y, r, c, N, stream, dev, e);
+    case 2: return launch_sparse_b<2>(values, masks, X, Y, r, c, N, stream, dev, e);
+    case 3: return launch_sparse_b<3>(values, masks, X, Y, r, c, N, stream, dev, e);
+    case 4: return launch_sparse_b<4>(values, masks, X, Y, r, c, N, stream, dev, e);
+    case 5: return launch_sparse_b<5>(values, masks, X, Y, r, c, N, stream, dev, e);
+    case 6: return launch_sparse_b<6>(values, masks, X, Y, r, c, N, stream, dev, e);
+    case 7: return launch_sparse_b<7>(values, masks, X, Y, r, c, N, stream, dev, e);
+    case 8: return launch_sparse_b<8>(values, masks, X, Y, r, c, N, stream, dev, e);
     default: return hipErrorInvalidValue;
   }
 }

@@ -271,10 +271,14 @@ constexpr int dense_waves_per_eu() {
 // the wave's steps, so that no lane repeats another lane's row (with 8-row slots and 4-row
 // workgroups half of every wave would); the CI partial sums of a row are added across lanes
 // before the LDS reduction.
-template <int N, int B, int DEC, int CI>
+//
+// FORM: the plain product, or a block product (nm_epilogue.h); a gated one has 2 * rpb row slots a
+// workgroup, as spmv_body.
+template <int N, int B, int DEC, int CI, int FORM = kPlainForm>
 __device__ __forceinline__ void spmm_body(const uint4* __restrict__ values, const uint32_t* __restrict__ masks,
-                                          const uint16_t* __restrict__ X, uint16_t* __restrict__ Y, int rows,
-                                          int cols, int rpb, int cs_count, int phase_cols) {
+                                          const uint16_t* __restrict__ X, uint16_t* Y, int rows,
+                                          int cols, int rpb, int cs_count, int phase_cols,
+                                          const BlockArgs& e = BlockArgs{}) {
   static_assert(DEC == kByteLut || (DEC == kBitWalk), "byte LUT or bit walk");
   static_assert(DEC != kByteLut || N <= 8, "the byte LUT needs at most 8 kept columns per mask half-word");
   static_assert(CI == 1 || CI == 2 || CI == 4, "column parts per wave: 1, 2 or 4");
@@ -302,14 +306,17 @@ __device__ __forceinline__ void spmm_body(const uint4* __restrict__ values, cons
   const int wsel = u >> 1;
   const int row0 = blockIdx.x * rpb;
   const int row_end = min(row0 + rpb, rows);
-  const unsigned r = unsigned(min(row0 + 8 * rg + rrow, row_end - 1));
+  static_assert(CI == 1 || FORM != kGatedForm, "gated products have no column ranges within a wave");
+  const bool second = FORM == kGatedForm && 8 * rg + rrow >= rpb;   // this lane's row is the second matrix's
+  const unsigned r = unsigned(min(row0 + 8 * rg + rrow - (second ? rpb : 0), row_end - 1));
 
   const int words = cols >> 5;
   const int steps = (words + 3) >> 2;
   const int full_steps = words >> 2;
   const int psteps = phase_cols >> 7;
-  const uint4* __restrict__ vrow = values + size_t(r) * unsigned(cols >> 4);
-  const uint32_t* __restrict__ mrow = masks + size_t(r) * unsigned(words);
+  const uint4* __restrict__ vrow =
+      (second ? reinterpret_cast<const uint4*>(e.up_values) : values) + size_t(r) * unsigned(cols >> 4);
+  const uint32_t* __restrict__ mrow = (second ? e.up_masks : masks) + size_t(r) * unsigned(words);
   const uint32_t xbase = lds_address(xbuf);
   const uint32_t lut = lds_address(lut_p);
 
@@ -403,9 +410,14 @@ __device__ __forceinline__ void spmm_body(const uint4* __restrict__ values, cons
     const int b = tid / rpb, rr = tid - b * rpb;
     if (rr < nr) {
       const int trg = rr >> 3, trow = rr & 7;
-      float t = 0.f;
+      float t = 0.f, t2 = 0.f;
       for (int k = 0; k < CS; ++k) t += red[((trg * CS + k) * 8 + trow) * kMaxBatch + b];
-      Y[size_t(b) * unsigned(rows) + unsigned(row0 + rr)] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(t));
+      if constexpr (FORM == kGatedForm) {
+        const int g2 = (rpb + rr) >> 3, row2 = (rpb + rr) & 7;
+        for (int k = 0; k < CS; ++k) t2 += red[((g2 * CS + k) * 8 + row2) * kMaxBatch + b];
+      }
+      const size_t at = size_t(b) * unsigned(rows) + unsigned(row0 + rr);
+      Y[at] = finish<FORM>(e, t, t2, unsigned(row0 + rr), at);
     }
   }
 }
@@ -422,6 +434,14 @@ __global__ __launch_bounds__((64 * max_waves<N, B>())) __attribute__((amdgpu_wav
     const uint4* __restrict__ values, const uint32_t* __restrict__ masks, const uint16_t* __restrict__ X,
     uint16_t* __restrict__ Y, int rows, int cols, int rpb, int cs_count, int phase_cols) {
   spmm_body<N, B, DEC, CI>(values, masks, X, Y, rows, cols, rpb, cs_count, phase_cols);
+}
+
+// The two above with a block product's end (linear: any CI; gated: CI = 1). Y may be the residual.
+template <int N, int B, int DEC, int CI, int FORM>
+__global__ __launch_bounds__((64 * max_waves<N, B>())) __attribute__((amdgpu_waves_per_eu((waves_per_eu<N, B>())))) void block_spmm_kernel(
+    const uint4* __restrict__ values, const uint32_t* __restrict__ masks, const uint16_t* __restrict__ X,
+    uint16_t* Y, int rows, int cols, int rpb, int cs_count, int phase_cols, BlockArgs e) {
+  spmm_body<N, B, DEC, CI, FORM>(values, masks, X, Y, rows, cols, rpb, cs_count, phase_cols, e);
 }
 
 // ---------------------------------------------------------------- dense counterpart

@@ -62,6 +62,17 @@ WorkgroupShape workgroup_shape(int64_t rows, int64_t steps, const DeviceInfo& de
   return s;
 }
 
+// A gated product's workgroups: the rule's rows per workgroup for the rows of both matrices, half of
+// them (rounded up) of each.
+WorkgroupShape gated_shape(int64_t rows, int64_t steps, const DeviceInfo& dev) {
+  WorkgroupShape s = workgroup_shape(2 * rows, steps, dev);
+  s.rpb = (s.rpb + 1) / 2;
+  s.row_groups = int(ceil_div(2 * s.rpb, 8));
+  s.cs = std::max(1, std::min(s.cs, kMaxWaves / s.row_groups));
+  s.grid = ceil_div(rows, s.rpb);
+  return s;
+}
+
 // The kernel for a shape's column ranges per wave: the narrow kernel serves the 16:32
 // reversed walk only (the bit walk, which narrow layers never need on this GPU, and the
 // other patterns take spmv_kernel, which suits any wave count).
@@ -82,12 +93,13 @@ const void* kernel_for(int ci) {
 
 template <int N, int DEC>
 hipError_t launch_kernel(const uint16_t* values, const uint32_t* masks, const uint16_t* x, uint16_t* y,
-                         int rows, int cols, const WorkgroupShape& s, hipStream_t stream, const DeviceInfo& dev) {
+                         int rows, int cols, const WorkgroupShape& s, hipStream_t stream, const DeviceInfo& dev,
+                         const BlockArgs* e) {
   const uint4* v4 = reinterpret_cast<const uint4*>(values);
   const uint4* x4 = reinterpret_cast<const uint4*>(x);
   int rpb = s.rpb, cs = s.cs;
-  void* args[] = {&v4, &masks, &x4, &y, &rows, &cols, &rpb, &cs};
-  return launch(kernel_for<N, DEC>(s.ci), dim3(unsigned(s.grid)), dim3(unsigned(64 * s.row_groups * s.cs)), args,
+  void* args[] = {&v4, &masks, &x4, &y, &rows, &cols, &rpb, &cs, const_cast<BlockArgs*>(e)};
+  return launch(e ? block_spmv_kernel_for(form_of(e), N, DEC, s.ci) : kernel_for<N, DEC>(s.ci), dim3(unsigned(s.grid)), dim3(unsigned(64 * s.row_groups * s.cs)), args,
                 lds_bytes<DEC>(cols), stream, dev);
 }
 
@@ -153,32 +165,34 @@ const char* spmv_variant(int64_t rows, int64_t cols, int N, int M, const DeviceI
 
 hipError_t launch_spmv(const uint16_t* values, const uint32_t* masks, const uint16_t* x,
                        uint16_t* y, int64_t rows, int64_t cols, int N, int M, hipStream_t stream,
-                       const DeviceInfo& dev) {
+                       const DeviceInfo& dev, const BlockArgs* e) {
   const int r = int(rows), c = int(cols);
+  const bool gated = form_of(e) == kGatedForm;
   if (M == 4 * N) {  // 25% density: one kernel for 1:4, 2:8, 4:16 and 8:32
-    const WorkgroupShape q = spmv_quarter_shape(rows, cols, dev);
+    const WorkgroupShape q = gated ? gated_shape(rows, ceil_div(cols, 256), dev) : spmv_quarter_shape(rows, cols, dev);
     const uint4* v4 = reinterpret_cast<const uint4*>(values);
     const uint4* x4 = reinterpret_cast<const uint4*>(x);
     int rr = r, cc = c, rpb = q.rpb, cs = q.cs;
-    void* args[] = {&v4, &masks, &x4, &y, &rr, &cc, &rpb, &cs};
-    return launch(reinterpret_cast<const void*>(&spmv_quarter_kernel<kBatch, kNTV>), dim3(unsigned(q.grid)),
-                  dim3(unsigned(64 * q.row_groups * q.cs)), args, lds_bytes<kBitWalk>(c), stream, dev);
+    void* args[] = {&v4, &masks, &x4, &y, &rr, &cc, &rpb, &cs, const_cast<BlockArgs*>(e)};
+    return launch(e ? block_spmv_quarter_kernel_for(form_of(e))
+                    : reinterpret_cast<const void*>(&spmv_quarter_kernel<kBatch, kNTV>),
+                  dim3(unsigned(q.grid)), dim3(unsigned(64 * q.row_groups * q.cs)), args, lds_bytes<kBitWalk>(c), stream, dev);
   }
-  const WorkgroupShape s = spmv_shape(rows, cols, N, dev);
+  const WorkgroupShape s = gated ? gated_shape(rows, ceil_div(cols, 128), dev) : spmv_shape(rows, cols, N, dev);
   const int dec = pick_decoder(N, cols, dev);
   switch (N) {
     case 2:
-      if (dec == kPairTable) return launch_kernel<2, kPairTable>(values, masks, x, y, r, c, s, stream, dev);
-      return launch_kernel<2, kBitWalk>(values, masks, x, y, r, c, s, stream, dev);
+      if (dec == kPairTable) return launch_kernel<2, kPairTable>(values, masks, x, y, r, c, s, stream, dev, e);
+      return launch_kernel<2, kBitWalk>(values, masks, x, y, r, c, s, stream, dev, e);
     case 4:
-      if (dec == kByteLut) return launch_kernel<4, kByteLut>(values, masks, x, y, r, c, s, stream, dev);
-      return launch_kernel<4, kBitWalk>(values, masks, x, y, r, c, s, stream, dev);
+      if (dec == kByteLut) return launch_kernel<4, kByteLut>(values, masks, x, y, r, c, s, stream, dev, e);
+      return launch_kernel<4, kBitWalk>(values, masks, x, y, r, c, s, stream, dev, e);
     case 8:
-      if (dec == kByteLut) return launch_kernel<8, kByteLut>(values, masks, x, y, r, c, s, stream, dev);
-      return launch_kernel<8, kBitWalk>(values, masks, x, y, r, c, s, stream, dev);
+      if (dec == kByteLut) return launch_kernel<8, kByteLut>(values, masks, x, y, r, c, s, stream, dev, e);
+      return launch_kernel<8, kBitWalk>(values, masks, x, y, r, c, s, stream, dev, e);
     case 16:
-      if (dec == kRevWalk) return launch_kernel<16, kRevWalk>(values, masks, x, y, r, c, s, stream, dev);
-      return launch_kernel<16, kBitWalk>(values, masks, x, y, r, c, s, stream, dev);
+      if (dec == kRevWalk) return launch_kernel<16, kRevWalk>(values, masks, x, y, r, c, s, stream, dev, e);
+      return launch_kernel<16, kBitWalk>(values, masks, x, y, r, c, s, stream, dev, e);
     default: return hipErrorInvalidValue;
   }
 }

@@ -41,6 +41,7 @@
 //   bytes of padding on each side, more than the furthest a bad mask can reach.
 #pragma once
 
+#include "nm_epilogue.h"
 #include "nm_internal.h"
 
 namespace nm {
@@ -418,10 +419,14 @@ constexpr size_t lds_bytes(int cols) {
 // across lanes before the LDS reduction.
 //
 // `block` is the workgroup's index within the product (blockIdx.x for a single product).
-template <int N, int BATCH, bool NTV, int DEC, int CI>
+//
+// FORM: the plain product, or a block product (nm_epilogue.h). A gated one has 2 * rpb row slots a
+// workgroup: rpb rows of the gate's matrix, then the same rows of the other, summed side by side in
+// the waves and joined by the threads that store.
+template <int N, int BATCH, bool NTV, int DEC, int CI, int FORM = kPlainForm>
 __device__ __forceinline__ void spmv_body(
     const uint4* __restrict__ values, const uint32_t* __restrict__ masks, const uint4* __restrict__ x,
-    uint16_t* __restrict__ y, int rows, int cols, int rpb, int cs_count, int block) {
+    uint16_t* y, int rows, int cols, int rpb, int cs_count, int block, const BlockArgs& e = BlockArgs{}) {
   static_assert((DEC != kPairTable || N == 2) && (DEC != kByteLut || N == 4 || N == 8) &&
                     (DEC != kRevWalk || N == 16),
                 "pair table: 2:4 only; byte LUT: 4:8 and 8:16 only; reversed walk: 16:32 only");
@@ -447,7 +452,9 @@ __device__ __forceinline__ void spmv_body(
   const int wsel = u >> 1;                         // which of the step's 4 words
   const int row0 = block * rpb;
   const int row_end = min(row0 + rpb, rows);
-  const unsigned r = unsigned(min(row0 + 8 * rg + rrow, row_end - 1));
+  static_assert(CI == 1 || FORM != kGatedForm, "gated products have no column ranges within a wave");
+  const bool second = FORM == kGatedForm && 8 * rg + rrow >= rpb;   // this lane's row is the second matrix's
+  const unsigned r = unsigned(min(row0 + 8 * rg + rrow - (second ? rpb : 0), row_end - 1));
 
   const int words = cols >> 5;
   const int steps = (words + 3) >> 2;
@@ -459,8 +466,9 @@ __device__ __forceinline__ void spmv_body(
   const int s_end = CI == 1 ? int(unsigned(steps) * unsigned(cs + 1) / unsigned(CS)) : s_beg + len;
   const int s_main = min(s_end, full_steps);
 
-  const uint4* __restrict__ vrow = values + size_t(r) * unsigned(cols >> 4);
-  const uint32_t* __restrict__ mrow = masks + size_t(r) * unsigned(words);
+  const uint4* __restrict__ vrow =
+      (second ? reinterpret_cast<const uint4*>(e.up_values) : values) + size_t(r) * unsigned(cols >> 4);
+  const uint32_t* __restrict__ mrow = (second ? e.up_masks : masks) + size_t(r) * unsigned(words);
   const uint32_t keep_high = half ? 0xFFFF0000u : 0xFFFFFFFFu;
 
   const uint4* __restrict__ vp = vrow + 8 * unsigned(s_beg) + unsigned(u);
@@ -544,9 +552,13 @@ __device__ __forceinline__ void spmv_body(
   __syncthreads();
   if (tid < row_end - row0) {
     const int trg = tid >> 3, trow = tid & 7;
-    float t = 0.f;
+    float t = 0.f, t2 = 0.f;
     for (int k = 0; k < CS; ++k) t += red[(trg * CS + k) * 8 + trow];
-    y[row0 + tid] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(t));
+    if constexpr (FORM == kGatedForm) {
+      const int g2 = (rpb + tid) >> 3, row2 = (rpb + tid) & 7;
+      for (int k = 0; k < CS; ++k) t2 += red[(g2 * CS + k) * 8 + row2];
+    }
+    y[row0 + tid] = finish<FORM>(e, t, t2, unsigned(row0 + tid), size_t(row0 + tid));
   }
 }
 
@@ -612,10 +624,10 @@ __global__ __launch_bounds__(64 * kMaxWaves) __attribute__((amdgpu_waves_per_eu(
 // 32-column window of the staged copy. The pattern only fixes how the 8 bits are spread,
 // not the work, so one kernel serves all four. Workgroup shape, prologue order, register
 // budget and reduction are those of spmv_kernel.
-template <int BATCH, bool NTV>
-__global__ __launch_bounds__(64 * kMaxWaves) __attribute__((amdgpu_waves_per_eu(8))) void spmv_quarter_kernel(
+template <int BATCH, bool NTV, int FORM>
+__device__ __forceinline__ void spmv_quarter_body(
     const uint4* __restrict__ values, const uint32_t* __restrict__ masks, const uint4* __restrict__ x,
-    uint16_t* __restrict__ y, int rows, int cols, int rpb, int cs_count) {
+    uint16_t* y, int rows, int cols, int rpb, int cs_count, const BlockArgs& e = BlockArgs{}) {
   extern __shared__ uint4 lds[];
   char* lds_b = reinterpret_cast<char*>(lds);
   float* red = reinterpret_cast<float*>(lds_b);
@@ -632,7 +644,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) __attribute__((amdgpu_waves_per_eu(
   const int u = ((lane >> 5) << 2) | (lane & 3);   // the step's word u of 8
   const int row0 = blockIdx.x * rpb;
   const int row_end = min(row0 + rpb, rows);
-  const unsigned r = unsigned(min(row0 + 8 * rg + rsub, row_end - 1));
+  const bool second = FORM == kGatedForm && 8 * rg + rsub >= rpb;
+  const unsigned r = unsigned(min(row0 + 8 * rg + rsub - (second ? rpb : 0), row_end - 1));
 
   const int words = cols >> 5;
   const int steps = (words + 7) >> 3;
@@ -641,8 +654,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) __attribute__((amdgpu_waves_per_eu(
   const int s_end = int(unsigned(steps) * unsigned(cs + 1) / unsigned(CS));
   const int s_main = min(s_end, full_steps);
 
-  const uint4* __restrict__ vrow = values + size_t(r) * unsigned(cols >> 5);   // 8 values per word
-  const uint32_t* __restrict__ mrow = masks + size_t(r) * unsigned(words);
+  const uint4* __restrict__ vrow = (second ? reinterpret_cast<const uint4*>(e.up_values) : values) +
+                                   size_t(r) * unsigned(cols >> 5);   // 8 values per word
+  const uint32_t* __restrict__ mrow = (second ? e.up_masks : masks) + size_t(r) * unsigned(words);
   const uint4* __restrict__ vp = vrow + 8 * unsigned(s_beg) + unsigned(u);
   const uint32_t* __restrict__ mp = mrow + 8 * unsigned(s_beg) + unsigned(u);
   const int n = s_main - s_beg;
@@ -696,10 +710,38 @@ __global__ __launch_bounds__(64 * kMaxWaves) __attribute__((amdgpu_waves_per_eu(
   __syncthreads();
   if (tid < row_end - row0) {
     const int trg = tid >> 3, trow = tid & 7;
-    float t = 0.f;
+    float t = 0.f, t2 = 0.f;
     for (int k = 0; k < CS; ++k) t += red[(trg * CS + k) * 8 + trow];
-    y[row0 + tid] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(t));
+    if constexpr (FORM == kGatedForm) {
+      const int g2 = (rpb + tid) >> 3, row2 = (rpb + tid) & 7;
+      for (int k = 0; k < CS; ++k) t2 += red[(g2 * CS + k) * 8 + row2];
+    }
+    y[row0 + tid] = finish<FORM>(e, t, t2, unsigned(row0 + tid), size_t(row0 + tid));
   }
+}
+
+template <int BATCH, bool NTV>
+__global__ __launch_bounds__(64 * kMaxWaves) __attribute__((amdgpu_waves_per_eu(8))) void spmv_quarter_kernel(
+    const uint4* __restrict__ values, const uint32_t* __restrict__ masks, const uint4* __restrict__ x,
+    uint16_t* __restrict__ y, int rows, int cols, int rpb, int cs_count) {
+  spmv_quarter_body<BATCH, NTV, kPlainForm>(values, masks, x, y, rows, cols, rpb, cs_count);
+}
+
+// ---------------------------------------------------------------- block products
+// spmv_kernel, spmv_narrow_kernel (linear only) and spmv_quarter_kernel with a block product's end.
+// y may be the residual, so it is not declared as the only pointer to its memory.
+template <int N, int BATCH, bool NTV, int DEC, int CI, int FORM>
+__global__ __launch_bounds__(64 * kMaxWaves) __attribute__((amdgpu_waves_per_eu(8))) void block_spmv_kernel(
+    const uint4* __restrict__ values, const uint32_t* __restrict__ masks, const uint4* __restrict__ x,
+    uint16_t* y, int rows, int cols, int rpb, int cs_count, BlockArgs e) {
+  spmv_body<N, BATCH, NTV, DEC, CI, FORM>(values, masks, x, y, rows, cols, rpb, cs_count, int(blockIdx.x), e);
+}
+
+template <int BATCH, bool NTV, int FORM>
+__global__ __launch_bounds__(64 * kMaxWaves) __attribute__((amdgpu_waves_per_eu(8))) void block_spmv_quarter_kernel(
+    const uint4* __restrict__ values, const uint32_t* __restrict__ masks, const uint4* __restrict__ x,
+    uint16_t* y, int rows, int cols, int rpb, int cs_count, BlockArgs e) {
+  spmv_quarter_body<BATCH, NTV, FORM>(values, masks, x, y, rows, cols, rpb, cs_count, e);
 }
 
 }  // namespace spmv_detail

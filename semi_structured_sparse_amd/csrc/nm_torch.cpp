@@ -1,10 +1,10 @@
-// The quick way from torch tensors to the calls of nm_decode.h: a Python extension that checks
-// the arguments as decode.py does, makes the outputs and calls the library, in 3 to 6 us of the
+// The quick way from torch tensors to the calls of nm_decode.h and nm_block.h: a Python extension
+// that checks the arguments as decode.py and block.py do, makes the outputs and calls the library, in 3 to 6 us of the
 // host where decode.py alone takes 9 to 16, launch and outputs' allocation included (4 is what
 // torch takes to fill an empty tensor; a decoding step makes three such calls a layer). Each
 // function returns NotImplemented where anything is not as it should be (a check that fails, a
 // tensor on another device than the current one, memory that runs out, a call that the library
-// refuses); decode.py then goes its own way, whose checks say what it is. Nothing here touches
+// refuses); the Python module then goes its own way, whose checks say what it is. Nothing here touches
 // tensor data.
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
@@ -16,6 +16,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "nm_block.h"
 #include "nm_decode.h"
 
 namespace {
@@ -29,6 +30,11 @@ struct Library {
   decltype(&nm_tree_attention) tree_attention;
   decltype(&nm_verify_chain) verify_chain;
   decltype(&nm_verify_tree) verify_tree;
+  decltype(&nm_linear) linear;
+  decltype(&nm_gated) gated;
+  decltype(&nm_norm) norm;
+  decltype(&nm_block_norm) block_norm;
+  decltype(&nm_logprobs) logprobs;
 };
 Library lib;   // the addresses of the library decode.py loaded
 
@@ -352,6 +358,212 @@ PyObject* verify(PyObject* const* a, Py_ssize_t n, bool tree) {
 PyObject* verify_chain(PyObject*, PyObject* const* a, Py_ssize_t n) { return verify(a, n, false); }
 PyObject* verify_tree(PyObject*, PyObject* const* a, Py_ssize_t n) { return verify(a, n, true); }
 
+// A packed matrix of rows x cols and pattern N:M: values a[0], masks a[1].
+struct Packed {
+  uint16_t* values;
+  uint32_t* masks;
+  int64_t rows, cols;
+};
+Packed packed(Call& c, PyObject* const* a, int64_t N, int64_t M) {
+  Packed p{};
+  const at::Tensor* m = c.tensor(a[1], at::kInt);
+  if (m == nullptr || m->dim() != 2 || !m->is_contiguous() || N < 1 || N > 32 || M < 1 || M > 32 || m->size(1) > (int64_t(1) << 26)) {
+    c.good = false;
+    return p;
+  }
+  p.rows = m->size(0);
+  p.cols = 32 * m->size(1);
+  p.masks = static_cast<uint32_t*>(m->data_ptr());
+  p.values = c.plain<uint16_t>(a[0], at::kHalf, {p.rows, p.cols * N / M});
+  return p;
+}
+
+// X fp16 [cols] or [batch, cols] and the output of its products with `rows` rows.
+struct Vectors {
+  uint16_t* x = nullptr;
+  int64_t batch = 1;
+  c10::SmallVector<int64_t, 2> out_shape;
+};
+Vectors vectors(Call& c, PyObject* o, const Packed& w) {
+  Vectors v;
+  const at::Tensor* x = c.tensor(o, at::kHalf);
+  if (x == nullptr || (x->dim() != 1 && x->dim() != 2) || x->size(-1) != w.cols || !x->is_contiguous()) {
+    c.good = false;
+    return v;
+  }
+  v.x = static_cast<uint16_t*>(x->data_ptr());
+  if (x->dim() == 2) v.out_shape.push_back(v.batch = x->size(0));
+  v.out_shape.push_back(w.rows);
+  return v;
+}
+
+// (values, masks, X, N, M, bias, activation, scale, residual, workspace, out)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  if (n != 11 || c.first(a[2]) == nullptr) return not_here();
+  const int64_t N = c.whole(a[3]), M = c.whole(a[4]);
+  const Packed w = packed(c, a, N, M);
+  if (!c.good) return not_here();
+  const Vectors v = vectors(c, a[2], w);
+  auto* bias = c.plain<uint16_t>(a[5], at::kHalf, {w.rows}, true);
+  auto* residual = c.plain<uint16_t>(a[8], at::kHalf, v.out_shape, true);
+  const int activation = int(c.whole(a[6]));
+  const float scale = float(c.number(a[7]));
+  size_t bytes = 0;
+  char* ws = workspace(c, a[9], &bytes);
+  if (!c.good) return not_here();
+  THPObjectPtr out = output(a[10], v.out_shape, c.device);
+  auto* op = c.plain<uint16_t>(out, at::kHalf, v.out_shape);
+  if (!c.good) return not_here();
+  return finish(lib.linear(w.values, w.masks, v.x, op, w.rows, w.cols, v.batch, int(N), int(M), bias, activation, scale,
+                           residual, ws, bytes, c.stream),
+                std::move(out));
+}
+
+// (gate values, gate masks, up values, up masks, X, N, M, activation, gate_bias, up_bias, workspace, out)
+PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  if (n != 12 || c.first(a[4]) == nullptr) return not_here();
+  const int64_t N = c.whole(a[5]), M = c.whole(a[6]);
+  const Packed g = packed(c, a, N, M), u = packed(c, a + 2, N, M);
+  if (!c.good || g.rows != u.rows || g.cols != u.cols) return not_here();
+  const Vectors v = vectors(c, a[4], g);
+  const int activation = int(c.whole(a[7]));
+  auto* gate_bias = c.plain<uint16_t>(a[8], at::kHalf, {g.rows}, true);
+  auto* up_bias = c.plain<uint16_t>(a[9], at::kHalf, {g.rows}, true);
+  size_t bytes = 0;
+  char* ws = workspace(c, a[10], &bytes);
+  if (!c.good) return not_here();
+  THPObjectPtr out = output(a[11], v.out_shape, c.device);
+  auto* op = c.plain<uint16_t>(out, at::kHalf, v.out_shape);
+  if (!c.good) return not_here();
+  return finish(lib.gated(g.values, g.masks, u.values, u.masks, v.x, op, g.rows, g.cols, v.batch, int(N), int(M), gate_bias,
+                          up_bias, activation, ws, bytes, c.stream),
+                std::move(out));
+}
+
+// Rows as block.py's _spaced takes them; fp32: allowed, and whether they are.
+struct Spaced {
+  void* at = nullptr;
+  int64_t tokens = 1, heads = 1, width = 0, stride = 0;
+  bool fp32 = false;
+  at::IntArrayRef shape;
+};
+Spaced spaced(Call& c, PyObject* o, bool fp32) {
+  Spaced s;
+  if (!c.good || !THPVariable_Check(o)) {
+    c.good = false;
+    return s;
+  }
+  const at::Tensor& t = THPVariable_Unpack(o);
+  s.fp32 = t.scalar_type() == at::kFloat;
+  const int64_t dims = t.dim();
+  if ((s.fp32 ? !fp32 : t.scalar_type() != at::kHalf) || !t.is_cuda() || t.get_device() != c.device || dims < 1 || dims > 4) {
+    c.good = false;
+    return s;
+  }
+  const auto size = t.sizes(), step = t.strides();
+  s.shape = size;
+  s.width = size[dims - 1];
+  if (dims > 2) s.heads = size[dims - 2];
+  const int64_t row = s.heads * s.width;
+  if ((step[dims - 1] != 1 && s.width > 1) || (dims > 2 && step[dims - 2] != s.width && s.heads > 1)) c.good = false;
+  s.stride = row;
+  if (dims == 2 || dims == 3 || (dims == 4 && size[1] == 1)) {
+    s.tokens = size[0];
+    if (size[0] > 1) s.stride = step[0];
+  } else if (dims == 4) {
+    if (size[0] > 1 && step[0] != size[1] * step[1]) c.good = false;
+    s.tokens = size[0] * size[1];
+    s.stride = step[1];
+  }
+  s.at = t.data_ptr();
+  return s;
+}
+
+// (x, weight, bias, kind, offset, eps, out)
+PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  if (n != 7 || c.first(a[0]) == nullptr) return not_here();
+  const Spaced x = spaced(c, a[0], true);
+  if (!c.good || !same_shape(a[6], THPVariable_Unpack(a[0]))) return not_here();
+  auto* weight = c.plain<uint16_t>(a[1], at::kHalf, {x.width}, true);
+  auto* bias = c.plain<uint16_t>(a[2], at::kHalf, {x.width}, true);
+  const int kind = int(c.whole(a[3]));
+  const float offset = float(c.number(a[4])), eps = float(c.number(a[5]));
+  if (!c.good) return not_here();
+  THPObjectPtr out = output(a[6], x.shape, c.device);
+  const Spaced y = spaced(c, out, false);
+  if (!c.good) return not_here();
+  return finish(lib.norm(x.at, static_cast<uint16_t*>(y.at), weight, bias, x.tokens, x.heads, x.width, x.stride, y.stride,
+                         x.fp32, kind, offset, eps, c.stream),
+                std::move(out));
+}
+
+// (x, branch, weight, bias, post, gate, scale, kind, offset, eps, h, out)
+PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  if (n != 12 || c.first(a[0]) == nullptr || a[1] == Py_None) return not_here();
+  const Spaced x = spaced(c, a[0], true);
+  if (!c.good) return not_here();
+  const at::Tensor& t = THPVariable_Unpack(a[0]);
+  if (t.dim() > 2 || !same_shape(a[1], t) || !same_shape(a[10], t) || !same_shape(a[11], t)) return not_here();
+  const Spaced branch = spaced(c, a[1], false);
+  uint16_t* vec[4];   // weight, bias, post, and a gate for all rows
+  for (int i = 0; i < 3; ++i) vec[i] = c.plain<uint16_t>(a[2 + i], at::kHalf, {x.width}, true);
+  int64_t gate_stride = 0;
+  if (c.good && THPVariable_Check(a[5]) && THPVariable_Unpack(a[5]).dim() == 2) {
+    if (!same_shape(a[5], t)) return not_here();
+    const Spaced gate = spaced(c, a[5], false);
+    vec[3] = static_cast<uint16_t*>(gate.at);
+    gate_stride = gate.stride;
+  } else {
+    vec[3] = c.plain<uint16_t>(a[5], at::kHalf, {x.width}, true);
+  }
+  const float scale = float(c.number(a[6]));
+  const int kind = int(c.whole(a[7]));
+  const float offset = float(c.number(a[8])), eps = float(c.number(a[9]));
+  if (!c.good) return not_here();
+  THPObjectPtr h = a[10] == Py_None ? THPObjectPtr(THPVariable_Wrap(made(x.shape, t.scalar_type(), c.device))) : output(a[10], x.shape, c.device);
+  THPObjectPtr out = output(a[11], x.shape, c.device);
+  const Spaced hs = spaced(c, h, x.fp32), ys = spaced(c, out, false);
+  if (!c.good || hs.fp32 != x.fp32) return not_here();
+  if (lib.block_norm(x.at, static_cast<uint16_t*>(branch.at), hs.at, static_cast<uint16_t*>(ys.at), vec[2], vec[3], vec[0],
+                     vec[1], x.tokens, x.width, x.stride, branch.stride, hs.stride, ys.stride, gate_stride, x.fp32, kind,
+                     scale, offset, eps, c.stream) != 0)
+    return not_here();
+  return PyTuple_Pack(2, out.get(), h.get());
+}
+
+// (logits, tokens, top, scale, workspace)
+PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  const at::Tensor* t = n == 5 ? c.first(a[0]) : nullptr;
+  if (t == nullptr || t->dim() != 2) return not_here();
+  const Spaced x = spaced(c, a[0], true);
+  if (!c.good) return not_here();
+  auto* tokens = c.plain<int32_t>(a[1], at::kInt, {x.tokens}, true);
+  const int64_t top = c.whole(a[2]);
+  const float scale = float(c.number(a[3]));
+  size_t bytes = 0;
+  char* ws = workspace(c, a[4], &bytes);
+  if (!c.good || top < 0 || top > NM_MAX_TOP) return not_here();
+  at::Tensor logprob, best, best_logprobs;
+  const at::Tensor entropy = made({x.tokens}, at::kFloat, c.device);
+  if (tokens != nullptr) logprob = made({x.tokens}, at::kFloat, c.device);
+  if (top > 0) {
+    best = made({x.tokens, top}, at::kInt, c.device);
+    best_logprobs = made({x.tokens, top}, at::kFloat, c.device);
+  }
+  auto at_of = [](const at::Tensor& m) { return m.defined() ? m.data_ptr() : nullptr; };
+  if (lib.logprobs(x.at, tokens, static_cast<float*>(at_of(logprob)), static_cast<float*>(at_of(entropy)),
+                   static_cast<int32_t*>(at_of(best)), static_cast<float*>(at_of(best_logprobs)), x.tokens, x.width, x.stride,
+                   top, !x.fp32, scale, ws, bytes, c.stream) != 0)
+    return not_here();
+  auto given = [](const at::Tensor& m) { return m.defined() ? THPVariable_Wrap(m) : none().release(); };
+  return Py_BuildValue("(NNNN)", given(logprob), given(entropy), given(best), given(best_logprobs));
+}
+
 // The functions' addresses in the loaded library, in Library's order.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   constexpr Py_ssize_t kCount = sizeof(Library) / sizeof(void*);
@@ -392,6 +604,11 @@ PyMethodDef methods[] = {method<bind>("bind"),
                          method<tree_attention>("nm_tree_attention"),
                          method<verify_chain>("nm_verify_chain"),
                          method<verify_tree>("nm_verify_tree"),
+                         method<linear>("nm_linear"),
+                         method<gated>("nm_gated"),
+                         method<norm>("nm_norm"),
+                         method<block_norm>("nm_block_norm"),
+                         method<logprobs>("nm_logprobs"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_nmtorch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -162,7 +162,7 @@ def _paging(table, first, first_name, count, batch, device):
 _functions = {}   # of the loaded library, by name
 _quick = None     # _nmtorch, bound to that library on the first call
 _QUICK = ("nm_rope", "nm_kv_append", "nm_rope_kv_append", "nm_kv_read", "nm_kv_compact", "nm_tree_attention",
-          "nm_verify_chain", "nm_verify_tree")
+          "nm_verify_chain", "nm_verify_tree", "nm_linear", "nm_gated", "nm_norm", "nm_block_norm", "nm_logprobs")
 
 
 class _Absent:
