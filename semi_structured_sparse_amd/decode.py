@@ -162,7 +162,8 @@ def _paging(table, first, first_name, count, batch, device):
 _functions = {}   # of the loaded library, by name
 _quick = None     # _nmtorch, bound to that library on the first call
 _QUICK = ("nm_rope", "nm_kv_append", "nm_rope_kv_append", "nm_kv_read", "nm_kv_compact", "nm_tree_attention",
-          "nm_verify_chain", "nm_verify_tree", "nm_linear", "nm_gated", "nm_norm", "nm_block_norm", "nm_logprobs")
+          "nm_verify_chain", "nm_verify_tree")
+_QUICK_BLOCK = ("nm_linear", "nm_gated", "nm_norm", "nm_block_norm", "nm_logprobs")   # block.py's, bound with these
 
 
 class _Absent:
@@ -183,7 +184,7 @@ def _bound():
                           "python -m semi_structured_sparse_amd.build", RuntimeWarning, stacklevel=3)
             _quick = _Absent()
             return _quick
-        _nmtorch.bind(*(_c.cast(getattr(lib, name), _c.c_void_p).value for name in _QUICK))
+        _nmtorch.bind(*(_c.cast(getattr(lib, name), _c.c_void_p).value for name in _QUICK + _QUICK_BLOCK))
         _quick = _nmtorch
     return _quick
 

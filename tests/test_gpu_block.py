@@ -388,3 +388,50 @@ def test_many_rows(rows):
     x = normal(gen, rows, 2500, spread=2.0)
     tokens = torch.randint(0, 2500, (rows,), generator=gen, device=device()).to(torch.int32)
     score(x, tokens, 5)
+
+
+class _Counts:
+    """Stands before the extension and counts the calls that it takes and leaves."""
+
+    def __init__(self, quick):
+        self.quick, self.took, self.left = quick, [], []
+
+    def __getattr__(self, name):
+        def call(*args):
+            done = getattr(self.quick, name)(*args)
+            (self.left if done is NotImplemented else self.took).append(name)
+            return done
+        return call
+
+
+def test_both_ways_to_the_library(monkeypatch):
+    """The extension and block.py's own checks make the same calls."""
+    from semi_structured_sparse_amd import block, decode
+
+    def calls():
+        gen = generator(1)
+        w, _ = packed(gen, 96, 512, 2, 4)
+        X, bias, residual = normal(gen, 30, 512), normal(gen, 96), normal(gen, 30, 96)
+        ws, gws = nm.linear_workspace(96, 512, 30, 2, 4), nm.gated_workspace(96, 512, 30, 2, 4)
+        made = [nm.nm_linear(*w, X, 2, 4, bias, "gelu", 0.5, residual, ws), nm.nm_linear(*w, X[3], 2, 4),
+                nm.nm_gated(w, w, X, 2, 4, "relu", bias, None, gws), nm.nm_gated(w, w, X[1], 2, 4)]
+        fused = normal(gen, 7, 5, 64)
+        made += [nm.nm_norm(fused[:, :3], bias[:64].contiguous(), kind="layer"), nm.nm_norm(X[0]),
+                 nm.nm_norm(fused.view(7, 1, 5, 64)[:, :, 1:3], out=torch.empty(7, 1, 2, 64, dtype=torch.float16, device=device()))]
+        stream = normal(gen, 30, 96, dtype=torch.float32)
+        made += nm.nm_block_norm(stream, residual, bias, None, bias, bias, 0.5, "layer", 1.0)
+        made += nm.nm_block_norm(residual, residual.clone(), gate=residual, out=torch.empty_like(residual))
+        logits = normal(gen, 9, 5001)[:, :5000]
+        tokens = torch.arange(9, dtype=torch.int32, device=device())
+        made += [t for t in nm.nm_logprobs(logits, tokens, 5, 0.5, nm.logprobs_workspace(9, 5000))]
+        made += [t for t in nm.nm_logprobs(logits.float()) if t is not None]
+        return made
+
+    counts = _Counts(decode._bound())
+    monkeypatch.setattr(decode, "_quick", counts)
+    quick = calls()
+    assert not counts.left and set(counts.took) == set(decode._QUICK_BLOCK)
+    monkeypatch.setattr(decode, "_quick", decode._Absent())
+    for a, b in zip(quick, calls()):
+        assert a.dtype == b.dtype and torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert block.MAX_TOP == 64
