@@ -450,24 +450,63 @@ constexpr int out_tiles() { return FORM == kGatedForm ? TR / 2 : TR; }
 // The workgroup's output of a block product. The fp32 sums go through LDS (the X buffers, free after
 // the main loop) in TR passes of kTokens / TR tokens, a token's sums in 16-byte chunks XOR-swizzled
 // by the token's low 4 bits, so that both sides are free of bank conflicts; then a thread takes 8
-// rows of a token, whose bias and residual it reads and whose outputs it writes in 16 bytes (one by
-// one where rows or the arrays do not allow that). The end of the product is thus one loop over
-// whole lines: applied where the sums lie it would be compiled TR * TT times over (two minutes of the
-// compiler for the linear kernels, erfcf and all) and read the residual in pieces of 8 bytes.
+// neighbouring rows of several tokens, always the same rows: their biases are read once, results
+// written in 16 bytes a thread, and residuals read so a pass ahead (a workgroup of 256 x 256 has its
+// CU to itself, so nothing else hides these trips: token by token they took 14336 x 4096 x 2047 from
+// 178 us, the plain product, to 210, and to 239 with a residual). Ending the product where the sums lie would compile it
+// TR * TT times over, and took the accumulators of 256 x 256 out of their registers.
 template <int TR, int TT, int KS, int FORM>
-__device__ __forceinline__ void store_block(const f4_t (&acc)[TR][TT], uint16_t* Y, int rows, int tokens, int wg_r0,
-                                            int t0, int wave, int lane, char* buf, const BlockArgs& epi) {
+__device__ __forceinline__ void store_block(const f4_t (&acc)[TR][TT], const BlockArgs& e, uint16_t* Y, int rows, int tokens,
+                                            int wg_r0, int t0, int wave, int lane, char* buf) {
   using T = Tile<TR, TT, KS>;
   constexpr int OT = out_tiles<TR, FORM>();
   constexpr int kPassTok = T::kTokens / TR;
   constexpr int kTokBytes = T::kRows * 4;
-  constexpr int kGroups = kWaves * 16 * OT / 8;   // 8-row groups of Y a token
-  constexpr int kItems = kPassTok * kGroups;
+  constexpr int kGroups = kWaves * 16 * OT / 8;      // 8-row groups of Y a token
+  constexpr int kStep = kThreads / kGroups;          // tokens that the workgroup takes at once
+  constexpr int kEach = (kPassTok + kStep - 1) / kStep;
   static_assert(T::kTokens % (16 * TR) == 0 && kPassTok * kTokBytes <= 2 * T::kXBytes, "a pass: whole token tiles that fit");
-  static_assert(kItems % kThreads == 0 || kItems < kThreads, "the groups of a pass split evenly over the workgroup");
+  static_assert(kThreads % kGroups == 0, "a thread keeps its rows");
+  typedef _Float16 group __attribute__((ext_vector_type(8)));
   const int q = lane >> 4, li = lane & 15;
-  const int tid = threadIdx.x;
-  const bool wide = wide_ok(epi, Y, rows);
+  const bool wide = wide_ok(e, Y, rows);
+  const int g = int(threadIdx.x) % kGroups, first = int(threadIdx.x) / kGroups;
+  const int row = wg_r0 + 8 * g, left = rows - row;
+  // the group's first chunk among a token's: its wave, row tile and half of it
+  const int c = ((g / (2 * OT)) * TR + (g / 2) % OT) * 4 + 2 * (g & 1);
+  float bias[8], more[8];
+  load_halves<8>(left > 0 ? e.bias : nullptr, size_t(row), left, wide, bias);
+  load_halves<8>(FORM == kGatedForm && left > 0 ? e.up_bias : nullptr, size_t(row), left, wide, more);
+  auto sums = [&](int tl, int chunk, float (&f)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f4_t v = *reinterpret_cast<const f4_t*>(buf + tl * kTokBytes + (((chunk + h) ^ (tl & 15)) << 4));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[4 * h + k] = v[k];
+    }
+  };
+  auto end = [&](auto act, int tl, const group& r, float (&y)[8]) {
+    float u[8];
+    sums(tl, c, y);
+    if constexpr (FORM == kGatedForm) sums(tl, c + 4 * OT, u);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float v = act(y[k] + bias[k]);
+      y[k] = FORM == kGatedForm ? v * (u[k] + more[k]) : fmaf(e.scale, v, float(r[k]));
+    }
+  };
+  const uint16_t* residual = FORM == kLinearForm && left > 0 ? e.residual : nullptr;
+  group ahead[2][kEach];   // a pass's residuals
+  auto request = [&](int p, group (&r)[kEach]) {
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int tok = t0 + p * kPassTok + first + j * kStep;
+      r[j] = group{0, 0, 0, 0, 0, 0, 0, 0};
+      if (wide && residual != nullptr && tok < tokens)
+        r[j] = *reinterpret_cast<const group*>(residual + size_t(tok) * unsigned(rows) + unsigned(row));
+    }
+  };
+  request(0, ahead[0]);
   __syncthreads();   // every wave's last reads of the X buffers are done
 #pragma unroll
   for (int p = 0; p < TR; ++p) {
@@ -480,28 +519,39 @@ __device__ __forceinline__ void store_block(const f4_t (&acc)[TR][TT], uint16_t*
         *reinterpret_cast<f4_t*>(buf + tl * kTokBytes + ((((wave * TR + a) * 4 + q) ^ (tl & 15)) << 4)) = acc[a][b];
     }
     __syncthreads();
+    if (p + 1 < TR) request(p + 1, ahead[(p + 1) & 1]);
+    const int tok0 = t0 + p * kPassTok;
+    with_activation(e.activation, [&](auto act) {
+      if (wide) {
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const int tl = first + j * kStep;
+          if (kPassTok % kStep != 0 && tl >= kPassTok) continue;
+          float y[8];
+          end(act, tl, ahead[p & 1][j], y);
+          group h;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[k] = static_cast<_Float16>(y[k]);
+          if (left > 0 && tok0 + tl < tokens)
+            *reinterpret_cast<group*>(Y + size_t(tok0 + tl) * unsigned(rows) + unsigned(row)) = h;
+        }
+      } else {
 #pragma unroll 1
-    for (int k = tid; k < kItems; k += kThreads) {
-      const int tl = k / kGroups, g = k % kGroups;
-      const int tok = t0 + p * kPassTok + tl, row = wg_r0 + 8 * g;
-      if (tok >= tokens || row >= rows) continue;
-      // the group's first chunk among the token's: its wave, row tile and half of it
-      const int c = ((g / (2 * OT)) * TR + (g / 2) % OT) * 4 + 2 * (g & 1);
-      const char* from = buf + tl * kTokBytes;
-      float s[8], u[8];
+        for (int tl = first; tl < kPassTok; tl += kStep) {
+          if (left <= 0 || tok0 + tl >= tokens) continue;
+          const size_t at = size_t(tok0 + tl) * unsigned(rows) + unsigned(row);
+          group r = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f4_t v = *reinterpret_cast<const f4_t*>(from + (((c + h) ^ (tl & 15)) << 4));
-        f4_t w = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (FORM == kGatedForm) w = *reinterpret_cast<const f4_t*>(from + (((c + 4 * OT + h) ^ (tl & 15)) << 4));
+          for (int k = 0; k < 8; ++k)
+            if (residual != nullptr && k < left) r[k] = __builtin_bit_cast(_Float16, residual[at + k]);
+          float y[8];
+          end(act, tl, r, y);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[4 * h + e] = v[e];
-          u[4 * h + e] = w[e];
+          for (int k = 0; k < 8; ++k)
+            if (k < left) Y[at + k] = to_half(y[k]);
         }
       }
-      finish_rows<FORM, 8>(epi, s, u, row, rows, size_t(tok) * unsigned(rows) + unsigned(row), wide, Y);
-    }
+    });
     if (p + 1 < TR) __syncthreads();
   }
 }
@@ -947,9 +997,9 @@ __device__ __forceinline__ void prefill_sparse_body(const uint16_t* __restrict__
   }
   // (the split kernels keep the direct stores: with the staged ones their 256 x 256 tile
   // measured 8% slower on 14336 x 4096 x 2048, the 2:4 and dense kernels 2-6% faster)
-  if constexpr (FORM != kPlainForm)
-    store_block<TR, TT, KS, FORM>(acc, Y, rows, tokens, tc.rx * kOutRows, t0, wave, lane, xs[0], epi);
-  else if constexpr (SPLIT)
+  if constexpr (FORM != kPlainForm) {
+    store_block<TR, TT, KS, FORM>(acc, epi, Y, rows, tokens, tc.rx * kOutRows, t0, wave, lane, xs[0]);
+  } else if constexpr (SPLIT)
     store_all(acc, Y, rows, tokens, r0, t0, lane);
   else
     store_out<TR, TT, KS>(acc, Y, rows, tokens, tc.rx * T::kRows, t0, wave, lane, xs[0]);
