@@ -9,13 +9,20 @@
 // wave's, not a lane's, so that it grows a few times a row and the rare tile where it does takes a
 // longer way.
 //
-// The best tokens: each lane keeps the largest value that it saw. The top-th largest of a workgroup's
-// 256 is exceeded or met by at least `top` elements and by few more, and only the lanes whose largest
-// meets it look at their elements again, which the caches still have. What they find is put in
-// order by counting, for each, how many go before it.
+// The best tokens: each lane keeps the largest value that it saw, its tile, and the largest of its other
+// tiles. A limit that `top` of a workgroup's 256 largest meet is met by few elements more, and they
+// are looked for in the tiles of those lanes alone, 16 or 32 elements of one lane and tile at a time, by
+// as many threads (each lane through its own registers instead: 64 rows of 151936 23.7 us against
+// XX, most of it instructions that find nothing). What is found is put in order by counting, for each,
+// how many go before it.
 //
-// What bounds it: reading the logits once. A row goes to several workgroups where there are few rows;
-// the last to arrive joins their sums and lists.
+// What bounds it: reading the logits once, with an exponential an element close behind (2047 rows of
+// 128256 fp16, 525 MB: 5.0 TB/s; 1024 in fp32 5.8). A row goes to several workgroups where there are few
+// rows; the last to arrive joins their sums and lists. There it is a chain of trips to memory (8 rows
+// of 128256 fp32 10.7 us: 6.7 without alternatives, finding them 2, joining their lists 2).
+#include <algorithm>
+#include <type_traits>
+
 #include "nm_block_internal.h"
 #include "nm_decode_internal.h"
 #include "nm_epilogue.h"
@@ -25,9 +32,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kLoads = 4;                  // 16-byte loads of a tile a lane
 constexpr int kMaxChunks = 32;             // workgroups of a row
-constexpr int kMinChunk = 2048;            // elements
 constexpr int kRoom = 2048;                // candidates for the best tokens
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kNone = -__builtin_inff();
@@ -41,6 +46,7 @@ constexpr int kElements = HALF ? 8 : 4;    // of a load
 // Where a row's workgroups leave their sums and lists, and each row's counter.
 struct ScoreSplit {
   int chunks;
+  int each;                // elements of a chunk
   int counter_step;
   uint32_t* counters;
   char* parts;             // kPartBytes a chunk
@@ -88,75 +94,106 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// A lane's elements of a tile of kThreads * kLoads * kElements from `at` on: load u at
+// What a wave's terms are relative to: 2^(x c - mc), mc the rounded m c, so that a term's exponent is
+// one instruction from fp16 (its conversion in it); what the rounding of mc left goes into the sums when
+// they are closed. Where m c could overflow, the exponent is (x - m) c.
+struct Reference {
+  float m, c, mc;
+  bool direct;
+  __device__ __forceinline__ Reference(float m_, float c_) : m(m_), c(c_), mc(m_ * c_), direct(fabsf(m_) > 1e30f) {}
+  __device__ __forceinline__ float rest() const { return direct ? 0.0f : fmaf(m, c, -mc); }
+  template <bool DIRECT>
+  __device__ __forceinline__ float exponent(float x) const {
+    return DIRECT ? (x - m) * c : fmaf(x, c, -mc);
+  }
+};
+
+// A lane's elements of a tile of kThreads * LOADS * kElements from `at` on: load u at
 // at + (u * kThreads + tid) * kElements; kNone past `hi`.
-template <bool HALF>
+template <bool HALF, int LOADS>
 struct Part {
   static constexpr int E = kElements<HALF>;
-  float x[kLoads * E];
+  typedef _Float16 half_group __attribute__((ext_vector_type(8)));
+  typedef float float_group __attribute__((ext_vector_type(4)));
+  typedef std::conditional_t<HALF, half_group, float_group> Group;
+  typedef std::conditional_t<HALF, halves, floats> Anywhere;
+  typedef std::conditional_t<HALF, _Float16, float> Element;
+  Group v[LOADS];
 
   static __device__ __forceinline__ int index(int at, int u) { return at + (u * kThreads + int(threadIdx.x)) * E; }
 
   __device__ __forceinline__ void load(const void* row, int at, int hi) {
+    const Element* p = static_cast<const Element*>(row);
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
+    for (int u = 0; u < LOADS; ++u) {
       const int i = index(at, u);
-      if constexpr (HALF) {
-        const uint16_t* p = static_cast<const uint16_t*>(row);
-        if (i + E <= hi) {
-          const halves v = *reinterpret_cast<const halves*>(p + i);
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[u * E + e] = float(v[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[u * E + e] = i + e < hi ? half_at(p, size_t(i + e)) : kNone;
-        }
+      if (i + E <= hi) {
+        v[u] = *reinterpret_cast<const Anywhere*>(p + i);
       } else {
-        const float* p = static_cast<const float*>(row);
-        if (i + E <= hi) {
-          const floats v = *reinterpret_cast<const floats*>(p + i);
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[u * E + e] = v[e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[u * E + e] = i + e < hi ? p[i + e] : kNone;
-        }
+        for (int e = 0; e < E; ++e) v[u][e] = i + e < hi ? p[i + e] : Element(kNone);
       }
     }
   }
-  __device__ __forceinline__ float largest() const {
-    float m = x[0];
+  __device__ __forceinline__ float at(int u, int e) const { return float(v[u][e]); }
+  __device__ __forceinline__ float largest() const {   // NaN aside: the sums find it
+    Group m = v[0];
 #pragma unroll
-    for (int e = 1; e < kLoads * E; ++e) m = fmaxf(m, x[e]);   // NaN aside: the sums find it
-    return m;
+    for (int u = 1; u < LOADS; ++u) m = __builtin_elementwise_max(m, v[u]);
+    Element r = m[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) r = __builtin_elementwise_max(r, m[e]);
+    return float(r);
   }
-  // Adds the terms, relative to m; skip: the lane's first element at m is left out.
-  template <bool SKIP>
-  __device__ __forceinline__ void add(float m, float c, bool skip, float& s, float& t) const {
+  // Adds the terms; skip: the lane's first element at the maximum is left out.
+  template <bool DIRECT, bool SKIP>
+  __device__ __forceinline__ void add(const Reference& r, bool skip, float& s, float& t) const {
 #pragma unroll
-    for (int e = 0; e < kLoads * E; ++e) {
-      const float d = (x[e] - m) * c;
-      float f = __builtin_amdgcn_exp2f(d);
-      if constexpr (SKIP) {
-        if (skip && x[e] == m) {
-          f = 0.0f;
-          skip = false;
+    for (int u = 0; u < LOADS; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float d = r.exponent<DIRECT>(at(u, e));
+        float f = __builtin_amdgcn_exp2f(d);
+        if constexpr (SKIP) {
+          if (skip && at(u, e) == r.m) {
+            f = 0.0f;
+            skip = false;
+          }
         }
+        s += f;
+        t = fmaf(f, fmaxf(d, -200.0f), t);   // 2^-200 is 0, and stays that beside an infinite d
       }
-      s += f;
-      t = fmaf(f, -fmaxf(d, -200.0f), t);   // 2^-200 is 0, and stays that beside an infinite d
-    }
   }
 };
 
+// A wave's sums as they grow: s and t (of 2^d d, so negative) are a lane's, m the wave's.
+struct Running {
+  float m = kNone, s = 0.0f, t = 0.0f;
+  // s and t as sums of 2^((x - m) c) and of that times (m - x) c
+  __device__ __forceinline__ Sums closed(float c) const {
+    if (!(m > kNone)) return Sums{m, s, 0.0f};
+    const float rest = Reference(m, c).rest(), f = __builtin_amdgcn_exp2f(-rest);
+    return Sums{m, s * f, fmaf(-t, f, rest * s)};
+  }
+  __device__ __forceinline__ void open(float m_, float c, float s_, float t_) {   // the same, backwards
+    const float rest = Reference(m_, c).rest(), f = __builtin_amdgcn_exp2f(rest);
+    m = m_;
+    s = s_ * f;
+    t = fmaf(-t_, f, rest * s_);
+  }
+};
+
+constexpr int kPlaces = 1024;              // tiles of lanes to look into
+
 struct Shared {
   uint64_t keys[kRoom];
-  float largest[kThreads];
+  int places[kPlaces];
   Sums sums[kWaves];
   uint64_t best[kWaves];
   int counts[kWaves];
-  uint32_t found;
-  float limit;
+  uint32_t found, listed;
+  float limits[kWaves];
+  uint64_t limit;
   uint32_t arrived;
 };
 
@@ -166,6 +203,7 @@ __device__ __forceinline__ void in_order(const Shared& sh, int n, int top, Put p
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t mine = sh.keys[i];
     int before = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) before += sh.keys[j] > mine ? 1 : 0;
     if (before < top) put(before, mine);
   }
@@ -205,79 +243,142 @@ __device__ __forceinline__ int one_by_one(const void* row, int lo, int hi, int t
   return n;
 }
 
-// Leaves the keys of at least the `top` best elements of the run in sh.keys; returns their number.
-template <bool HALF>
-__device__ __forceinline__ int candidates(const void* row, int lo, int hi, int top, float largest, Shared& sh) {
-  constexpr int E = kElements<HALF>;
-  const int tid = threadIdx.x;
-  sh.largest[tid] = largest;
-  if (tid == 0) {
-    sh.found = 0;
-    sh.limit = kNone;
-  }
-  __syncthreads();
-  int before = 0;
-  for (int j = 0; j < kThreads; ++j) {
-    const float other = sh.largest[j];
-    before += other > largest || (other == largest && j < tid) ? 1 : 0;
-  }
-  if (before == top - 1) sh.limit = largest;
-  __syncthreads();
-  const float limit = sh.limit;
-  if (largest >= limit && largest > kNone) {
-    for (int at = lo; at < hi; at += kThreads * kLoads * E) {
-      Part<HALF> p;
-      p.load(row, at, hi);
+// A value that at least `count` of a wave's lanes' values meet, and few more: halvings between the
+// least and the largest until `count` meet it (twelve at most, then what they came to).
+__device__ __forceinline__ float met_by(float mine, float most, int count) {
+  float low = mine;
 #pragma unroll
-      for (int e = 0; e < kLoads * E; ++e) {
-        if (p.x[e] >= limit && p.x[e] > kNone) {
-          const uint32_t n = atomicAdd(&sh.found, 1u);
-          if (n < kRoom) sh.keys[n] = key_of(p.x[e], Part<HALF>::index(at, e / E) + e % E);
-        }
-      }
+  for (int d = 1; d < 64; d <<= 1) low = fminf(low, __shfl_xor(low, d));
+  float high = most;
+  for (int i = 0; i < 12 && low > kNone; ++i) {   // without -infinity there, all halves are finite
+    const float half = 0.5f * low + 0.5f * high;
+    const int met = __builtin_popcountll(__ballot(mine >= half));
+    if (met >= count) low = half;
+    else high = half;
+    if (met == count) break;
+  }
+  if (low > kNone) return low;
+  // lanes without a value: the count-th largest, one after the other
+  float best = __builtin_inff();
+  for (int n = 0; n < count && best > kNone;) {
+    best = wave_max(mine < best ? mine : kNone);
+    n += __builtin_popcountll(__ballot(mine == best));
+  }
+  return best;
+}
+
+// What a lane keeps of the values that it saw.
+struct Largest {
+  float value = kNone, other = kNone;   // the largest; the largest of its other tiles
+  int at = 0;                           // its tile
+  __device__ __forceinline__ void see(float v, int tile) {
+    const bool more = v > value;
+    other = fmaxf(other, more ? value : v);
+    at = more ? tile : at;
+    value = fmaxf(value, v);
+  }
+};
+
+// Leaves the keys of at least the `top` best elements of the run in sh.keys; returns their number.
+// Each wave finds a value that a quarter of `top` of its lanes' largest meet; the least of the four
+// values is met by `top` elements at least.
+template <bool HALF, int LOADS>
+__device__ __forceinline__ int candidates(const void* row, int lo, int hi, int top, const Largest& mine, float most,
+                                          Shared& sh) {
+  constexpr int E = kElements<HALF>, kTile = kThreads * LOADS * E, kGroup = LOADS * E, kAtOnce = 4;
+  const int tid = threadIdx.x;
+  const float own = met_by(mine.value, most, (top + kWaves - 1) / kWaves);
+  if ((tid & 63) == 0) sh.limits[tid >> 6] = own;
+  if (tid == 0) sh.found = sh.listed = 0;
+  __syncthreads();
+  float limit = sh.limits[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) limit = fminf(limit, sh.limits[w]);
+  limit = fmaxf(limit, HALF ? -65504.0f : -3.402823466e38f);   // -infinity meets no limit
+  // where to look: first element of the lane in the tile
+  auto list = [&](int tile) {
+    const uint32_t n = atomicAdd(&sh.listed, 1u);
+    if (n < kPlaces) sh.places[n] = tile + tid * E;
+  };
+  if (mine.value >= limit) {
+    if (mine.other >= limit) {
+      for (int at = lo; at < hi; at += kTile) list(at);
+    } else {
+      list(mine.at);
     }
   }
   __syncthreads();
-  const uint32_t n = sh.found;
+  const int places = int(min(sh.listed, uint32_t(kPlaces)));
+  const int j = tid % kGroup, offset = (j / E) * (kThreads * E) + j % E;
+  for (int i = tid / kGroup; i < places; i += kAtOnce * (kThreads / kGroup)) {
+    float x[kAtOnce];
+    int at[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int place = i + k * (kThreads / kGroup);
+      at[k] = place < places ? sh.places[place] + offset : hi;
+      x[k] = kNone;
+      if (at[k] < hi) x[k] = float(static_cast<const typename Part<HALF, LOADS>::Element*>(row)[at[k]]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (x[k] >= limit) {
+        const uint32_t n = atomicAdd(&sh.found, 1u);
+        if (n < kRoom) sh.keys[n] = key_of(x[k], at[k]);
+      }
+  }
   __syncthreads();
-  return n <= kRoom ? int(n) : one_by_one<HALF>(row, lo, hi, top, sh);
+  const uint32_t n = sh.found, listed = sh.listed;
+  __syncthreads();
+  return n <= kRoom && listed <= kPlaces ? int(n) : one_by_one<HALF>(row, lo, hi, top, sh);
 }
 
-template <bool HALF, bool TOP>
-__global__ __launch_bounds__(kThreads) void score_kernel(ScoreCall a, ScoreSplit sp) {
-  constexpr int E = kElements<HALF>, kTile = kThreads * kLoads * E;
+// Four waves a SIMD: with the 131 registers that the compiler takes otherwise only three fit (2047 rows
+// of 128256 fp16 with 20 alternatives 135 us, 120 so; five, and the loads no longer overlap: 270).
+template <bool HALF, bool TOP, int LOADS>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void score_kernel(ScoreCall a, ScoreSplit sp) {
+  constexpr int kTile = kThreads * LOADS * kElements<HALF>;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t r = int64_t(blockIdx.x) / sp.chunks;
   const int chunk = int(int64_t(blockIdx.x) - r * sp.chunks);
   const void* row = static_cast<const char*>(a.logits) + r * a.stride * (HALF ? 2 : 4);
-  const int each = (a.vocab + sp.chunks - 1) / sp.chunks;
-  const int lo = min(a.vocab, chunk * each), hi = min(a.vocab, lo + each);
+  const int lo = int(min(int64_t(a.vocab), int64_t(chunk) * sp.each)), hi = int(min(int64_t(a.vocab), int64_t(lo) + sp.each));
   const float c = a.scale * kLog2e;
 
-  // the wave's maximum, the lane's share of its sums, the lane's own maximum
-  float m = kNone, s = 0.0f, t = 0.0f, largest = kNone;
+  Running run;
+  Largest largest;   // the lane's own
+  Part<HALF, LOADS> p, next;
+  p.load(row, lo, hi);
   for (int at = lo; at < hi; at += kTile) {
-    Part<HALF> p;
-    p.load(row, at, hi);
+    const bool more = at + kTile < hi;
+    if (more) next.load(row, at + kTile, hi);   // in flight while this tile's terms are added
     const float mine = p.largest();
-    if (TOP) largest = fmaxf(largest, mine);
-    if (__ballot(mine > m) != 0) {
+    if (TOP) largest.see(mine, at);
+    bool skip = false;
+    const bool grows = __ballot(mine > run.m) != 0;
+    if (grows) {
       const float top = wave_max(mine);
-      if (m > kNone) {
-        const float g = fminf((top - m) * c, 200.0f), f = __builtin_amdgcn_exp2f(-g);
-        if (lane == 0) s += 1.0f;
-        t = f * fmaf(g, s, t);
-        s *= f;
+      if (run.m > kNone) {
+        const Sums old = run.closed(c);
+        const float g = fminf((top - run.m) * c, 200.0f), f = __builtin_amdgcn_exp2f(-g);
+        const float s = lane == 0 ? old.s + 1.0f : old.s;   // the old maximum joins the others
+        run.open(top, c, f * s, f * fmaf(g, s, old.t));
       }
-      m = top;
-      const bool skip = lane == __builtin_ctzll(__ballot(mine == m));
-      p.template add<true>(m, c, skip, s, t);
-    } else {
-      p.template add<false>(m > kNone ? m : 0.0f, c, false, s, t);
+      run.m = top;
+      skip = lane == __builtin_ctzll(__ballot(mine == top));
     }
+    const Reference ref(run.m > kNone ? run.m : 0.0f, c);
+    if (ref.direct)
+      p.template add<true, true>(ref, skip, run.s, run.t);
+    else if (grows)
+      p.template add<false, true>(ref, skip, run.s, run.t);
+    else
+      p.template add<false, false>(ref, false, run.s, run.t);
+    if (more) p = next;
   }
-  Sums all{m, wave_sum(s), wave_sum(t)};
+  Sums all = run.closed(c);
+  all = Sums{all.m, wave_sum(all.s), wave_sum(all.t)};
   if (lane == 0) sh.sums[wave] = all;
   __syncthreads();
   all = sh.sums[0];
@@ -285,7 +386,7 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreCall a, ScoreSplit
   for (int w = 1; w < kWaves; ++w) all = joined(all, sh.sums[w], c);
 
   int n = 0;
-  if constexpr (TOP) n = candidates<HALF>(row, lo, hi, a.top, largest, sh);
+  if constexpr (TOP) n = candidates<HALF, LOADS>(row, lo, hi, a.top, largest, run.m, sh);
 
   if (sp.chunks > 1) {
     char* parts = sp.parts + r * sp.chunks * int64_t(kPartBytes);
@@ -309,32 +410,62 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreCall a, ScoreSplit
     __syncthreads();
     if (sh.arrived != uint32_t(sp.chunks - 1)) return;
     if (tid == 0) atomicExch(counter, 0u);
-    all = Sums{kNone, 0.0f, 0.0f};
-    for (int k = 0; k < sp.chunks; ++k) {   // in the chunks' order
-      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(buf, uint32_t(k) * kPartBytes, 0, kCoherent);
-      all = joined(all, Sums{__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2])}, c);
+    // every part at once: the sums a lane each, the lists' keys a few a thread
+    auto listed = [&](int k, int j) {
+      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(buf, uint32_t(k) * kPartBytes + 16u + 8u * uint32_t(j), 0, kCoherent);
+      return uint64_t(v[1]) << 32 | v[0];
+    };
+    constexpr int kKeys = kMaxChunks * NM_MAX_TOP / kThreads;
+    static_assert(kMaxChunks <= 32 && kMaxChunks * NM_MAX_TOP <= kRoom, "a lane for each part, room for the lists");
+    Sums part{kNone, 0.0f, 0.0f};
+    if (lane < sp.chunks) {
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(buf, uint32_t(lane) * kPartBytes, 0, kCoherent);
+      part = Sums{__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2])};
     }
+    // of the lists' first `ahead` keys, `top` or more in all, the top-th is met by all that matter
+    const int total = sp.chunks * a.top, ahead = min(a.top, (2 * a.top + sp.chunks - 1) / sp.chunks);
+    uint64_t keys[kKeys] = {};
+    bool first[kKeys];
     if constexpr (TOP) {
-      // of the lists' first `ahead` keys, at least `top` in all, the top-th is met by all that matter
-      auto listed = [&](int k, int j) {
-        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(buf, uint32_t(k) * kPartBytes + 16u + 8u * uint32_t(j), 0, kCoherent);
-        return uint64_t(v[1]) << 32 | v[0];
-      };
-      const int ahead = min(a.top, (2 * a.top + sp.chunks - 1) / sp.chunks), few = sp.chunks * ahead;
-      static_assert(2 * NM_MAX_TOP + kMaxChunks <= kThreads && kMaxChunks * NM_MAX_TOP <= kRoom, "room for the lists");
-      const uint64_t mine = tid < few ? listed(tid / ahead, tid % ahead) : 0;
-      sh.keys[tid] = mine;
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) {
+        if (kThreads * i >= total) break;
+        const int at_key = tid + kThreads * i;
+        const int k = int(unsigned(at_key) / unsigned(a.top)), j = at_key - k * a.top;
+        if (at_key < total) keys[i] = listed(k, j);
+        first[i] = j < ahead;
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {   // neighbours first, the lower one on the left: one order
+      const Sums other{__shfl_xor(part.m, d), __shfl_xor(part.s, d), __shfl_xor(part.t, d)};
+      part = (lane & d) ? joined(other, part, c) : joined(part, other, c);
+    }
+    all = Sums{__shfl(part.m, 0), __shfl(part.s, 0), __shfl(part.t, 0)};
+    if constexpr (TOP) {
+      if (tid == 0) {
+        sh.found = 0;
+        sh.limit = 0;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i)
+        if (kThreads * i < total && keys[i] != 0 && first[i]) sh.keys[atomicAdd(&sh.found, 1u)] = keys[i];
+      __syncthreads();
+      const int few = int(sh.found);
+      for (int i = tid; i < few; i += kThreads) {
+        const uint64_t mine = sh.keys[i];
+        int before = 0;
+        for (int j = 0; j < few; ++j) before += sh.keys[j] > mine ? 1 : 0;
+        if (before == a.top - 1) sh.limit = mine;   // no one: fewer than `top` keys there, all are taken
+      }
+      __syncthreads();
+      const uint64_t limit = sh.limit;
       if (tid == 0) sh.found = 0;
       __syncthreads();
-      int before = 0;
-      for (int j = 0; j < few; ++j) before += sh.keys[j] > mine || (sh.keys[j] == mine && j < tid) ? 1 : 0;
-      if (tid < few && before == a.top - 1) sh.best[0] = mine;
-      __syncthreads();
-      const uint64_t limit = sh.best[0];
-      for (int i = tid; i < sp.chunks * a.top; i += kThreads) {
-        const uint64_t key = listed(i / a.top, i % a.top);
-        if (key != 0 && key >= limit) sh.keys[atomicAdd(&sh.found, 1u)] = key;
-      }
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i)
+        if (kThreads * i < total && keys[i] != 0 && keys[i] >= limit) sh.keys[atomicAdd(&sh.found, 1u)] = keys[i];
       __syncthreads();
       n = int(sh.found);
     }
@@ -380,27 +511,49 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreCall a, ScoreSplit
   }
 }
 
-// Workgroups of a row: four a CU in all, of kMinChunk elements or more.
-int chunks_of(int64_t rows, int64_t vocab, const DeviceInfo& dev) {
-  if (rows > NM_DECODE_COUNTER_BYTES / 4) return 1;
-  int64_t c = 4 * int64_t(dev.cu_count) / rows;
-  if (c > kMaxChunks) c = kMaxChunks;
-  if (c > vocab / kMinChunk) c = vocab / kMinChunk;
-  return c < 1 ? 1 : int(c);
+// Loads of a lane's tile, and the tiles of a row's workgroups: whole ones, for about three workgroups a
+// CU in all. Measured (us; loads 2 / 4): fp16 64 rows of 151936 with 20 alternatives 19.0 / 20.5, 2047
+// of 128256 without 110 / 106; fp32 8 rows of 128256 with 5 11.2 / 10.7, 1024 without 90 / 94. Four
+// workgroups a CU: 64 rows of 151936 20.7, 512 of 32000 20.8 against 18.6 with three and 18.4 with two,
+// which take 36.2 for 256 of 151936 against 33.8.
+constexpr int loads_of(bool half, bool split) { return half == split ? 2 : 4; }
+
+template <bool HALF>
+ScoreSplit split_of(int64_t rows, int64_t vocab, const DeviceInfo& dev) {
+  constexpr int64_t kTile = kThreads * loads_of(HALF, true) * kElements<HALF>;
+  ScoreSplit sp{1, int(vocab), 0, nullptr, nullptr};
+  const int64_t tiles = (vocab + kTile - 1) / kTile;
+  int64_t want = 3 * int64_t(dev.cu_count) / rows;
+  if (want > kMaxChunks) want = kMaxChunks;
+  if (want < 2 || rows > NM_DECODE_COUNTER_BYTES / 4) return sp;
+  const int64_t each = (tiles + want - 1) / want;
+  sp.chunks = int((tiles + each - 1) / each);
+  if (sp.chunks > 1) sp.each = int(each * kTile);
+  return sp;
 }
 
-size_t split_bytes(int64_t rows, int64_t vocab, const DeviceInfo& dev) {
-  const int c = chunks_of(rows, vocab, dev);
+ScoreSplit split_of(int64_t rows, int64_t vocab, bool fp16, const DeviceInfo& dev) {
+  return fp16 ? split_of<true>(rows, vocab, dev) : split_of<false>(rows, vocab, dev);
+}
+
+size_t split_bytes(int64_t rows, int64_t vocab, bool fp16, const DeviceInfo& dev) {
+  const int c = split_of(rows, vocab, fp16, dev).chunks;
   return c > 1 ? NM_DECODE_COUNTER_BYTES + size_t(rows) * size_t(c) * kPartBytes : 0;
+}
+
+template <bool HALF, bool TOP>
+const void* kernel_of(bool split) {
+  return split ? reinterpret_cast<const void*>(&score_kernel<HALF, TOP, loads_of(HALF, true)>)
+               : reinterpret_cast<const void*>(&score_kernel<HALF, TOP, loads_of(HALF, false)>);
 }
 
 }  // namespace
 
-// The most that as many rows or fewer take: rows * chunks is at most four workgroups a CU.
+// The most that as many rows or fewer take: rows * chunks is at most three workgroups a CU.
 size_t score_workspace_bytes(int64_t rows, int64_t vocab, const DeviceInfo& dev) {
   size_t most = 0;
   for (int64_t r = rows < 2 * int64_t(dev.cu_count) ? rows : 2 * int64_t(dev.cu_count); r > 0; --r) {
-    const size_t n = split_bytes(r, vocab, dev);
+    const size_t n = std::max(split_bytes(r, vocab, true, dev), split_bytes(r, vocab, false, dev));
     if (n > most) most = n;
   }
   return most;
@@ -409,21 +562,19 @@ size_t score_workspace_bytes(int64_t rows, int64_t vocab, const DeviceInfo& dev)
 hipError_t launch_score(const ScoreCall& c, bool fp16, void* workspace, size_t workspace_bytes, hipStream_t stream,
                         const DeviceInfo& dev) {
   ScoreCall a = c;
-  ScoreSplit sp{1, 0, nullptr, nullptr};
-  const size_t need = split_bytes(c.rows, c.vocab, dev);
+  ScoreSplit sp{1, c.vocab, 0, nullptr, nullptr};
+  const size_t need = split_bytes(c.rows, c.vocab, fp16, dev);
   if (need > 0 && workspace != nullptr && workspace_bytes >= need) {
-    sp.chunks = chunks_of(c.rows, c.vocab, dev);
+    sp = split_of(c.rows, c.vocab, fp16, dev);
     // a counter a line where they are few: additions to one line wait for each other
     const int64_t room = NM_DECODE_COUNTER_BYTES / 4 / c.rows;
     sp.counter_step = room > 32 ? 32 : int(room);
     sp.counters = static_cast<uint32_t*>(workspace);
     sp.parts = static_cast<char*>(workspace) + NM_DECODE_COUNTER_BYTES;
   }
-  const bool top = c.top > 0;
-  const void* k = fp16 ? (top ? reinterpret_cast<const void*>(&score_kernel<true, true>)
-                              : reinterpret_cast<const void*>(&score_kernel<true, false>))
-                       : (top ? reinterpret_cast<const void*>(&score_kernel<false, true>)
-                              : reinterpret_cast<const void*>(&score_kernel<false, false>));
+  const bool top = c.top > 0, split = sp.chunks > 1;
+  const void* k = fp16 ? (top ? kernel_of<true, true>(split) : kernel_of<true, false>(split))
+                       : (top ? kernel_of<false, true>(split) : kernel_of<false, false>(split));
   void* args[] = {&a, &sp};
   return launch(k, dim3(unsigned(int64_t(c.rows) * sp.chunks)), dim3(kThreads), args, 0, stream, dev);
 }
