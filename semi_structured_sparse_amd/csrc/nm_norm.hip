@@ -71,21 +71,23 @@ __device__ __forceinline__ float lane_moved(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
 
-// The sum over the G lanes of a row, in all of them. room: LDS of a float a wave, of this sum alone.
+constexpr int kMaxWaves = 16;
+
+// The sum over the G lanes of a row, or (G = 0) over the workgroup's waves, in all of them. room: LDS of
+// a float a wave, of this sum alone.
 template <int G>
 __device__ __forceinline__ float row_sum(float v, float* room) {
   v += lane_moved<0xB1>(v);    // quad_perm: neighbours, then pairs
   v += lane_moved<0x4E>(v);
   v += lane_moved<0x141>(v);   // row_half_mirror: the other quad of 8
-  if constexpr (G >= 16) v += lane_moved<0x140>(v);   // row_mirror: the other 8 of 16
-  if constexpr (G >= 32) v += __shfl_xor(v, 16);
-  if constexpr (G >= 64) v += __shfl_xor(v, 32);
-  if constexpr (G > 64) {
+  if constexpr (G == 0 || G >= 16) v += lane_moved<0x140>(v);   // row_mirror: the other 8 of 16
+  if constexpr (G == 0 || G >= 32) v += __shfl_xor(v, 16);
+  if constexpr (G == 0 || G >= 64) v += __shfl_xor(v, 32);
+  if constexpr (G == 0) {
     if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < G / 64; ++w) v += room[w];
+    v = room[0];
+    for (int w = 1; w < int(blockDim.x >> 6); ++w) v += room[w];
   }
   return v;
 }
@@ -94,6 +96,7 @@ __device__ __forceinline__ float row_sum(float v, float* room) {
 // root mean square.
 template <int G, int NU>
 __device__ __forceinline__ void normalise(float (&v)[NU][8], int first, int width, int kind, float eps, float* room) {
+  const int step = 8 * (G ? G : int(blockDim.x));
   const float each = 1.0f / float(width);
   if (kind == NM_NORM_LAYER) {
     float s = 0.0f;
@@ -105,14 +108,14 @@ __device__ __forceinline__ void normalise(float (&v)[NU][8], int first, int widt
 #pragma unroll
     for (int j = 0; j < NU; ++j)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[j][k] = first + 8 * G * j + k < width ? v[j][k] - mean : 0.0f;
+      for (int k = 0; k < 8; ++k) v[j][k] = first + step * j + k < width ? v[j][k] - mean : 0.0f;
   }
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < NU; ++j)
 #pragma unroll
     for (int k = 0; k < 8; ++k) s = fmaf(v[j][k], v[j][k], s);
-  const float r = __builtin_amdgcn_rsqf(row_sum<G>(s, room + (G > 64 ? G / 64 : 0)) * each + eps);   // good to 1 ulp
+  const float r = __builtin_amdgcn_rsqf(row_sum<G>(s, room + kMaxWaves) * each + eps);   // good to 1 ulp
 #pragma unroll
   for (int j = 0; j < NU; ++j)
 #pragma unroll
@@ -127,15 +130,14 @@ __device__ __forceinline__ void weigh(float (&v)[8], const uint16_t* weight, flo
   for (int k = 0; k < 8; ++k) v[k] *= offset + w[k];
 }
 
-// G lanes a row, NU units a lane (8 * G * NU >= width), threads / G rows a workgroup.
+// G lanes a row, or the workgroup's (G = 0), and NU units a lane (8 * NU of all of them >= width).
 template <int G, int NU, typename Stream, bool BRANCH>
-__global__ __launch_bounds__((G > 256 ? G : 256)) void norm_kernel(NormCall a) {
-  constexpr int kThreads = G > 256 ? G : 256;
-  __shared__ float room[4 * (kThreads / 64)];
-  const int tid = threadIdx.x;
-  const int64_t row = int64_t(blockIdx.x) * (kThreads / G) + tid / G;
+__global__ __launch_bounds__((G ? 256 : 64 * kMaxWaves)) void norm_kernel(NormCall a) {
+  __shared__ float room[4 * kMaxWaves];
+  const int tid = threadIdx.x, lanes = G ? G : int(blockDim.x), step = 8 * lanes;
+  const int64_t row = G ? int64_t(blockIdx.x) * (256 / (G ? G : 1)) + tid / lanes : int64_t(blockIdx.x);
   if (row >= a.rows) return;   // whole rows of lanes; a workgroup that meets at barriers has one row
-  const int first = 8 * (tid % G), width = a.width;
+  const int first = 8 * (G ? tid % lanes : tid), width = a.width;
   int64_t token = row;
   int64_t in_token = 0;
   if (!BRANCH && a.heads > 1) {
@@ -145,35 +147,35 @@ __global__ __launch_bounds__((G > 256 ? G : 256)) void norm_kernel(NormCall a) {
   const Stream* x = static_cast<const Stream*>(a.x) + token * a.x_stride + in_token;
   float v[NU][8];
 #pragma unroll
-  for (int j = 0; j < NU; ++j) load_unit(x, first + 8 * G * j, width, v[j]);
+  for (int j = 0; j < NU; ++j) load_unit(x, first + step * j, width, v[j]);
   if constexpr (BRANCH) {
     const uint16_t* branch = a.branch + token * a.branch_stride;
     float b[NU][8];
 #pragma unroll
-    for (int j = 0; j < NU; ++j) load_unit(branch, first + 8 * G * j, width, b[j]);
+    for (int j = 0; j < NU; ++j) load_unit(branch, first + step * j, width, b[j]);
     if (a.post != nullptr) {
       normalise<G, NU>(b, first, width, a.kind, a.eps, room);
 #pragma unroll
-      for (int j = 0; j < NU; ++j) weigh(b[j], a.post, a.offset, first + 8 * G * j, width);
+      for (int j = 0; j < NU; ++j) weigh(b[j], a.post, a.offset, first + step * j, width);
     }
     const uint16_t* gate = a.gate != nullptr ? a.gate + token * a.gate_stride : nullptr;
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      weigh(b[j], gate, 0.0f, first + 8 * G * j, width);
+      weigh(b[j], gate, 0.0f, first + step * j, width);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[j][k] = fmaf(a.scale, b[j][k], v[j][k]);
     }
     if (a.h != nullptr) {
       Stream* h = static_cast<Stream*>(a.h) + token * a.h_stride;
 #pragma unroll
-      for (int j = 0; j < NU; ++j) store_unit(h, first + 8 * G * j, width, v[j]);
+      for (int j = 0; j < NU; ++j) store_unit(h, first + step * j, width, v[j]);
     }
   }
-  normalise<G, NU>(v, first, width, a.kind, a.eps, room + 2 * (kThreads / 64));
+  normalise<G, NU>(v, first, width, a.kind, a.eps, room + 2 * kMaxWaves);
   uint16_t* y = a.y + token * a.y_stride + in_token;
 #pragma unroll
   for (int j = 0; j < NU; ++j) {
-    const int i = first + 8 * G * j;
+    const int i = first + step * j;
     weigh(v[j], a.weight, a.offset, i, width);
     if (a.bias != nullptr) {
       float c[8];
@@ -186,33 +188,32 @@ __global__ __launch_bounds__((G > 256 ? G : 256)) void norm_kernel(NormCall a) {
 }
 
 struct Shape {
-  int lanes, units;
+  int lanes, units, threads;   // lanes 0: the workgroup's
 };
 
-// Lanes a row and units a lane.
+// Lanes a row and units a lane: as few lanes as hold the row, since idle ones cost as much as others
+// (8191 x 4100 with a branch in fp32 101 us with 512 lanes, 90 with 320; heads of 64 3.3 TB/s with 16
+// lanes, 5.5 with 8). Several waves share a row from two units a lane on.
 Shape shape_of(int width) {
   const int units = (width + 7) / 8;
-  if (units <= 16) return {16, 1};
-  if (units <= 64) return {64, 1};
-  if (units <= 128) return {64, 2};
-  if (units <= 256) return {256, 1};
-  if (units <= 512) return {256, 2};
-  if (units <= 1024) return {512, 2};
-  if (units <= 2048) return {1024, 2};
-  return {1024, 4};
+  for (int lanes = 8; lanes <= 64; lanes *= 2)
+    if (units <= lanes) return {lanes, 1, 256};
+  if (units <= 128) return {64, 2, 256};
+  const int each = units <= 256 ? 1 : units <= 2048 ? 2 : 4;
+  return {0, each, 64 * ((units + 64 * each - 1) / (64 * each))};
 }
 
 template <typename Stream, bool BRANCH>
 const void* kernel_of(const Shape& s) {
   switch (s.lanes) {
+    case 8: return reinterpret_cast<const void*>(&norm_kernel<8, 1, Stream, BRANCH>);
     case 16: return reinterpret_cast<const void*>(&norm_kernel<16, 1, Stream, BRANCH>);
+    case 32: return reinterpret_cast<const void*>(&norm_kernel<32, 1, Stream, BRANCH>);
     case 64: return s.units == 1 ? reinterpret_cast<const void*>(&norm_kernel<64, 1, Stream, BRANCH>)
                                  : reinterpret_cast<const void*>(&norm_kernel<64, 2, Stream, BRANCH>);
-    case 256: return s.units == 1 ? reinterpret_cast<const void*>(&norm_kernel<256, 1, Stream, BRANCH>)
-                                  : reinterpret_cast<const void*>(&norm_kernel<256, 2, Stream, BRANCH>);
-    case 512: return reinterpret_cast<const void*>(&norm_kernel<512, 2, Stream, BRANCH>);
-    default: return s.units == 2 ? reinterpret_cast<const void*>(&norm_kernel<1024, 2, Stream, BRANCH>)
-                                 : reinterpret_cast<const void*>(&norm_kernel<1024, 4, Stream, BRANCH>);
+    default: return s.units == 1   ? reinterpret_cast<const void*>(&norm_kernel<0, 1, Stream, BRANCH>)
+                    : s.units == 2 ? reinterpret_cast<const void*>(&norm_kernel<0, 2, Stream, BRANCH>)
+                                   : reinterpret_cast<const void*>(&norm_kernel<0, 4, Stream, BRANCH>);
   }
 }
 
@@ -221,13 +222,13 @@ const void* kernel_of(const Shape& s) {
 hipError_t launch_norm(const NormCall& c, bool fp32_stream, hipStream_t stream, const DeviceInfo& dev) {
   NormCall a = c;
   const Shape s = shape_of(a.width);
-  const int threads = s.lanes > 256 ? s.lanes : 256;
-  const int64_t grid = (a.rows + threads / s.lanes - 1) / (threads / s.lanes);
+  const int each = s.lanes ? s.threads / s.lanes : 1;   // rows a workgroup
+  const int64_t grid = (a.rows + each - 1) / each;
   const bool branch = a.branch != nullptr;
   const void* k = fp32_stream ? (branch ? kernel_of<float, true>(s) : kernel_of<float, false>(s))
                               : (branch ? kernel_of<uint16_t, true>(s) : kernel_of<uint16_t, false>(s));
   void* args[] = {&a};
-  return launch(k, dim3(unsigned(grid)), dim3(unsigned(threads)), args, 0, stream, dev);
+  return launch(k, dim3(unsigned(grid)), dim3(unsigned(s.threads)), args, 0, stream, dev);
 }
 
 }  // namespace nm
