@@ -13,7 +13,7 @@
 // tiles. A limit that `top` of a workgroup's 256 largest meet is met by few elements more, and they
 // are looked for in the tiles of those lanes alone, 16 or 32 elements of one lane and tile at a time, by
 // as many threads (each lane through its own registers instead: 64 rows of 151936 23.7 us against
-// XX, most of it instructions that find nothing). What is found is put in order by counting, for each,
+// 41, most of it instructions that find nothing). What is found is put in order by counting, for each,
 // how many go before it.
 //
 // What bounds it: reading the logits once, with an exponential an element close behind (2047 rows of

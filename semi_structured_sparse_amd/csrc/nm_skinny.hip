@@ -33,11 +33,11 @@ size_t lead_of(int mode) {
   return mode == kModeSplit ? lead_bytes<kModeSplit>() : mode == kModeExpand ? lead_bytes<kModeExpand>() : 0;
 }
 
-size_t x_budget(int mode, const DeviceInfo& dev) {
+size_t x_budget(int mode, const DeviceInfo& dev, int chunks = kXChunksPerThread) {
   const size_t lds = size_t(dev.max_lds_per_block > 0 ? dev.max_lds_per_block : 65536);
   const size_t lead = lead_of(mode);
   const size_t avail = lds > lead ? lds - lead : 0;
-  return std::min<size_t>(kMaxXBytes, avail);
+  return std::min<size_t>(kMaxXBytes / kXChunksPerThread * chunks, avail);
 }
 
 // Column splits: a layer of at most half as many 16-row tiles as CUs (1024 rows: 64 tiles)
@@ -61,11 +61,11 @@ int splits_for(int64_t tiles, int64_t cols, int tokens, int mode, const DeviceIn
 }
 
 SkinnyShape skinny_shape(int64_t rows, int64_t cols, int tokens, int mode, const DeviceInfo& dev,
-                         bool with_ws = false, bool gated = false) {
+                         bool with_ws = false, int form = kPlainForm) {
   const int64_t cus = dev.cu_count > 0 ? dev.cu_count : 256;
   const int64_t tiles = ceil_div(rows, 16);
   // a gated product's row groups come in pairs, one of each matrix
-  const int64_t each = gated ? 2 : 1;
+  const int64_t each = form == kGatedForm ? 2 : 1;
   const int64_t want = std::min<int64_t>(kMaxWaves / each, std::max<int64_t>(1, ceil_div(tiles, cus)));
   SkinnyShape s;
   s.rg = int(want * each);
@@ -73,8 +73,13 @@ SkinnyShape skinny_shape(int64_t rows, int64_t cols, int tokens, int mode, const
   s.splits = with_ws && s.rg == 1 ? splits_for(tiles, cols, tokens, mode, dev) : 1;
   s.grid = ceil_div(tiles, want) * s.splits;
   // phases of whole 128-column lines (the loads of the 2:4 and split kernels cover lines)
-  const int64_t pc_max = int64_t(x_budget(mode, dev) / (2 * size_t(tokens))) / 128 * 128;
+  const size_t budget = x_budget(mode, dev, form == kPlainForm ? kXChunksPerThread : kBlockXChunks);
+  const int64_t pc_max = int64_t(budget / (2 * size_t(tokens))) / 128 * 128;
   s.phase_cols = int(std::min<int64_t>(pc_max, ceil_div(cols, 128) * 128));
+  if (form != kPlainForm && pc_max >= 128 * s.cs) {   // phases of whole lines for every wave, evenly many
+    const int64_t lines = ceil_div(ceil_div(cols, 128), s.cs), most = pc_max / (128 * s.cs);
+    s.phase_cols = int(std::min<int64_t>(ceil_div(lines, ceil_div(lines, most)) * s.cs, ceil_div(cols, 128)) * 128);
+  }
   s.lds = std::max(lead_of(mode) + x_bytes(tokens, s.phase_cols), red_bytes(kMaxWaves));
   return s;
 }
@@ -141,7 +146,7 @@ hipError_t launch_skinny_spmm(const uint16_t* values, const uint32_t* masks, con
   const size_t need = skinny_workspace_bytes(rows, cols, tokens, n, dev);
   const int form = form_of(e);
   const bool split = need > 0 && workspace != nullptr && workspace_bytes >= need && form != kGatedForm;
-  const SkinnyShape s = skinny_shape(rows, cols, tokens, mode, dev, split, form == kGatedForm);
+  const SkinnyShape s = skinny_shape(rows, cols, tokens, mode, dev, split, form);
   int r = int(rows), c = int(cols), t = tokens, rg = s.rg, cs = s.cs, pc = s.phase_cols, sp = s.splits;
   unsigned* cnt = split ? static_cast<unsigned*>(workspace) : nullptr;
   float4* part = split ? reinterpret_cast<float4*>(static_cast<char*>(workspace) + counter_bytes(dev)) : nullptr;

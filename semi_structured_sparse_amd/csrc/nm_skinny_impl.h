@@ -42,6 +42,10 @@ constexpr int kMaxTokens = 16;
 constexpr int kThreadsFixed = 64 * kMaxWaves;           // every launch uses 16 waves
 constexpr int kXChunksPerThread = 8;                    // X staged per phase: <= 8 x 16 B per thread
 constexpr size_t kMaxXBytes = size_t(kThreadsFixed) * kXChunksPerThread * 16;   // 128 KiB
+// Block products stage up to 144 KiB, and where X takes several phases, phases of whole rounds of
+// lines over the waves: 13 vectors of 5120 columns (130 KiB) leave a second phase of one line a row
+// otherwise (7168 rows, 4:8: 16.7 us, 15.0 in one phase; 17408 rows, 2:4: 26.0 and 23.5).
+constexpr int kBlockXChunks = 9;
 
 // LDS bytes of the X buffer for `tokens` rows of `phase_cols` columns, and of the reduction
 // area for `waves` waves (one float4 per lane).
@@ -120,9 +124,10 @@ struct Tile {
 // X[0 .. tokens)[p0 .. p0 + chunks * 8) of one phase: flat chunk k = tid + kThreadsFixed * j
 // of token t = k / chunks, chunk c = k % chunks (one division, then steps of kThreadsFixed).
 // Chunks past the row load out of range (zero); chunks past the end are not written.
+template <int CHUNKS>
 struct XStage {
-  uint4 xs[kXChunksPerThread];
-  uint32_t xdst[kXChunksPerThread];
+  uint4 xs[CHUNKS];
+  uint32_t xdst[CHUNKS];
 
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t xr, int tokens, int cols, int p0, int chunks,
                                        uint32_t rb) {
@@ -131,7 +136,7 @@ struct XStage {
     const int dt = kThreadsFixed / chunks, dc = kThreadsFixed - dt * chunks;
     int t = tid / chunks, c = tid - t * chunks;
 #pragma unroll
-    for (int j = 0; j < kXChunksPerThread; ++j) {
+    for (int j = 0; j < CHUNKS; ++j) {
       const int k = tid + kThreadsFixed * j;
       const int col = p0 + 8 * c;
       const bool ok = k < nchunks && col < cols;
@@ -145,7 +150,7 @@ struct XStage {
 
   __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
-    for (int j = 0; j < kXChunksPerThread; ++j)
+    for (int j = 0; j < CHUNKS; ++j)
       if (xdst[j] != 0xFFFFFFFFu) *reinterpret_cast<uint4*>(lds + xdst[j]) = xs[j];
   }
 };
@@ -325,7 +330,7 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
       const uint32_t cm = uint32_t(c_lo + 128 * min(p, last)) >> 3;
       mnext = buf_load8(w.mr, n > 0 ? moff + cm : kOutOfRange);
     };
-    XStage xst;
+    XStage<(FORM == kPlainForm ? kXChunksPerThread : kBlockXChunks)> xst;
     xst.load(w.xr, tokens, cols, p0, plines * 16, rb);
     // then the first weight loads, in flight while X is written to LDS (the X loads were
     // issued first, so waiting for them does not wait for these; mask block first, as in
@@ -465,7 +470,7 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
       const uint32_t cm = uint32_t(c_lo + 64 * min(s, last)) >> 3;
       mnext = buf_load8(w.mr, n > 0 ? moff + cm : kOutOfRange);
     };
-    XStage xst;
+    XStage<(FORM == kPlainForm ? kXChunksPerThread : kBlockXChunks)> xst;
     xst.load(w.xr, tokens, cols, p0, psteps * 8, rb);
     load_m(0);
 #pragma unroll
