@@ -143,10 +143,13 @@ ColPlan colsplit_plan(int64_t rows, int64_t cols, int64_t tokens, const DeviceIn
   p.tt = tokens <= 32 ? 2 : 4;
   p.tiles = ceil_div(rows, Small::kRows * p.tr) * ceil_div(tokens, 16 * p.tt);
   const int64_t nblk = ceil_div(cols, kColBlock);
-  const int64_t cap = p.tiles * nblk >= 4 * cus ? 2 * cus : cus;   // workgroups in the grid
+  // (a gated tile of 64 tokens is twice the work of a plain one: two workgroups a CU only for the tiles
+  // of 32; 2 x 4096 x 4096 x 200 30.6 us split so, 26.0 whole, 2 x 14336 x 4096 x 48 39.8 and 38.4)
+  const bool two = !gated || p.tt == 2;
+  const int64_t cap = two && p.tiles * nblk >= 4 * cus ? 2 * cus : cus;   // workgroups in the grid
   int s = 1;
   while (s < kMaxColSplits && p.tiles * (2 * s) <= cap && 2 * s <= nblk) s *= 2;
-  if (s == 1 && p.tiles * 2 <= 2 * cus && nblk >= 2) s = 2;
+  if (s == 1 && two && p.tiles * 2 <= 2 * cus && nblk >= 2) s = 2;
   if (s == 1) return p;
   p.blocks = int(ceil_div(nblk, s));
   p.splits = int(ceil_div(nblk, p.blocks));   // every split non-empty

@@ -12,9 +12,9 @@
 // The best tokens: each lane keeps the largest value that it saw, its tile, and the largest of its other
 // tiles. A limit that `top` of a workgroup's 256 largest meet is met by few elements more, and they
 // are looked for in the tiles of those lanes alone, 16 or 32 elements of one lane and tile at a time, by
-// as many threads (each lane through its own registers instead: 64 rows of 151936 23.7 us against
-// 41, most of it instructions that find nothing). What is found is put in order by counting, for each,
-// how many go before it.
+// as many threads (each lane through its own elements instead, in its registers or read again, most of it
+// instructions that find nothing: 256 rows of 151936 46 us against 41). What is found is put in order
+// by counting, for each, how many go before it.
 //
 // What bounds it: reading the logits once, with an exponential an element close behind (2047 rows of
 // 128256 fp16, 525 MB: 5.0 TB/s; 1024 in fp32 5.8). A row goes to several workgroups where there are few
