@@ -152,7 +152,11 @@ int spmm_dispatch(const uint16_t* values, const uint32_t* masks, const uint16_t*
     err = launch_prefill_spmm(values, masks, X, Y, rows, cols, batch, N, M, s, dev, workspace, workspace_bytes, e);
     return err == hipSuccess ? NM_OK : hip_fail(err);
   }
-  if (prefill_route(all, cols, batch, N, M, dev)) {  // matrix-core prefill product
+  // A gated product's skinny launches read two matrices for every 16 vectors, so its larger layers go
+  // to the prefill kernels at once (2 x 14336 x 4096, us skinny / prefill at 24 vectors: 2:4 53 / 37, 16:32
+  // 109 / 81; at 4096 rows and 32 vectors 22 / 25, 4:8 at 17408 x 5120 and 24 91 / 92)
+  const bool early = gated && batch > kSkinnyBatch && all > 2 * kSkinnyBeforePrefillMaxRows && M == 2 * N && (N == 2 || N == 16);
+  if (early || prefill_route(all, cols, batch, N, M, dev)) {  // matrix-core prefill product
     if (!prefill_fits(all, cols, batch)) return NM_ERR_SHAPE;
     err = launch_prefill_spmm(values, masks, X, Y, rows, cols, batch, N, M, s, dev, workspace, workspace_bytes, e);
     return err == hipSuccess ? NM_OK : hip_fail(err);

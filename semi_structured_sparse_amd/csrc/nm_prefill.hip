@@ -135,7 +135,7 @@ struct ColPlan {
 };
 
 // (gated: rows of both matrices, in tiles of 128, 64 of each)
-ColPlan colsplit_plan(int64_t rows, int64_t cols, int64_t tokens, const DeviceInfo& dev, bool gated = false) {
+ColPlan colsplit_plan(int64_t rows, int64_t cols, int64_t tokens, int mode, const DeviceInfo& dev, bool gated = false) {
   ColPlan p;
   p.tr = gated ? 2 : 1;
   if (use_large<SparseLarge>(rows, tokens, dev)) return p;
@@ -144,8 +144,9 @@ ColPlan colsplit_plan(int64_t rows, int64_t cols, int64_t tokens, const DeviceIn
   p.tiles = ceil_div(rows, Small::kRows * p.tr) * ceil_div(tokens, 16 * p.tt);
   const int64_t nblk = ceil_div(cols, kColBlock);
   // (a gated tile of 64 tokens is twice the work of a plain one: two workgroups a CU only for the tiles
-  // of 32; 2 x 4096 x 4096 x 200 30.6 us split so, 26.0 whole, 2 x 14336 x 4096 x 48 39.8 and 38.4)
-  const bool two = !gated || p.tt == 2;
+  // of 32, and for 16:32; 2:4 2 x 4096 x 4096 x 200 30.6 us split so, 26.0 whole, 2 x 14336 x 4096 x 48
+  // 39.8 and 38.4; 16:32 there 74 and 81)
+  const bool two = !gated || p.tt == 2 || mode == kPfExpand;
   const int64_t cap = two && p.tiles * nblk >= 4 * cus ? 2 * cus : cus;   // workgroups in the grid
   int s = 1;
   while (s < kMaxColSplits && p.tiles * (2 * s) <= cap && 2 * s <= nblk) s *= 2;
@@ -217,7 +218,7 @@ TallPlan tall_plan(int64_t rows, int64_t cols, int64_t tokens, int mode, const D
   const int64_t cus = dev.cu_count > 0 ? dev.cu_count : 256;
   const int64_t nblk = ceil_div(cols, kColBlock);
   double current;
-  const ColPlan p = colsplit_plan(rows, cols, tokens, dev, gated);
+  const ColPlan p = colsplit_plan(rows, cols, tokens, mode, dev, gated);
   const TileCost* small = mode_tile(mode, p.tr, p.tt);
   if (p.splits > 1 && small != nullptr) {
     current = split_estimate_us(int64_t(p.blocks) * kStepsPerBlock, *small, ceil_div(p.tiles * p.splits, cus),
@@ -282,7 +283,7 @@ size_t prefill_workspace_bytes(int64_t rows, int64_t cols, int64_t tokens, int n
   if (!prefill_fits(rows, cols, tokens)) return 0;
   const TallPlan t = tall_plan(rows, cols, tokens, pf_mode(n), dev, gated);
   if (t.tiles > 0) return tall_bytes(t, dev);
-  return colsplit_bytes(colsplit_plan(rows, cols, tokens, dev, gated), dev);
+  return colsplit_bytes(colsplit_plan(rows, cols, tokens, pf_mode(n), dev, gated), dev);
 }
 
 hipError_t launch_prefill_spmm(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y,
@@ -309,7 +310,7 @@ hipError_t launch_prefill_spmm(const uint16_t* values, const uint32_t* masks, co
     if (tp.tiles > 0 && workspace_bytes >= tall_bytes(tp, dev))
       return split(kernel(tall_kernel(tp, mode), tp.tr, tp.tt, true), tp.splits, tp.blocks, tp.tiles);
   }
-  const ColPlan p = colsplit_plan(all, cols, tokens, dev, gated);
+  const ColPlan p = colsplit_plan(all, cols, tokens, mode, dev, gated);
   const size_t need = colsplit_bytes(p, dev);
   if (need > 0 && workspace != nullptr && workspace_bytes >= need)
     return split(kernel(colsplit_kernel(p.tt, mode), p.tr, p.tt, true), p.splits, p.blocks, p.tiles);
@@ -340,7 +341,7 @@ const char* prefill_colsplit_variant(int64_t rows, int64_t cols, int64_t tokens,
     if (mode == kPfSplit) return "prefill_colsplit_kernel<2, 8, 64, 2, true>";
     return t.tr == 2 ? "prefill_colsplit_kernel<2, 8, 64, 2, false>" : "prefill_colsplit_kernel<4, 8, 64, 2, false>";
   }
-  const ColPlan p = colsplit_plan(rows, cols, tokens, dev);
+  const ColPlan p = colsplit_plan(rows, cols, tokens, mode, dev);
   if (p.splits == 1) return "";
   if (mode == kPfExpand)
     return p.tt == 2 ? "prefill_colsplit_expand_kernel<1, 2, 64, 2>" : "prefill_colsplit_expand_kernel<1, 4, 64, 2>";
