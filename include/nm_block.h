@@ -40,8 +40,10 @@ enum { NM_ACT_NONE = 0, NM_ACT_RELU = 1, NM_ACT_SILU = 2, NM_ACT_GELU = 3, NM_AC
  *             batch that it takes; nm_spmm_workspace_bytes says how much workspace it can use)
  *   bias      fp16 [rows], or NULL (none)
  *   residual  fp16 [batch][rows], or NULL (none); may be Y
- * Errors as nm_spmm_ws; NM_ERR_FORMAT: unknown activation; NM_ERR_ALIGN also for bias or residual
- * not 2-byte aligned. (8-byte aligned ones, with rows a multiple of 4, are read four at a time.) */
+ * Errors as nm_spmm_ws; NM_ERR_SHAPE also for rows above 2^26 - 64 or rows * batch above 2^35;
+ * NM_ERR_FORMAT: unknown activation; NM_ERR_ALIGN also for bias or residual not 2-byte aligned. (Y,
+ * bias and residual that are 16-byte aligned, with rows a multiple of 8, are moved 8 rows at a time.)
+ * One workspace serves these calls and nm_spmm_ws's in stream order, but not nm_logprobs's. */
 int nm_linear(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y, int64_t rows,
               int64_t cols, int64_t batch, int N, int M, const uint16_t* bias, int activation, float scale,
               const uint16_t* residual, void* workspace, size_t workspace_bytes, void* stream);
@@ -52,7 +54,7 @@ int nm_linear(const uint16_t* values, const uint32_t* masks, const uint16_t* X, 
  *   gate_bias, up_bias  fp16 [rows], or NULL
  *   workspace  as nm_spmm_ws's, of nm_gated_workspace_bytes or more (NULL, or less: columns are
  *              not split)
- * Errors as nm_linear; NM_ERR_SHAPE also where 2 * rows exceeds what rows may be. */
+ * Errors as nm_linear, whose limits here are 2 * rows'. */
 int nm_gated(const uint16_t* gate_values, const uint32_t* gate_masks, const uint16_t* up_values,
              const uint32_t* up_masks, const uint16_t* X, uint16_t* Y, int64_t rows, int64_t cols, int64_t batch,
              int N, int M, const uint16_t* gate_bias, const uint16_t* up_bias, int activation, void* workspace,
@@ -103,7 +105,8 @@ int nm_block_norm(const void* x, const uint16_t* branch, void* h, uint16_t* y, c
  *   logits       fp32, or fp16 (fp16_logits), row r at [r * stride], any alignment of its elements
  *   workspace    nm_logprobs_workspace_bytes of zeroed memory, 16-byte aligned, or NULL (with that,
  *                or less, rows are not split); a call leaves its counters at zero, so one serves any
- *                sequence of these calls and those of nm_decode.h in stream order
+ *                sequence of these calls and those of nm_decode.h in stream order (not the products',
+ *                whose counters lie otherwise)
  * Logits of -infinity have no probability and are never listed: entries past the last token with
  * one are -1 and -infinity. A row without any has log probabilities of -infinity and an entropy of
  * 0. A row with a NaN or +infinity has NaN for each number and -1 for each top token. Logits of the

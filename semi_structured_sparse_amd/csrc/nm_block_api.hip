@@ -21,6 +21,10 @@ int finish(hipError_t e) {
   return NM_ERR_HIP;
 }
 
+// Sizes of the block products whose every launch stays within a grid's 2^32 threads: 64 a row in the
+// single-vector kernels, 256 for 64 x 64 outputs of the prompt kernels. all: the rows of both matrices.
+bool grid_fits(int64_t all, int64_t batch) { return all <= (int64_t(1) << 26) - 64 && batch <= (int64_t(1) << 35) / all; }
+
 int norm_check(const NormCall& c, bool fp32, int64_t heads, int64_t width) {
   const uintptr_t wide = fp32 ? 4 : 2;
   if (!c.x || !c.y) return NM_ERR_NULL;
@@ -61,6 +65,7 @@ int nm_linear(const uint16_t* values, const uint32_t* masks, const uint16_t* X, 
               void* workspace, size_t workspace_bytes, void* stream) {
   const int st = nm::spmm_check(values, masks, X, Y, rows, cols, batch, N, M);
   if (st != NM_OK) return st;
+  if (!nm::grid_fits(rows, batch)) return NM_ERR_SHAPE;
   if (!within(activation, NM_ACT_NONE, NM_ACT_GELU_TANH)) return NM_ERR_FORMAT;
   if (!aligned(bias, 2) || !aligned(residual, 2)) return NM_ERR_ALIGN;
   const nm::BlockArgs e{nullptr, nullptr, bias, nullptr, residual, scale, activation};
@@ -77,6 +82,7 @@ int nm_gated(const uint16_t* gate_values, const uint32_t* gate_masks, const uint
   if (st == NM_OK && rows > INT64_MAX / 2) st = NM_ERR_SHAPE;
   if (st == NM_OK) st = nm::spmm_check(up_values, up_masks, X, Y, 2 * rows, cols, batch, N, M);
   if (st != NM_OK) return st;
+  if (!nm::grid_fits(2 * rows, batch)) return NM_ERR_SHAPE;
   if (!within(activation, NM_ACT_NONE, NM_ACT_GELU_TANH)) return NM_ERR_FORMAT;
   if (!aligned(gate_bias, 2) || !aligned(up_bias, 2)) return NM_ERR_ALIGN;
   const nm::BlockArgs e{up_values, up_masks, gate_bias, up_bias, nullptr, 1.0f, activation};

@@ -36,12 +36,14 @@ ROWS = [(dict(x=None), nm.NM_ERR_NULL), (dict(y=None), nm.NM_ERR_NULL), (dict(ki
 REFUSED = (
     [("nm_linear", LINEAR, kw, st) for kw, st in PRODUCT + [
         (dict(values=None), nm.NM_ERR_NULL), (dict(masks=None), nm.NM_ERR_NULL), (dict(bias=A + 1), nm.NM_ERR_ALIGN),
-        (dict(residual=A + 1), nm.NM_ERR_ALIGN), (dict(values=A + 8), nm.NM_ERR_ALIGN), (dict(rows=1 << 31), nm.NM_ERR_SHAPE)]] +
+        (dict(residual=A + 1), nm.NM_ERR_ALIGN), (dict(values=A + 8), nm.NM_ERR_ALIGN), (dict(rows=1 << 31), nm.NM_ERR_SHAPE),
+        (dict(rows=1 << 26), nm.NM_ERR_SHAPE), (dict(rows=1 << 20, batch=(1 << 15) + 1), nm.NM_ERR_SHAPE)]] +
     [("nm_gated", GATED, kw, st) for kw, st in PRODUCT + [
         (dict(gate_values=None), nm.NM_ERR_NULL), (dict(gate_masks=None), nm.NM_ERR_NULL), (dict(up_values=None), nm.NM_ERR_NULL),
         (dict(up_masks=None), nm.NM_ERR_NULL), (dict(gate_bias=A + 1), nm.NM_ERR_ALIGN), (dict(up_bias=A + 1), nm.NM_ERR_ALIGN),
         (dict(up_values=A + 8), nm.NM_ERR_ALIGN), (dict(up_masks=A + 2), nm.NM_ERR_ALIGN), (dict(rows=1 << 30), nm.NM_ERR_SHAPE),
-        (dict(rows=(1 << 63) - 1), nm.NM_ERR_SHAPE)]] +
+        (dict(rows=(1 << 63) - 1), nm.NM_ERR_SHAPE), (dict(rows=1 << 25), nm.NM_ERR_SHAPE),
+        (dict(rows=1 << 20, batch=(1 << 14) + 1), nm.NM_ERR_SHAPE)]] +
     [("nm_norm", NORM, kw, st) for kw, st in ROWS + [
         (dict(tokens=0), nm.NM_ERR_SHAPE), (dict(heads=0), nm.NM_ERR_SHAPE), (dict(heads=1 << 25), nm.NM_ERR_SHAPE),
         (dict(tokens=1 << 40), nm.NM_ERR_SHAPE), (dict(tokens=(1 << 26) + 1, heads=1, width=64), nm.NM_ERR_SHAPE),
