@@ -180,7 +180,9 @@ __device__ __forceinline__ void reduce_store(const Tile& w, f4_t acc, int cs_cou
   float4* red = reinterpret_cast<float4*>(lds_base);
   red[w.wave * 64 + w.lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
   __syncthreads();
-  if (w.cs != 0 || !w.active || w.second) return;
+  if (w.cs != 0 || !w.active) return;
+  if constexpr (FORM == kGatedForm)
+    if (w.second) return;
   float4 s = red[w.wave * 64 + w.lane];
   for (int k = 1; k < cs_count; ++k) {
     const float4 v = red[(w.wave + k) * 64 + w.lane];
