@@ -168,7 +168,7 @@ __host__ __device__ constexpr SplitEntry split_entry(int side, int byte) {
   return e;
 }
 
-// The tables as laid out in LDS (17 KiB): entry e's selectors at 32 e, its codes at
+// The tables as laid out in LDS by the plain products (17 KiB): entry e's selectors at 32 e, its codes at
 // kSplitSelBytes + 2 e. Built at compile time; each workgroup copies them to LDS once.
 struct SplitTable {
   uint4 sel[2 * kSplitEntries];
@@ -744,10 +744,27 @@ __device__ __forceinline__ bool split_handoff(f4_t (&acc)[TR][TT], const ColSpli
 // 2:4 directly on the sparse instruction; 4:8 and 8:16 split into two 2:4 operands (the
 // split tables); 16:32 expanded to dense fragments for the dense instruction (the expansion
 // table), one per 32-column word.
+// What the block products lay out otherwise in LDS, against bank conflicts (64 banks of 4 bytes). Tables:
+// the entries' first halves, then their second ones, so that random reads of one half reach every bank.
+// 16:32: a row's values 80 bytes apart.
+template <int FORM>
+constexpr uint32_t kExpandRow = FORM == kPlainForm ? 64 : 80;
+
+// LDS byte offset of half `half` (16 bytes) of entry `entry` of a table of `entries`, and of its i-th chunk.
+template <int FORM>
+__device__ __forceinline__ uint32_t table_half(uint32_t entry, uint32_t half, uint32_t entries) {
+  return FORM == kPlainForm ? 32u * entry + 16u * half : 16u * (half * entries + entry);
+}
+template <int FORM>
+__device__ __forceinline__ uint32_t table_chunk(uint32_t i, uint32_t entries) {
+  return FORM == kPlainForm || i >= 2 * entries ? 16u * i : table_half<FORM>(i >> 1, i & 1u, entries);
+}
+
 constexpr int kPfDirect = 0, kPfSplit = 1, kPfExpand = 2;
 // EXPAND: LDS bytes of one wave's value area per row tile: the step's values of its 16 rows
-// (64 bytes each) and room for a window read past the last row's second word
-constexpr uint32_t kPfAreaBytes = 16 * 64 + 64;
+// (kExpandRow apart) and room for a window read past the last row's second word
+template <int FORM = kPlainForm>
+constexpr uint32_t kPfAreaBytes = 16 * kExpandRow<FORM> + 64;
 
 // The sparse products: values [rows][cols / 2] fp16, masks [rows][cols / 32]; MODE as above
 // (lut: the pattern's table in LDS; area: EXPAND's per-wave value areas, TR per wave).
@@ -793,7 +810,9 @@ __device__ __forceinline__ void prefill_sparse_body(const uint16_t* __restrict__
     if constexpr (SPLIT || EXPAND) {
 #pragma unroll
       for (int j = 0; j < kLutPer; ++j)
-        if (tid + kThreads * j < kLutChunks) reinterpret_cast<uint4*>(lut)[tid + kThreads * j] = lreg[j];
+        if (tid + kThreads * j < kLutChunks)
+          *reinterpret_cast<uint4*>(lut + table_chunk<FORM>(uint32_t(tid + kThreads * j), EXPAND ? kExpandEntries : kSplitEntries)) =
+              lreg[j];
     }
   };
 
@@ -885,16 +904,17 @@ __device__ __forceinline__ void prefill_sparse_body(const uint16_t* __restrict__
   zero(acc);
   // X fragment of token 16 b + li: column chunks q and 4 + q of the step
   const uint32_t b_lo = x_offset<T::kRowBytes>(li, q), b_hi = x_offset<T::kRowBytes>(li, 4 + q);
-  // EXPAND: this wave's value areas (row tile a at a * kPfAreaBytes)
-  char* const warea = EXPAND ? area + uint32_t(wave) * TR * kPfAreaBytes : nullptr;
+  // EXPAND: this wave's value areas (row tile a at a * kPfAreaBytes<FORM>)
+  char* const warea = EXPAND ? area + uint32_t(wave) * TR * kPfAreaBytes<FORM> : nullptr;
   auto compute_expand = [&](const AF& f, const char* buf, auto pc) {
     constexpr int J = decltype(pc)::value;
     const int src = 4 * (li + 16 * (J >> 1));
-    // the step's values of the wave's rows to its areas (row li at 64 li: word 0's 16 values,
+    // the step's values of the wave's rows to its areas (row li at kExpandRow li: word 0's 16 values,
     // then word 1's; lane q's 16 bytes at 16 q), visible to the wave's other lanes before
     // they read them back
 #pragma unroll
-    for (int a = 0; a < TR; ++a) *reinterpret_cast<uint4*>(warea + a * kPfAreaBytes + 64 * li + 16 * q) = f.v[a][0];
+    for (int a = 0; a < TR; ++a)
+      *reinterpret_cast<uint4*>(warea + a * kPfAreaBytes<FORM> + kExpandRow<FORM> * uint32_t(li) + 16 * q) = f.v[a][0];
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -912,14 +932,14 @@ __device__ __forceinline__ void prefill_sparse_body(const uint16_t* __restrict__
         // first kept value of the byte among the word's 16 (clamped: any mask keeps the
         // window inside the areas)
         const uint32_t first = min(uint32_t(__builtin_popcount(wi & ((1u << (8 * q)) - 1u))), 16u);
-        const uint32_t off = uint32_t(a) * kPfAreaBytes + 64u * uint32_t(li) + 32u * uint32_t(i) + 2u * first;
+        const uint32_t off = uint32_t(a) * kPfAreaBytes<FORM> + kExpandRow<FORM> * uint32_t(li) + 32u * uint32_t(i) + 2u * first;
         const uint32_t* wd = reinterpret_cast<const uint32_t*>(warea + (off & ~3u));
         const uint32_t sh = (off & 2u) * 8u;   // 16 when the window starts mid-dword
         const uint32_t r0 = wd[0], r1 = wd[1], r2 = wd[2], r3 = wd[3], r4 = wd[4];
         const uint32_t v0 = __builtin_amdgcn_alignbit(r1, r0, sh), v1 = __builtin_amdgcn_alignbit(r2, r1, sh);
         const uint32_t v2 = __builtin_amdgcn_alignbit(r3, r2, sh), v3 = __builtin_amdgcn_alignbit(r4, r3, sh);
-        const uint4 s0 = *reinterpret_cast<const uint4*>(lut + 32u * byte);
-        const uint4 s1 = *reinterpret_cast<const uint4*>(lut + 32u * byte + 16u);
+        const uint4 s0 = *reinterpret_cast<const uint4*>(lut + table_half<FORM>(byte, 0, kExpandEntries));
+        const uint4 s1 = *reinterpret_cast<const uint4*>(lut + table_half<FORM>(byte, 1, kExpandEntries));
         auto pick = [&](uint32_t lo_sel, uint32_t hi_sel) {
           return __builtin_amdgcn_perm(v1, v0, lo_sel) | __builtin_amdgcn_perm(v3, v2, hi_sel);
         };
@@ -962,11 +982,11 @@ __device__ __forceinline__ void prefill_sparse_body(const uint16_t* __restrict__
       const uint32_t m16 = __builtin_amdgcn_ubfe((q >> 1) ? w1 : w0, uint32_t(mshift), 16);
       if constexpr (SPLIT) {
         // the lane's 16 mask bits select the table entries of its two bytes
-        const uint32_t e0 = 32u * (m16 & 0xFFu), e1 = 32u * (256u + (m16 >> 8));
-        const uint4 s0 = *reinterpret_cast<const uint4*>(lut + e0);
-        const uint4 s1 = *reinterpret_cast<const uint4*>(lut + e0 + 16);
-        const uint4 s2 = *reinterpret_cast<const uint4*>(lut + e1);
-        const uint4 s3 = *reinterpret_cast<const uint4*>(lut + e1 + 16);
+        auto half_of = [&](uint32_t entry, uint32_t half) {
+          return *reinterpret_cast<const uint4*>(lut + table_half<FORM>(entry, half, kSplitEntries));
+        };
+        const uint32_t e0 = m16 & 0xFFu, e1 = 256u + (m16 >> 8);
+        const uint4 s0 = half_of(e0, 0), s1 = half_of(e0, 1), s2 = half_of(e1, 0), s3 = half_of(e1, 1);
         const uint16_t* codes = reinterpret_cast<const uint16_t*>(lut + kSplitSelBytes);
         const uint32_t i0 = codes[m16 & 0xFFu], i1 = codes[256u + (m16 >> 8)];
         const uint4 v = f.v[a][0];
@@ -1064,7 +1084,7 @@ __global__ __launch_bounds__(kThreads) void prefill_expand_kernel(const uint16_t
   using T = Tile<TR, TT, KS>;
   __shared__ __attribute__((aligned(16))) char xs[2][T::kXBytes];
   __shared__ __attribute__((aligned(16))) char lut[kExpandBytes];
-  __shared__ __attribute__((aligned(16))) char area[kWaves * TR * kPfAreaBytes];
+  __shared__ __attribute__((aligned(16))) char area[kWaves * TR * kPfAreaBytes<>];
   const TileCoord tc = tile_of(int(blockIdx.x), (rows + T::kRows - 1) / T::kRows, (tokens + T::kTokens - 1) / T::kTokens);
   prefill_sparse_body<TR, TT, KS, D, kPfExpand, false>(values, masks, X, Y, rows, cols, tokens, xs, lut, area, tc, 0,
                                                        cols, ColSplit{});
@@ -1108,7 +1128,7 @@ __global__ __launch_bounds__(kThreads) void prefill_colsplit_expand_kernel(const
   using T = Tile<TR, TT, KS>;
   __shared__ __attribute__((aligned(16))) char xs[2][T::kXBytes];
   __shared__ __attribute__((aligned(16))) char lut[kExpandBytes];
-  __shared__ __attribute__((aligned(16))) char area[kWaves * TR * kPfAreaBytes];
+  __shared__ __attribute__((aligned(16))) char area[kWaves * TR * kPfAreaBytes<>];
   __shared__ unsigned flag;
   const int b = int(blockIdx.x);
   const int tile = b / splits, split = b - tile * splits;
@@ -1133,7 +1153,7 @@ __global__ __launch_bounds__(kThreads) void block_prefill_kernel(const uint16_t*
   constexpr int kOutRows = kWaves * 16 * out_tiles<TR, FORM>();
   __shared__ __attribute__((aligned(16))) char xs[2][T::kXBytes];
   __shared__ __attribute__((aligned(16))) char lut[table_bytes<MODE>()];
-  __shared__ __attribute__((aligned(16))) char area[MODE == kPfExpand ? kWaves * TR * kPfAreaBytes : 16];
+  __shared__ __attribute__((aligned(16))) char area[MODE == kPfExpand ? kWaves * TR * kPfAreaBytes<FORM> : 16];
   const TileCoord tc = tile_of(int(blockIdx.x), (rows + kOutRows - 1) / kOutRows, (tokens + T::kTokens - 1) / T::kTokens);
   prefill_sparse_body<TR, TT, KS, D, MODE, false, FORM>(values, masks, X, Y, rows, cols, tokens, xs, lut, area, tc, 0,
                                                         cols, ColSplit{}, e);
@@ -1150,7 +1170,7 @@ __global__ __launch_bounds__(kThreads) void block_colsplit_kernel(const uint16_t
   constexpr int kOutRows = kWaves * 16 * out_tiles<TR, FORM>();
   __shared__ __attribute__((aligned(16))) char xs[2][T::kXBytes];
   __shared__ __attribute__((aligned(16))) char lut[table_bytes<MODE>()];
-  __shared__ __attribute__((aligned(16))) char area[MODE == kPfExpand ? kWaves * TR * kPfAreaBytes : 16];
+  __shared__ __attribute__((aligned(16))) char area[MODE == kPfExpand ? kWaves * TR * kPfAreaBytes<FORM> : 16];
   __shared__ unsigned flag;
   const int b = int(blockIdx.x);
   const int tile = b / splits, split = b - tile * splits;

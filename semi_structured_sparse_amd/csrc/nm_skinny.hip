@@ -29,14 +29,18 @@ struct SkinnyShape {
 // tables the pattern needs).
 int mode_of(int n) { return n == 2 ? kModeDirect : n == 16 ? kModeExpand : kModeSplit; }
 
-size_t lead_of(int mode) {
-  return mode == kModeSplit ? lead_bytes<kModeSplit>() : mode == kModeExpand ? lead_bytes<kModeExpand>() : 0;
+size_t lead_of(int mode, int form = kPlainForm) {
+  return mode == kModeSplit                         ? lead_bytes<kModeSplit>()
+         : mode == kModeExpand && form != kPlainForm ? lead_bytes<kModeExpand, kLinearForm>()
+         : mode == kModeExpand                       ? lead_bytes<kModeExpand>()
+                                                     : 0;
 }
 
-size_t x_budget(int mode, const DeviceInfo& dev, int chunks = kXChunksPerThread) {
+size_t x_budget(int mode, const DeviceInfo& dev, int form = kPlainForm) {
   const size_t lds = size_t(dev.max_lds_per_block > 0 ? dev.max_lds_per_block : 65536);
-  const size_t lead = lead_of(mode);
+  const size_t lead = lead_of(mode, form);
   const size_t avail = lds > lead ? lds - lead : 0;
+  const int chunks = form == kPlainForm ? kXChunksPerThread : kBlockXChunks;
   return std::min<size_t>(kMaxXBytes / kXChunksPerThread * chunks, avail);
 }
 
@@ -73,14 +77,14 @@ SkinnyShape skinny_shape(int64_t rows, int64_t cols, int tokens, int mode, const
   s.splits = with_ws && s.rg == 1 ? splits_for(tiles, cols, tokens, mode, dev) : 1;
   s.grid = ceil_div(tiles, want) * s.splits;
   // phases of whole 128-column lines (the loads of the 2:4 and split kernels cover lines)
-  const size_t budget = x_budget(mode, dev, form == kPlainForm ? kXChunksPerThread : kBlockXChunks);
+  const size_t budget = x_budget(mode, dev, form);
   const int64_t pc_max = int64_t(budget / (2 * size_t(tokens))) / 128 * 128;
   s.phase_cols = int(std::min<int64_t>(pc_max, ceil_div(cols, 128) * 128));
   if (form != kPlainForm && pc_max >= 128 * s.cs) {   // phases of whole lines for every wave, evenly many
     const int64_t lines = ceil_div(ceil_div(cols, 128), s.cs), most = pc_max / (128 * s.cs);
     s.phase_cols = int(std::min<int64_t>(ceil_div(lines, ceil_div(lines, most)) * s.cs, ceil_div(cols, 128)) * 128);
   }
-  s.lds = std::max(lead_of(mode) + x_bytes(tokens, s.phase_cols), red_bytes(kMaxWaves));
+  s.lds = std::max(lead_of(mode, form) + x_bytes(tokens, s.phase_cols), red_bytes(kMaxWaves));
   return s;
 }
 

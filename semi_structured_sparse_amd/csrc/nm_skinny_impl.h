@@ -22,7 +22,7 @@
 //
 // 16:32 (skinny_expand_kernel): a word's 16 kept values may sit anywhere in its 32 columns,
 // so the dense 16 x 16 x 32 instruction takes each word, with the lanes' fragments expanded
-// to dense columns: each wave writes the step's loaded values (16 rows x 64 bytes) to its
+// to dense columns: each wave writes the step's loaded values (64 bytes of each of 16 rows) to its
 // own LDS area, and lane (row, q) reads the 8 halves from its mask byte's first kept value
 // on and places them with the expansion table below (skinny_expand_body).
 #pragma once
@@ -54,22 +54,28 @@ __host__ __device__ inline size_t red_bytes(int waves) { return size_t(waves) * 
 
 // LDS byte offset of 16-byte chunk c of token t, rows of rb bytes: the low 3 bits of the
 // chunk index are XORed with the token's (8 tokens read at a time land on 8 bank groups).
+template <int SWAPPED = 7>
 __device__ __forceinline__ uint32_t xoff(int t, int c, uint32_t rb) {
-  return uint32_t(t) * rb + (uint32_t(c ^ (t & 7)) << 4);
+  return uint32_t(t) * rb + (uint32_t(c ^ (t & SWAPPED)) << 4);
 }
 
 // What the kernel does with the packed operand: 2:4 directly, 4:8 / 8:16 split, 16:32
 // expanded.
 constexpr int kModeDirect = 0, kModeSplit = 1, kModeExpand = 2;
+// The block products' X chunks are XORed with 4 bits of the token (16 tokens on 16 bank groups): 4:8 at
+// 16 vectors 2 to 5% faster; 2:4, which does not wait for LDS, is as fast either way.
+template <int FORM>
+constexpr int kSwapped = FORM == kPlainForm ? 7 : 15;
 // EXPAND: LDS bytes of one wave's area: the step's values of 16 rows (64 bytes each) and
 // room for a window read past the last row's second word
-constexpr uint32_t kExpandWaveBytes = 16 * 64 + 64;
+template <int FORM>
+constexpr uint32_t kExpandWaveBytes = 16 * kExpandRow<FORM> + 64;
 
 // LDS bytes ahead of X: the split tables, or the expansion table and the waves' value areas.
-template <int MODE>
+template <int MODE, int FORM = kPlainForm>
 __host__ __device__ constexpr uint32_t lead_bytes() {
   return MODE == kModeSplit ? kSplitLutBytes
-       : MODE == kModeExpand ? kExpandBytes + uint32_t(kMaxWaves) * kExpandWaveBytes
+       : MODE == kModeExpand ? kExpandBytes + uint32_t(kMaxWaves) * kExpandWaveBytes<FORM>
                              : 0u;
 }
 
@@ -124,7 +130,7 @@ struct Tile {
 // X[0 .. tokens)[p0 .. p0 + chunks * 8) of one phase: flat chunk k = tid + kThreadsFixed * j
 // of token t = k / chunks, chunk c = k % chunks (one division, then steps of kThreadsFixed).
 // Chunks past the row load out of range (zero); chunks past the end are not written.
-template <int CHUNKS>
+template <int CHUNKS, int SWAPPED = 7>
 struct XStage {
   uint4 xs[CHUNKS];
   uint32_t xdst[CHUNKS];
@@ -141,7 +147,7 @@ struct XStage {
       const int col = p0 + 8 * c;
       const bool ok = k < nchunks && col < cols;
       xs[j] = buf_load16(xr, ok ? (uint32_t(t) * uint32_t(cols) + uint32_t(col)) * 2u : kOutOfRange);
-      xdst[j] = k < nchunks ? xoff(t, c, rb) : 0xFFFFFFFFu;
+      xdst[j] = k < nchunks ? xoff<SWAPPED>(t, c, rb) : 0xFFFFFFFFu;
       t += dt;
       c += dc;
       if (c >= chunks) { c -= chunks; ++t; }
@@ -274,7 +280,7 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
   constexpr bool SPLIT = MODE == kModeSplit;
   static_assert(MODE == kModeDirect || MODE == kModeSplit, "whole-line loads: 2:4 and the split patterns");
   extern __shared__ __attribute__((aligned(16))) char lds_base[];
-  char* const lds = lds_base + lead_bytes<MODE>();   // SPLIT: the split tables first, X after them
+  char* const lds = lds_base + lead_bytes<MODE, FORM>();   // SPLIT: the split tables first, X after them
   const int tid = threadIdx.x;
   static_assert(!COLS || FORM != kGatedForm, "gated products have no column splits here");
   const Tile w(values, masks, X, rows, cols, tokens, rg_count, cs_count, COLS ? sw.splits : 1, FORM == kGatedForm, e);
@@ -332,7 +338,7 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
       const uint32_t cm = uint32_t(c_lo + 128 * min(p, last)) >> 3;
       mnext = buf_load8(w.mr, n > 0 ? moff + cm : kOutOfRange);
     };
-    XStage<(FORM == kPlainForm ? kXChunksPerThread : kBlockXChunks)> xst;
+    XStage<(FORM == kPlainForm ? kXChunksPerThread : kBlockXChunks), kSwapped<FORM>> xst;
     xst.load(w.xr, tokens, cols, p0, plines * 16, rb);
     // then the first weight loads, in flight while X is written to LDS (the X loads were
     // issued first, so waiting for them does not wait for these; mask block first, as in
@@ -343,7 +349,7 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
     __syncthreads();                                 // the previous phase's LDS reads are done
     if constexpr (SPLIT) {
       if (p0 == c_beg) {
-        reinterpret_cast<uint4*>(lds_base)[tid] = lut_a;
+        *reinterpret_cast<uint4*>(lds_base + table_chunk<FORM>(uint32_t(tid), kSplitEntries)) = lut_a;
         if (tid < 64) reinterpret_cast<uint4*>(lds_base)[2 * kSplitEntries + tid] = lut_b;
       }
     }
@@ -351,8 +357,8 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
     __syncthreads();
     if (n > 0) {
       // X fragment addresses of products 0 and 1 of the phase's first line
-      const uint32_t b_lo0 = xoff(xt, xq, rb), b_hi0 = xoff(xt, xq + 8, rb);
-      const uint32_t b_lo1 = xoff(xt, xq + 2, rb), b_hi1 = xoff(xt, xq + 10, rb);
+      const uint32_t b_lo0 = xoff<kSwapped<FORM>>(xt, xq, rb), b_hi0 = xoff<kSwapped<FORM>>(xt, xq + 8, rb);
+      const uint32_t b_lo1 = xoff<kSwapped<FORM>>(xt, xq + 2, rb), b_hi1 = xoff<kSwapped<FORM>>(xt, xq + 10, rb);
       for (int pb = 0; pb < n; pb += kMaskLines) {
         // 2:4: the position codes of the block's words, once per block
         mcur = SPLIT ? mnext : make_uint2(pair_codes32(mnext.x), pair_codes32(mnext.y));
@@ -390,11 +396,11 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
             const h16_t bf = __builtin_bit_cast(h16_t, xv);
             const uint32_t m16 = __builtin_amdgcn_ubfe(word, 16u * uint32_t(h), 16);
             if constexpr (SPLIT) {
-              const uint32_t e0 = 32u * (m16 & 0xFFu), e1 = 32u * (256u + (m16 >> 8));
-              const uint4 s0 = *reinterpret_cast<const uint4*>(lds_base + e0);
-              const uint4 s1 = *reinterpret_cast<const uint4*>(lds_base + e0 + 16);
-              const uint4 s2 = *reinterpret_cast<const uint4*>(lds_base + e1);
-              const uint4 s3 = *reinterpret_cast<const uint4*>(lds_base + e1 + 16);
+              auto half_of = [&](uint32_t entry, uint32_t half) {
+                return *reinterpret_cast<const uint4*>(lds_base + table_half<FORM>(entry, half, kSplitEntries));
+              };
+              const uint32_t e0 = m16 & 0xFFu, e1 = 256u + (m16 >> 8);
+              const uint4 s0 = half_of(e0, 0), s1 = half_of(e0, 1), s2 = half_of(e1, 0), s3 = half_of(e1, 1);
               const uint16_t* codes = reinterpret_cast<const uint16_t*>(lds_base + kSplitSelBytes);
               const uint32_t i0 = codes[m16 & 0xFFu], i1 = codes[256u + (m16 >> 8)];
               auto pick = [&](uint32_t lo_sel, uint32_t hi_sel) {
@@ -433,7 +439,7 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
                                                    int phase_cols, const BlockArgs& e = BlockArgs{}) {
   extern __shared__ __attribute__((aligned(16))) char lds_base[];
   // the expansion table and the waves' value areas, then X
-  char* const lds = lds_base + lead_bytes<kModeExpand>();
+  char* const lds = lds_base + lead_bytes<kModeExpand, FORM>();
   const int tid = threadIdx.x;
   const Tile w(values, masks, X, rows, cols, tokens, rg_count, cs_count, 1, FORM == kGatedForm, e);
   const int q = w.q, li = w.li;
@@ -445,7 +451,7 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
   const int qcol = 32 * (q >> 1);
   // token rows past the batch read the last token's X: their products are never stored
   const int xt = min(li, tokens - 1);
-  char* const area = lds_base + kExpandBytes + uint32_t(w.wave) * kExpandWaveBytes;
+  char* const area = lds_base + kExpandBytes + uint32_t(w.wave) * kExpandWaveBytes<FORM>;
 
   f4_t acc = f4_t{0.f, 0.f, 0.f, 0.f};
   uint4 vbuf[kDepth];
@@ -478,7 +484,8 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) load_v(vbuf[d], d);
     __syncthreads();                                 // the previous phase's LDS reads are done
-    if (p0 == 0 && tid < 2 * kExpandEntries) reinterpret_cast<uint4*>(lds_base)[tid] = lut;
+    if (p0 == 0 && tid < 2 * kExpandEntries)
+      *reinterpret_cast<uint4*>(lds_base + table_chunk<FORM>(uint32_t(tid), kExpandEntries)) = lut;
     xst.store(lds);
     __syncthreads();
     if (n > 0) {
@@ -504,7 +511,7 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
           const uint32_t w1 = uint32_t(__builtin_amdgcn_ds_bpermute(src, int(mcur.y)));
           // the step's values to this wave's area (row li at 64 li, lane q's 16 bytes at
           // 16 q), visible to the other lanes of the wave before they are read back
-          *reinterpret_cast<uint4*>(area + 64 * li + 16 * q) = cur;
+          *reinterpret_cast<uint4*>(area + kExpandRow<FORM> * uint32_t(li) + 16 * q) = cur;
           __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
           __builtin_amdgcn_wave_barrier();
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -515,14 +522,14 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
             // first kept value of the lane's byte among the word's 16 (at most 16 for a
             // valid mask; clamped so that any mask keeps the window inside the area)
             const uint32_t first = min(uint32_t(__builtin_popcount(wi & ((1u << (8 * q)) - 1u))), 16u);
-            const uint32_t off = 64u * uint32_t(li) + 32u * uint32_t(i) + 2u * first;   // window, bytes
+            const uint32_t off = kExpandRow<FORM> * uint32_t(li) + 32u * uint32_t(i) + 2u * first;   // window, bytes
             const uint32_t* wd = reinterpret_cast<const uint32_t*>(area + (off & ~3u));
             const uint32_t sh = (off & 2u) * 8u;   // 16 when the window starts mid-dword
             const uint32_t r0 = wd[0], r1 = wd[1], r2 = wd[2], r3 = wd[3], r4 = wd[4];
             const uint32_t v0 = __builtin_amdgcn_alignbit(r1, r0, sh), v1 = __builtin_amdgcn_alignbit(r2, r1, sh);
             const uint32_t v2 = __builtin_amdgcn_alignbit(r3, r2, sh), v3 = __builtin_amdgcn_alignbit(r4, r3, sh);
-            const uint4 s0 = *reinterpret_cast<const uint4*>(lds_base + 32u * byte);
-            const uint4 s1 = *reinterpret_cast<const uint4*>(lds_base + 32u * byte + 16u);
+            const uint4 s0 = *reinterpret_cast<const uint4*>(lds_base + table_half<FORM>(byte, 0, kExpandEntries));
+            const uint4 s1 = *reinterpret_cast<const uint4*>(lds_base + table_half<FORM>(byte, 1, kExpandEntries));
             auto pick = [&](uint32_t lo_sel, uint32_t hi_sel) {
               return __builtin_amdgcn_perm(v1, v0, lo_sel) | __builtin_amdgcn_perm(v3, v2, hi_sel);
             };
