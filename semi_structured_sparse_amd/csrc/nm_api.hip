@@ -103,8 +103,14 @@ bool prefill_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, cons
 // against 97.2 and 106; 14336 x 4096 at 64 26.8 against 27.9. At 16 vectors and below one
 // skinny launch is as fast or faster (4096 x 4096 2:4: 9.2 against 11.9).
 bool colsplit_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev, bool gated) {
-  const bool size = batch > kSkinnyBatch || (N == 16 && batch >= kExpandColSplitMinBatch &&
-                                             (gated ? 2 * rows : rows) <= kExpandColSplitMaxRows);
+  const int64_t all = gated ? 2 * rows : rows;
+  // gated products of few long rows: no column splits for them in the skinny kernels (us at 12 vectors, skinny /
+  // this: 2:4 2 x 512 x 8192 16.0 / 11.0, 2 x 2048 x 8192 16.1 / 12.8; 4:8 17.5 / 14.9, 17.9 / 17.0; 16:32
+  // 2 x 2048 x 8192 22.7 / 19.0; two of 4096 x 14336 34 / 39 in 4:8)
+  const bool few_long = gated && cols >= kGatedColSplitMinCols && all <= kSkinnyBeforePrefillMaxRows &&
+                        batch >= (N == 16 ? kExpandColSplitMinBatch : kGatedColSplitMinBatch);
+  const bool size = batch > kSkinnyBatch || few_long ||
+                    (N == 16 && batch >= kExpandColSplitMinBatch && all <= kExpandColSplitMaxRows);
   return size && prefill_pattern(N, M) && prefill_workspace_bytes(rows, cols, batch, N, dev, gated) > 0;
 }
 
@@ -152,10 +158,18 @@ int spmm_dispatch(const uint16_t* values, const uint32_t* masks, const uint16_t*
     err = launch_prefill_spmm(values, masks, X, Y, rows, cols, batch, N, M, s, dev, workspace, workspace_bytes, e);
     return err == hipSuccess ? NM_OK : hip_fail(err);
   }
-  // A gated product's skinny launches read two matrices for every 16 vectors, so its larger layers go
-  // to the prefill kernels at once (2 x 14336 x 4096, us skinny / prefill at 24 vectors: 2:4 53 / 37, 16:32
-  // 109 / 81; at 4096 rows and 32 vectors 22 / 25, 4:8 at 17408 x 5120 and 24 91 / 92)
-  const bool early = gated && batch > kSkinnyBatch && all > 2 * kSkinnyBeforePrefillMaxRows && M == 2 * N && (N == 2 || N == 16);
+  // A gated product's skinny launches read two matrices for every 16 vectors, so its larger layers go to the
+  // prefill kernels at once, and 16:32 block products earlier than plain ones (us skinny / prefill, no workspace:
+  // gated 2:4 2 x 14336 x 4096 at 24 vectors 54 / 36, 2 x 4096 x 4096 at 32 22.8 / 25.5, 4:8 2 x 17408 x 5120 at 24
+  // 81 / 83; 16:32 14336 x 4096 at 17 34 / 34, at 24 42 / 34, 17408 x 5120 at 17 53 / 64, at 24 67 / 64, 7168 x
+  // 5120 at 32 37 / 41, at 48 56 / 41; gated 2 x 14336 x 4096 at 17 70 / 53, 2 x 7168 x 5120 at 32 61 / 63)
+  const int64_t large = 2 * kSkinnyBeforePrefillMaxRows;
+  bool early = false;
+  if (e != nullptr && N == 2 && M == 4) early = gated && batch > kSkinnyBatch && all > large;
+  if (e != nullptr && N == 16 && M == 32)
+    early = (batch > 2 * kSkinnyBatch && rows > kSkinnyBeforePrefillMaxRows) ||
+            (gated ? batch > kSkinnyBatch && all > 2 * large : batch >= kSkinnyBatch + kSmallBatch && all > large);
+  early = early && prefill_fits(all, cols, batch);
   if (early || prefill_route(all, cols, batch, N, M, dev)) {  // matrix-core prefill product
     if (!prefill_fits(all, cols, batch)) return NM_ERR_SHAPE;
     err = launch_prefill_spmm(values, masks, X, Y, rows, cols, batch, N, M, s, dev, workspace, workspace_bytes, e);
@@ -168,7 +182,7 @@ int spmm_dispatch(const uint16_t* values, const uint32_t* masks, const uint16_t*
     // vectors at a time
     for (int64_t b0 = 0; b0 < batch; b0 += kSkinnyBatch) {
       const int64_t nb = batch - b0 < kSkinnyBatch ? batch - b0 : kSkinnyBatch;
-      if (skinny_expand_chunk(all, cols, nb, dev)) {
+      if (e ? block_expand_chunk(rows, cols, nb, gated, dev) : skinny_expand_chunk(rows, cols, nb, dev)) {
         err = skinny(b0, nb, nullptr, 0);
         if (err != hipSuccess) return hip_fail(err);
         continue;
@@ -180,13 +194,20 @@ int spmm_dispatch(const uint16_t* values, const uint32_t* masks, const uint16_t*
     }
     return NM_OK;
   }
-  if (use_skinny(all, cols, batch < kSkinnyBatch ? batch : kSkinnyBatch, N, M, dev)) {
+  // up to 8 vectors of two short matrices: a skinny launch has no column split for them (us at 8 vectors, skinny /
+  // small: 2:4 2 x 1024 x 4096 9.6 / 8.9, x 8192 14.4 / 13.5, 2 x 1536 x 5120 11.3 / 12.9; 4:8 10.6 / 8.7, 15.6 /
+  // 13.3, 12.9 / 12.4, 2 x 2048 x 4096 10.8 / 10.8)
+  auto skinny_takes = [&](int64_t count) {
+    if (gated && count <= kSmallBatch && (N == 2 ? rows <= kSkinnyMinRows / 2 : rows < kSkinnyMinRows)) return false;
+    return use_skinny(all, cols, count, N, M, dev);
+  };
+  if (skinny_takes(batch < kSkinnyBatch ? batch : kSkinnyBatch)) {
     // 50% patterns at 5..31 vectors where measured faster: the matrix instructions, 16
     // vectors per launch (launches in stream order, so one workspace serves them all); a
     // last launch too small for them (17..20 vectors leave 1..4) runs on the small-batch kernel
     for (int64_t b0 = 0; b0 < batch; b0 += kSkinnyBatch) {
       const int64_t nb = batch - b0 < kSkinnyBatch ? batch - b0 : kSkinnyBatch;
-      if (use_skinny(all, cols, nb, N, M, dev)) {
+      if (skinny_takes(nb)) {
         err = skinny(b0, nb, workspace, workspace_bytes);
       } else {
         err = small(b0, nb < kSmallBatch ? nb : kSmallBatch);

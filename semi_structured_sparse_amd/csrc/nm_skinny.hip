@@ -122,6 +122,17 @@ bool skinny_expand_chunk(int64_t rows, int64_t cols, int64_t tokens, const Devic
   return tokens >= kSkinnyExpandMinBatch && rows >= kSkinnyExpandMinRows && cols <= kSkinnyExpandMaxCols;
 }
 
+// Block products, us small-batch / expansion: 17408 x 5120 at 6 vectors 35.0 / 30.7, at 9 57.3 / 34.2; 7168 x 5120
+// at 8 16.8 / 16.8, at 9 26.3 / 17.0; 2048 x 4096 at 8 7.5 / 9.5, at 9 11.0 / 9.6; 1024 x 8192 at 9 13.8 / 14.8,
+// at 12 16.9 / 15.8. Gated: 2 x 7168 x 5120 at 5 21.8 / 23.5, at 6 28.5 / 23.9; 2 x 5120 x 17408 at 8 60 / 70,
+// at 13 108 / 80; 2 x 1024 x 8192 at 12 20.6 / 22.8, at 14 24.0 / 22.4.
+bool block_expand_chunk(int64_t rows, int64_t cols, int64_t tokens, bool gated, const DeviceInfo& dev) {
+  if (rows < kSkinnySmallMinRows || !skinny_fits(rows, cols, kSkinnyBatch, 16, 32, dev)) return false;
+  const int64_t all = gated ? 2 * rows : rows;
+  return tokens >= (gated ? 14 : 12) || (tokens > kSmallBatch && rows >= kSkinnyMinRows) ||
+         (tokens >= 6 && all > 2 * kSkinnyBeforePrefillMaxRows && cols <= 8192);   // X in one phase
+}
+
 const char* skinny_variant(int n) {
   return n == 2 ? "skinny_spmm_kernel<1, false>" : n == 16 ? "skinny_expand_kernel<1>" : "skinny_spmm_kernel<1, true>";
 }
