@@ -5,7 +5,9 @@
 // mean, then the squares around it, which keeps the digits that mean(v^2) - mean(v)^2 loses), and as
 // many before it for the norm after the branch. Sums are in fp32 in a fixed order.
 //
-// What bounds it: the bytes of the rows, once in and once out; for few rows the trips to memory.
+// What bounds it: the bytes of the rows, once in and once out (8191 rows of 8192 in fp32 with a branch,
+// 805 MB: 151 us, 5.3 TB/s; 81920 heads of 128: 8.7 us, 4.8); for few rows the trips to memory (8 rows of
+// 4096: 3.9 us on the device, little more than an empty launch).
 #include "nm_block_internal.h"
 #include "nm_epilogue.h"
 
