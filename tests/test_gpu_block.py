@@ -44,6 +44,10 @@ def near(got, want, slack, what):
 BATCHES = [1, 2, 3, 4, 5, 8, 9, 16, 17, 21, 32, 33, 49, 65, 130, 200]
 SHAPES = [(37, 96), (64, 256), (300, 1056), (1000, 4096), (2056, 512), (4104, 2080)]
 EVERY = [(p, b, s) for p in nm.PATTERNS for b, s in itertools.product(BATCHES, SHAPES) if b * s[0] * s[1] <= 3e8]
+# two long matrices of few rows, whose columns are split from 9 (16:32: 12) vectors on; X in several phases;
+# 16:32 on many rows, from 6 vectors on the matrix instructions and from 17, 24 or 33 on the prompt kernels
+EVERY += [(p, b, s) for p in nm.PATTERNS for b, s in itertools.product([9, 12, 16], [(300, 8192), (2048, 8224), (40, 14368)])]
+EVERY += [((16, 32), b, (8200, 160)) for b in (5, 6, 7, 12, 14, 16, 17, 23, 24, 33, 40)]
 
 
 @pytest.mark.parametrize("pattern,batch,shape", EVERY, ids=str)
