@@ -8,7 +8,7 @@
 // hundreds of products that made its sum, and a kernel for each would multiply the library.
 #pragma once
 
-#include "nm_block.h"
+#include "../../include/nm_block.h"   // by its place: programs that check a kernel header give csrc alone
 #include "nm_internal.h"
 
 namespace nm {
