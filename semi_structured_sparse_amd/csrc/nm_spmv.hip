@@ -99,7 +99,8 @@ hipError_t launch_kernel(const uint16_t* values, const uint32_t* masks, const ui
   const uint4* x4 = reinterpret_cast<const uint4*>(x);
   int rpb = s.rpb, cs = s.cs;
   void* args[] = {&v4, &masks, &x4, &y, &rows, &cols, &rpb, &cs, const_cast<BlockArgs*>(e)};
-  return launch(e ? block_spmv_kernel_for(form_of(e), N, DEC, s.ci) : kernel_for<N, DEC>(s.ci), dim3(unsigned(s.grid)), dim3(unsigned(64 * s.row_groups * s.cs)), args,
+  const void* k = e ? block_spmv_kernel_for(form_of(e), N, DEC, s.ci) : kernel_for<N, DEC>(s.ci);
+  return launch(k, dim3(unsigned(s.grid)), dim3(unsigned(64 * s.row_groups * s.cs)), args,
                 lds_bytes<DEC>(cols), stream, dev);
 }
 

@@ -524,7 +524,8 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int kind = int(c.whole(a[7]));
   const float offset = float(c.number(a[8])), eps = float(c.number(a[9]));
   if (!c.good) return not_here();
-  THPObjectPtr h = a[10] == Py_None ? THPObjectPtr(THPVariable_Wrap(made(x.shape, t.scalar_type(), c.device))) : output(a[10], x.shape, c.device);
+  THPObjectPtr h = a[10] != Py_None ? output(a[10], x.shape, c.device)
+                                    : THPObjectPtr(THPVariable_Wrap(made(x.shape, t.scalar_type(), c.device)));
   THPObjectPtr out = output(a[11], x.shape, c.device);
   const Spaced hs = spaced(c, h, x.fp32), ys = spaced(c, out, false);
   if (!c.good || hs.fp32 != x.fp32) return not_here();
