@@ -97,6 +97,23 @@ bool prefill_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, cons
   return !(short_batch && use_skinny(rows, cols, kSkinnyBatch, N, M, dev));
 }
 
+// Block products of 17 to 32 vectors of 2:4, 4:8 and 8:16 in one skinny launch: the weights are read once, where
+// two launches of 16 read them twice, and unsplit prompt kernels fill the card badly (us without a workspace,
+// 24 vectors, those / this: 2:4 2048 x 4096 14.5 / 10.8, 17408 x 5120 45.6 / 28.6, 4:8 48.5 / 31.7, 4096 x 14336
+// 43.1 / 37.5; gated 2:4 2 x 17408 x 5120 83.0 / 52.4, 2 x 4096 x 14336 60.7 / 40.2).
+bool wide_fits(int64_t all, int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev) {
+  return batch > kSkinnyBatch && batch <= 2 * kSkinnyBatch && M == 2 * N && N != 16 && all >= kSkinnySmallMinRows &&
+         skinny_fits(rows, cols, kSkinnyBatch, N, M, dev);
+}
+
+// Where a gated product of so many vectors needs no workspace: also before the column splits on many rows, with X
+// in two or three phases (us, column splits / skinny, 24 vectors: 2:4 2 x 7168 x 5120 29.8 / 23.3, 2 x 14336 x 4096
+// 36.1 / 33.2, 4:8 30.0 / 25.9, 38.4 / 36.6; 2:4 2 x 8192 x 8192 37.5 / 39.2, 2 x 4096 x 4096 13.2 / 15.7).
+bool wide_first(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev) {
+  return 2 * rows > 2 * kSkinnyBeforePrefillMaxRows && cols <= kWideFirstMaxCols &&
+         wide_fits(2 * rows, rows, cols, batch, N, M, dev);
+}
+
 // From a sweep on MI355X at 17..256 vectors (µs, column split against the unsplit prefill
 // kernel and against 16-vector skinny launches): 4096 x 4096 2:4 at 32 vectors 10.8 against
 // 25.9 and 16.7; 1024 x 8192 at 64 12.3 against 48.7 and 46.3; 4096 x 14336 4:8 at 64 30.7
@@ -104,6 +121,7 @@ bool prefill_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, cons
 // skinny launch is as fast or faster (4096 x 4096 2:4: 9.2 against 11.9).
 bool colsplit_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev, bool gated) {
   const int64_t all = gated ? 2 * rows : rows;
+  if (gated && wide_first(rows, cols, batch, N, M, dev)) return false;
   // gated products of few long rows: no column splits for them in the skinny kernels (us at 12 vectors, skinny /
   // this: 2:4 2 x 512 x 8192 16.0 / 11.0, 2 x 2048 x 8192 16.1 / 12.8; 4:8 17.5 / 14.9, 17.9 / 17.0; 16:32
   // 2 x 2048 x 8192 22.7 / 19.0; two of 4096 x 14336 34 / 39 in 4:8)
@@ -158,14 +176,15 @@ int spmm_dispatch(const uint16_t* values, const uint32_t* masks, const uint16_t*
     err = launch_prefill_spmm(values, masks, X, Y, rows, cols, batch, N, M, s, dev, workspace, workspace_bytes, e);
     return err == hipSuccess ? NM_OK : hip_fail(err);
   }
-  // A gated product's skinny launches read two matrices for every 16 vectors, so its larger layers go to the
-  // prefill kernels at once, and 16:32 block products earlier than plain ones (us skinny / prefill, no workspace:
-  // gated 2:4 2 x 14336 x 4096 at 24 vectors 54 / 36, 2 x 4096 x 4096 at 32 22.8 / 25.5, 4:8 2 x 17408 x 5120 at 24
-  // 81 / 83; 16:32 14336 x 4096 at 17 34 / 34, at 24 42 / 34, 17408 x 5120 at 17 53 / 64, at 24 67 / 64, 7168 x
-  // 5120 at 32 37 / 41, at 48 56 / 41; gated 2 x 14336 x 4096 at 17 70 / 53, 2 x 7168 x 5120 at 32 61 / 63)
+  if (e != nullptr && wide_fits(all, rows, cols, batch, N, M, dev)) {
+    err = launch_block_skinny_wide(values, masks, X, Y, rows, cols, int(batch), N, M, s, dev, *e);
+    return err == hipSuccess ? NM_OK : hip_fail(err);
+  }
+  // 16:32 block products go to the prompt kernels earlier than plain ones (us skinny / prefill, no workspace:
+  // 14336 x 4096 at 17 vectors 34 / 34, at 24 42 / 34, 17408 x 5120 at 17 53 / 64, at 24 67 / 64, 7168 x 5120 at 32
+  // 37 / 41, at 48 56 / 41; gated 2 x 14336 x 4096 at 17 70 / 53, 2 x 7168 x 5120 at 32 61 / 63)
   const int64_t large = 2 * kSkinnyBeforePrefillMaxRows;
   bool early = false;
-  if (e != nullptr && N == 2 && M == 4) early = gated && batch > kSkinnyBatch && all > large;
   if (e != nullptr && N == 16 && M == 32)
     early = (batch > 2 * kSkinnyBatch && rows > kSkinnyBeforePrefillMaxRows) ||
             (gated ? batch > kSkinnyBatch && all > 2 * large : batch >= kSkinnyBatch + kSmallBatch && all > large);

@@ -21,6 +21,14 @@ const void* block_skinny_kernel_for(int form, int mode) {
   return form == kGatedForm ? of_mode<kGatedForm>(mode) : of_mode<kLinearForm>(mode);
 }
 
+const void* block_skinny_wide_kernel_for(int form, int mode) {
+  if (form == kGatedForm)
+    return mode == kModeDirect ? reinterpret_cast<const void*>(&block_skinny_wide_kernel<kModeDirect, kGatedForm>)
+                               : reinterpret_cast<const void*>(&block_skinny_wide_kernel<kModeSplit, kGatedForm>);
+  return mode == kModeDirect ? reinterpret_cast<const void*>(&block_skinny_wide_kernel<kModeDirect, kLinearForm>)
+                             : reinterpret_cast<const void*>(&block_skinny_wide_kernel<kModeSplit, kLinearForm>);
+}
+
 const void* block_skinny_colsplit_kernel_for(int mode) {
   return mode == kModeSplit ? reinterpret_cast<const void*>(&block_skinny_colsplit_kernel<kModeSplit>)
                             : reinterpret_cast<const void*>(&block_skinny_colsplit_kernel<kModeDirect>);

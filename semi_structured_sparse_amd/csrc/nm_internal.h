@@ -149,6 +149,10 @@ hipError_t launch_skinny_spmm(const uint16_t* values, const uint32_t* masks, con
                               int64_t rows, int64_t cols, int tokens, int n, int m, hipStream_t stream,
                               const DeviceInfo& dev, void* workspace = nullptr, size_t workspace_bytes = 0,
                               const BlockArgs* e = nullptr);
+// Block products of kSkinnyBatch + 1 .. 2 * kSkinnyBatch vectors of 2:4, 4:8 and 8:16 in one such launch.
+hipError_t launch_block_skinny_wide(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y,
+                                    int64_t rows, int64_t cols, int tokens, int n, int m, hipStream_t stream,
+                                    const DeviceInfo& dev, const BlockArgs& e);
 // nm_spmm runs the skinny kernel, kSkinnyBatch vectors per launch, from kSkinnyMinBatch
 // vectors up to kMatrixCoreMinBatch, where the prefill kernels take over: on layers of at
 // least kSkinnyMinRows rows for 2:4, 4:8 and 8:16; on smaller layers (down to
@@ -186,6 +190,7 @@ constexpr int64_t kExpandColSplitMaxRows = 2048;
 constexpr int64_t kSkinnyBeforePrefillMaxRows = 4096;
 constexpr int64_t kGatedColSplitMinBatch = 9;
 constexpr int64_t kGatedColSplitMinCols = 8192;
+constexpr int64_t kWideFirstMaxCols = 6144;
 constexpr int64_t kSkinnyExpandFullMinRows = 2048;
 bool use_skinny(int64_t rows, int64_t cols, int64_t batch, int n, int m, const DeviceInfo& dev);
 // 16:32 is routed per launch of up to kSkinnyBatch vectors: a launch of `tokens` vectors
@@ -225,6 +230,7 @@ const void* block_spmv_quarter_kernel_for(int form);
 const void* block_spmm_linear_kernel_for(int N, int batch, int ci);
 const void* block_spmm_gated_kernel_for(int N, int batch);
 const void* block_skinny_kernel_for(int form, int mode);
+const void* block_skinny_wide_kernel_for(int form, int mode);
 const void* block_skinny_colsplit_kernel_for(int mode);
 const void* block_prefill_linear_kernel_for(int mode, int tr, int tt, bool colsplit);
 const void* block_prefill_gated_kernel_for(int mode, int tr, int tt, bool colsplit);

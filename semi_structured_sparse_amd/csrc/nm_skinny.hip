@@ -84,7 +84,7 @@ SkinnyShape skinny_shape(int64_t rows, int64_t cols, int tokens, int mode, const
     const int64_t lines = ceil_div(ceil_div(cols, 128), s.cs), most = pc_max / (128 * s.cs);
     s.phase_cols = int(std::min<int64_t>(ceil_div(lines, ceil_div(lines, most)) * s.cs, ceil_div(cols, 128)) * 128);
   }
-  s.lds = std::max(lead_of(mode, form) + x_bytes(tokens, s.phase_cols), red_bytes(kMaxWaves));
+  s.lds = std::max(lead_of(mode, form) + x_bytes(tokens, s.phase_cols), red_bytes(kMaxWaves) * size_t(ceil_div(tokens, 16)));
   return s;
 }
 
@@ -178,6 +178,19 @@ hipError_t launch_skinny_spmm(const uint16_t* values, const uint32_t* masks, con
                   : mode == kModeSplit  ? reinterpret_cast<const void*>(&skinny_spmm_kernel<1, true>)
                                         : reinterpret_cast<const void*>(&skinny_spmm_kernel<1, false>);
   return launch(k, dim3(unsigned(s.grid)), dim3(kThreadsFixed), args, s.lds, stream, dev);
+}
+
+hipError_t launch_block_skinny_wide(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y,
+                                    int64_t rows, int64_t cols, int tokens, int n, int m, hipStream_t stream,
+                                    const DeviceInfo& dev, const BlockArgs& e) {
+  const int mode = mode_of(n), form = form_of(&e);
+  if (mode == kModeExpand || tokens <= kMaxTokens || tokens > 2 * kMaxTokens || !skinny_fits(rows, cols, kMaxTokens, n, m, dev) ||
+      x_budget(mode, dev, form) < 2 * size_t(tokens) * 128)
+    return hipErrorInvalidValue;
+  const SkinnyShape s = skinny_shape(rows, cols, tokens, mode, dev, false, form);
+  int r = int(rows), c = int(cols), t = tokens, rg = s.rg, cs = s.cs, pc = s.phase_cols;
+  void* args[] = {&values, &masks, &X, &Y, &r, &c, &t, &rg, &cs, &pc, const_cast<BlockArgs*>(&e)};
+  return launch(block_skinny_wide_kernel_for(form, mode), dim3(unsigned(s.grid)), dim3(kThreadsFixed), args, s.lds, stream, dev);
 }
 
 }  // namespace nm

@@ -239,6 +239,36 @@ __device__ __forceinline__ void reduce_store(const Tile& w, f4_t acc, int cs_cou
   }
 }
 
+// The same for TG groups of 16 tokens, without column splits: a row group's waves take the groups in turn.
+template <int FORM, int TG>
+__device__ __forceinline__ void reduce_store_groups(const Tile& w, const f4_t (&acc)[TG], int cs_count, int rows, int tokens,
+                                                    uint16_t* Y, char* lds_base, const BlockArgs& e) {
+  __syncthreads();
+  float4* red = reinterpret_cast<float4*>(lds_base);
+#pragma unroll
+  for (int g = 0; g < TG; ++g)
+    red[(g * kMaxWaves + w.wave) * 64 + w.lane] = make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
+  __syncthreads();
+  if (!w.active || w.second) return;
+  const int row = w.wg_r0 + w.rt * 16 + 4 * w.q;
+  const bool wide = wide_ok(e, Y, rows);
+  for (int g = w.cs; g < TG; g += cs_count) {
+    const float4* mine = red + (g * kMaxWaves + w.wave - w.cs) * 64 + w.lane;
+    float sums[4] = {0.f, 0.f, 0.f, 0.f}, ups[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < cs_count; ++k) {
+      const float4 v = mine[k * 64];
+      sums[0] += v.x; sums[1] += v.y; sums[2] += v.z; sums[3] += v.w;
+      if constexpr (FORM == kGatedForm) {   // the pair's other row group: the cs_count waves after these
+        const float4 u = mine[(cs_count + k) * 64];
+        ups[0] += u.x; ups[1] += u.y; ups[2] += u.z; ups[3] += u.w;
+      }
+    }
+    const int token = 16 * g + w.li;
+    if (token < tokens && row < rows)
+      finish_rows<FORM, 4>(e, sums, ups, row, rows, size_t(token) * unsigned(rows) + unsigned(row), wide, Y);
+  }
+}
+
 // ---- 2:4 (DIRECT) and 4:8 / 8:16 (SPLIT): whole 128-byte lines per load.
 // The instruction's A layout puts 16 rows on the lanes of every 16-lane row (lane l: row
 // l % 16), so a load shaped like the operand covers 16 rows x 64 bytes: half of each row's
@@ -269,8 +299,9 @@ constexpr int kLineDepth = 2;   // lines (two loads each) in flight per wave
 constexpr int kMaskLines = 2;   // lines per mask block (8 words of each row)
 
 // COLS: the column-split form (skinny_colsplit_kernel); without it the split bookkeeping is
-// compiled out, so that the unsplit kernel is the same code as before the split existed.
-template <int MODE, bool COLS, int FORM = kPlainForm>
+// compiled out, so that the unsplit kernel is the same code as before the split existed. TG: groups of 16
+// tokens (block products without column splits take two).
+template <int MODE, bool COLS, int FORM = kPlainForm, int TG = 1>
 __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ values,
                                                  const uint32_t* __restrict__ masks,
                                                  const uint16_t* __restrict__ X, uint16_t* Y,
@@ -282,6 +313,7 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
   extern __shared__ __attribute__((aligned(16))) char lds_base[];
   char* const lds = lds_base + lead_bytes<MODE, FORM>();   // SPLIT: the split tables first, X after them
   const int tid = threadIdx.x;
+  static_assert(TG == 1 || (!COLS && FORM != kPlainForm), "two groups: block products, no column splits");
   static_assert(!COLS || FORM != kGatedForm, "gated products have no column splits here");
   const Tile w(values, masks, X, rows, cols, tokens, rg_count, cs_count, COLS ? sw.splits : 1, FORM == kGatedForm, e);
   const int q = w.q, li = w.li;
@@ -302,9 +334,13 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
   const bool lo8 = (w.lane & 8) == 0;
   const int xq = 4 * (q >> 1) + (q & 1);   // X chunk of lane q in product 0 of a line
   // token rows past the batch read the last token's X: their products are never stored
-  const int xt = min(li, tokens - 1);
-
-  f4_t acc = f4_t{0.f, 0.f, 0.f, 0.f};
+  int xt[TG];
+  f4_t acc[TG];
+#pragma unroll
+  for (int g = 0; g < TG; ++g) {
+    xt[g] = min(16 * g + li, tokens - 1);
+    acc[g] = f4_t{0.f, 0.f, 0.f, 0.f};
+  }
   uint4 va[kLineDepth], vb[kLineDepth];
   uint2 mcur, mnext;
   // SPLIT: this thread's 16-byte chunks of the split tables (1024 + 64 chunks), loaded
@@ -357,8 +393,12 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
     __syncthreads();
     if (n > 0) {
       // X fragment addresses of products 0 and 1 of the phase's first line
-      const uint32_t b_lo0 = xoff<kSwapped<FORM>>(xt, xq, rb), b_hi0 = xoff<kSwapped<FORM>>(xt, xq + 8, rb);
-      const uint32_t b_lo1 = xoff<kSwapped<FORM>>(xt, xq + 2, rb), b_hi1 = xoff<kSwapped<FORM>>(xt, xq + 10, rb);
+      uint32_t b_lo0[TG], b_hi0[TG], b_lo1[TG], b_hi1[TG];
+#pragma unroll
+      for (int g = 0; g < TG; ++g) {
+        b_lo0[g] = xoff<kSwapped<FORM>>(xt[g], xq, rb), b_hi0[g] = xoff<kSwapped<FORM>>(xt[g], xq + 8, rb);
+        b_lo1[g] = xoff<kSwapped<FORM>>(xt[g], xq + 2, rb), b_hi1[g] = xoff<kSwapped<FORM>>(xt[g], xq + 10, rb);
+      }
       for (int pb = 0; pb < n; pb += kMaskLines) {
         // 2:4: the position codes of the block's words, once per block
         mcur = SPLIT ? mnext : make_uint2(pair_codes32(mnext.x), pair_codes32(mnext.y));
@@ -377,13 +417,18 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
           const uint4 t0 = sel4(lo8, va[d], ror8_rows(vb[d]));
           const uint4 t1 = sel4(lo8, ror8_rows(va[d]), vb[d]);
           // X of the line's two products; zero past the range (a wave-uniform test)
-          uint4 x0l = make_uint4(0, 0, 0, 0), x0h = x0l, x1l = x0l, x1h = x0l;
+          uint4 x0l[TG], x0h[TG], x1l[TG], x1h[TG];
+#pragma unroll
+          for (int g = 0; g < TG; ++g) x0l[g] = x0h[g] = x1l[g] = x1h[g] = make_uint4(0, 0, 0, 0);
           if (p < n) {
             const uint32_t cb = uint32_t(l_lo + p) * 256u;
-            x0l = *reinterpret_cast<const uint4*>(lds + b_lo0 + cb);
-            x0h = *reinterpret_cast<const uint4*>(lds + b_hi0 + cb);
-            x1l = *reinterpret_cast<const uint4*>(lds + b_lo1 + cb);
-            x1h = *reinterpret_cast<const uint4*>(lds + b_hi1 + cb);
+#pragma unroll
+            for (int g = 0; g < TG; ++g) {
+              x0l[g] = *reinterpret_cast<const uint4*>(lds + b_lo0[g] + cb);
+              x0h[g] = *reinterpret_cast<const uint4*>(lds + b_hi0[g] + cb);
+              x1l[g] = *reinterpret_cast<const uint4*>(lds + b_lo1[g] + cb);
+              x1h[g] = *reinterpret_cast<const uint4*>(lds + b_hi1[g] + cb);
+            }
           }
           // the loaded registers are free once the operands are formed: the line after the
           // next one is requested now, while the products run
@@ -391,9 +436,13 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint4 cur = h ? t1 : t0;
-            const uint4 lo = h ? x1l : x0l, hi = h ? x1h : x0h;
-            const u8_t xv = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            const h16_t bf = __builtin_bit_cast(h16_t, xv);
+            h16_t bf[TG];
+#pragma unroll
+            for (int g = 0; g < TG; ++g) {
+              const uint4 lo = h ? x1l[g] : x0l[g], hi = h ? x1h[g] : x0h[g];
+              const u8_t xv = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+              bf[g] = __builtin_bit_cast(h16_t, xv);
+            }
             const uint32_t m16 = __builtin_amdgcn_ubfe(word, 16u * uint32_t(h), 16);
             if constexpr (SPLIT) {
               auto half_of = [&](uint32_t entry, uint32_t half) {
@@ -410,21 +459,28 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
               const uint4 opb = make_uint4(pick(s0.z, s0.w), pick(s1.z, s1.w), pick(s2.z, s2.w), pick(s3.z, s3.w));
               const int ia = int(__builtin_amdgcn_perm(i1, i0, 0x0C0C0400u));   // A codes of groups 0..3
               const int ib = int(__builtin_amdgcn_perm(i1, i0, 0x0C0C0501u));   // B codes
-              acc = __builtin_amdgcn_smfmac_f32_16x16x64_f16(__builtin_bit_cast(h8_t, opa), bf, acc, ia, 0, 0);
-              acc = __builtin_amdgcn_smfmac_f32_16x16x64_f16(__builtin_bit_cast(h8_t, opb), bf, acc, ib, 0, 0);
+#pragma unroll
+              for (int g = 0; g < TG; ++g) {
+                acc[g] = __builtin_amdgcn_smfmac_f32_16x16x64_f16(__builtin_bit_cast(h8_t, opa), bf[g], acc[g], ia, 0, 0);
+                acc[g] = __builtin_amdgcn_smfmac_f32_16x16x64_f16(__builtin_bit_cast(h8_t, opb), bf[g], acc[g], ib, 0, 0);
+              }
             } else {
               // m16 holds the position codes of the lane's 4 groups
-              acc = __builtin_amdgcn_smfmac_f32_16x16x64_f16(__builtin_bit_cast(h8_t, cur), bf, acc, int(m16), 0, 0);
+#pragma unroll
+              for (int g = 0; g < TG; ++g)
+                acc[g] = __builtin_amdgcn_smfmac_f32_16x16x64_f16(__builtin_bit_cast(h8_t, cur), bf[g], acc[g], int(m16), 0, 0);
             }
           }
         }
       }
     }
   }
-  if constexpr (COLS)
-    reduce_store<FORM>(w, acc, cs_count, rows, tokens, Y, lds_base, sw, e);
+  if constexpr (TG > 1)
+    reduce_store_groups<FORM>(w, acc, cs_count, rows, tokens, Y, lds_base, e);
+  else if constexpr (COLS)
+    reduce_store<FORM>(w, acc[0], cs_count, rows, tokens, Y, lds_base, sw, e);
   else
-    reduce_store<FORM>(w, acc, cs_count, rows, tokens, Y, lds_base, SplitWs{nullptr, nullptr, 1}, e);
+    reduce_store<FORM>(w, acc[0], cs_count, rows, tokens, Y, lds_base, SplitWs{nullptr, nullptr, 1}, e);
 }
 
 // ---- 16:32 (EXPAND): 64-column steps, each wave's values of a step through its own LDS area.
@@ -601,6 +657,17 @@ __global__ __launch_bounds__(kThreadsFixed) void block_skinny_kernel(const uint1
   else
     skinny_line_body<MODE, false, FORM>(values, masks, X, Y, rows, cols, tokens, rg_count, cs_count, phase_cols,
                                         SplitWs{nullptr, nullptr, 1}, e);
+}
+
+// 17 to 32 tokens in one launch: each weight fragment is multiplied with two groups of 16.
+template <int MODE, int FORM>
+__global__ __launch_bounds__(kThreadsFixed) void block_skinny_wide_kernel(const uint16_t* __restrict__ values,
+                                                                           const uint32_t* __restrict__ masks,
+                                                                           const uint16_t* __restrict__ X, uint16_t* Y,
+                                                                           int rows, int cols, int tokens, int rg_count,
+                                                                           int cs_count, int phase_cols, BlockArgs e) {
+  skinny_line_body<MODE, false, FORM, 2>(values, masks, X, Y, rows, cols, tokens, rg_count, cs_count, phase_cols,
+                                         SplitWs{nullptr, nullptr, 1}, e);
 }
 
 template <int MODE>
