@@ -97,20 +97,26 @@ bool prefill_route(int64_t rows, int64_t cols, int64_t batch, int N, int M, cons
   return !(short_batch && use_skinny(rows, cols, kSkinnyBatch, N, M, dev));
 }
 
-// Block products of 17 to 32 vectors of 2:4, 4:8 and 8:16 in one skinny launch: the weights are read once, where
-// two launches of 16 read them twice, and unsplit prompt kernels fill the card badly (us without a workspace,
-// 24 vectors, those / this: 2:4 2048 x 4096 14.5 / 10.8, 17408 x 5120 45.6 / 28.6, 4:8 48.5 / 31.7, 4096 x 14336
-// 43.1 / 37.5; gated 2:4 2 x 17408 x 5120 83.0 / 52.4, 2 x 4096 x 14336 60.7 / 40.2).
+// Block products of 17 to 32 vectors in one skinny launch: the weights are read once, where two launches of 16
+// read them twice, and unsplit prompt kernels fill the card badly (us without a workspace, 24 vectors, those /
+// this: 2:4 2048 x 4096 14.5 / 10.8, 17408 x 5120 45.6 / 28.6, 4:8 48.5 / 31.7, 16:32 66.0 / 42.4, 4:8 4096 x 14336
+// 43.1 / 37.5; gated 2:4 2 x 17408 x 5120 83.0 / 52.4, 2 x 4096 x 14336 60.7 / 40.2, 16:32 76.3 / 55.6). 16:32 pays for
+// its second group of 16 in LDS traffic, so a few vectors more than 16 of few rows stay apart (17 vectors: 1024 x 4096
+// 13.9 / 15.2, 4096 x 14336 40.2 / 43.7, 2048 x 4096 15.1 / 15.4, 5120 x 17408 65.9 / 61.2).
 bool wide_fits(int64_t all, int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev) {
-  return batch > kSkinnyBatch && batch <= 2 * kSkinnyBatch && M == 2 * N && N != 16 && all >= kSkinnySmallMinRows &&
+  if (N == 16 && batch < kSkinnyBatch + kSmallBatch &&
+      (all < kSkinnyMinRows || (all <= kSkinnyBeforePrefillMaxRows && cols > kGatedColSplitMinCols)))
+    return false;
+  return batch > kSkinnyBatch && batch <= 2 * kSkinnyBatch && M == 2 * N && all >= kSkinnySmallMinRows &&
          skinny_fits(rows, cols, kSkinnyBatch, N, M, dev);
 }
 
 // Where a gated product of so many vectors needs no workspace: also before the column splits on many rows, with X
 // in two or three phases (us, column splits / skinny, 24 vectors: 2:4 2 x 7168 x 5120 29.8 / 23.3, 2 x 14336 x 4096
-// 36.1 / 33.2, 4:8 30.0 / 25.9, 38.4 / 36.6; 2:4 2 x 8192 x 8192 37.5 / 39.2, 2 x 4096 x 4096 13.2 / 15.7).
+// 36.1 / 33.2, 4:8 30.0 / 25.9, 38.4 / 36.6; 2:4 2 x 8192 x 8192 37.5 / 39.2, 2 x 4096 x 4096 13.2 / 15.7; 16:32 2 x 7168
+// x 5120 33.1 / 33.7, 2 x 14336 x 4096 41.9 / 44.2).
 bool wide_first(int64_t rows, int64_t cols, int64_t batch, int N, int M, const DeviceInfo& dev) {
-  return 2 * rows > 2 * kSkinnyBeforePrefillMaxRows && cols <= kWideFirstMaxCols &&
+  return N != 16 && 2 * rows > 2 * kSkinnyBeforePrefillMaxRows && cols <= kWideFirstMaxCols &&
          wide_fits(2 * rows, rows, cols, batch, N, M, dev);
 }
 
@@ -180,15 +186,11 @@ int spmm_dispatch(const uint16_t* values, const uint32_t* masks, const uint16_t*
     err = launch_block_skinny_wide(values, masks, X, Y, rows, cols, int(batch), N, M, s, dev, *e);
     return err == hipSuccess ? NM_OK : hip_fail(err);
   }
-  // 16:32 block products go to the prompt kernels earlier than plain ones (us skinny / prefill, no workspace:
-  // 14336 x 4096 at 17 vectors 34 / 34, at 24 42 / 34, 17408 x 5120 at 17 53 / 64, at 24 67 / 64, 7168 x 5120 at 32
-  // 37 / 41, at 48 56 / 41; gated 2 x 14336 x 4096 at 17 70 / 53, 2 x 7168 x 5120 at 32 61 / 63)
-  const int64_t large = 2 * kSkinnyBeforePrefillMaxRows;
-  bool early = false;
-  if (e != nullptr && N == 16 && M == 32)
-    early = (batch > 2 * kSkinnyBatch && rows > kSkinnyBeforePrefillMaxRows) ||
-            (gated ? batch > kSkinnyBatch && all > 2 * large : batch >= kSkinnyBatch + kSmallBatch && all > large);
-  early = early && prefill_fits(all, cols, batch);
+  // 16:32 block products go to the prompt kernels earlier than plain ones (us without a workspace, 48 vectors,
+  // skinny / prefill: 7168 x 5120 56 / 41, 14336 x 4096 63 / 34, 4096 x 4096 33 / 34; gated 2 x 7168 x 5120 89 / 64, 2 x 4096
+  // x 4096 46 / 52)
+  const bool early = e != nullptr && N == 16 && M == 32 && batch > 2 * kSkinnyBatch &&
+                     rows > kSkinnyBeforePrefillMaxRows && prefill_fits(all, cols, batch);
   if (early || prefill_route(all, cols, batch, N, M, dev)) {  // matrix-core prefill product
     if (!prefill_fits(all, cols, batch)) return NM_ERR_SHAPE;
     err = launch_prefill_spmm(values, masks, X, Y, rows, cols, batch, N, M, s, dev, workspace, workspace_bytes, e);

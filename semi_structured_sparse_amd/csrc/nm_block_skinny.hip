@@ -15,6 +15,13 @@ const void* of_mode(int mode) {
                               : reinterpret_cast<const void*>(&block_skinny_kernel<kModeExpand, FORM>);
 }
 
+template <int FORM>
+const void* wide_of_mode(int mode) {
+  return mode == kModeDirect  ? reinterpret_cast<const void*>(&block_skinny_wide_kernel<kModeDirect, FORM>)
+         : mode == kModeSplit ? reinterpret_cast<const void*>(&block_skinny_wide_kernel<kModeSplit, FORM>)
+                              : reinterpret_cast<const void*>(&block_skinny_wide_kernel<kModeExpand, FORM>);
+}
+
 }  // namespace
 
 const void* block_skinny_kernel_for(int form, int mode) {
@@ -22,11 +29,7 @@ const void* block_skinny_kernel_for(int form, int mode) {
 }
 
 const void* block_skinny_wide_kernel_for(int form, int mode) {
-  if (form == kGatedForm)
-    return mode == kModeDirect ? reinterpret_cast<const void*>(&block_skinny_wide_kernel<kModeDirect, kGatedForm>)
-                               : reinterpret_cast<const void*>(&block_skinny_wide_kernel<kModeSplit, kGatedForm>);
-  return mode == kModeDirect ? reinterpret_cast<const void*>(&block_skinny_wide_kernel<kModeDirect, kLinearForm>)
-                             : reinterpret_cast<const void*>(&block_skinny_wide_kernel<kModeSplit, kLinearForm>);
+  return form == kGatedForm ? wide_of_mode<kGatedForm>(mode) : wide_of_mode<kLinearForm>(mode);
 }
 
 const void* block_skinny_colsplit_kernel_for(int mode) {

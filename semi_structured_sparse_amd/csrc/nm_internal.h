@@ -149,7 +149,7 @@ hipError_t launch_skinny_spmm(const uint16_t* values, const uint32_t* masks, con
                               int64_t rows, int64_t cols, int tokens, int n, int m, hipStream_t stream,
                               const DeviceInfo& dev, void* workspace = nullptr, size_t workspace_bytes = 0,
                               const BlockArgs* e = nullptr);
-// Block products of kSkinnyBatch + 1 .. 2 * kSkinnyBatch vectors of 2:4, 4:8 and 8:16 in one such launch.
+// Block products of kSkinnyBatch + 1 .. 2 * kSkinnyBatch vectors in one such launch.
 hipError_t launch_block_skinny_wide(const uint16_t* values, const uint32_t* masks, const uint16_t* X, uint16_t* Y,
                                     int64_t rows, int64_t cols, int tokens, int n, int m, hipStream_t stream,
                                     const DeviceInfo& dev, const BlockArgs& e);

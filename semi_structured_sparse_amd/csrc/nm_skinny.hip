@@ -184,7 +184,7 @@ hipError_t launch_block_skinny_wide(const uint16_t* values, const uint32_t* mask
                                     int64_t rows, int64_t cols, int tokens, int n, int m, hipStream_t stream,
                                     const DeviceInfo& dev, const BlockArgs& e) {
   const int mode = mode_of(n), form = form_of(&e);
-  if (mode == kModeExpand || tokens <= kMaxTokens || tokens > 2 * kMaxTokens || !skinny_fits(rows, cols, kMaxTokens, n, m, dev) ||
+  if (tokens <= kMaxTokens || tokens > 2 * kMaxTokens || !skinny_fits(rows, cols, kMaxTokens, n, m, dev) ||
       x_budget(mode, dev, form) < 2 * size_t(tokens) * 128)
     return hipErrorInvalidValue;
   const SkinnyShape s = skinny_shape(rows, cols, tokens, mode, dev, false, form);

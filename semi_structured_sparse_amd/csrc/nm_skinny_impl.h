@@ -487,7 +487,7 @@ __device__ __forceinline__ void skinny_line_body(const uint16_t* __restrict__ va
 constexpr int kMaskSteps = 4;   // 64-column steps per mask block
 constexpr int kDepth = 4;       // value loads in flight per wave
 
-template <int FORM = kPlainForm>
+template <int FORM = kPlainForm, int TG = 1>
 __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ values,
                                                    const uint32_t* __restrict__ masks,
                                                    const uint16_t* __restrict__ X, uint16_t* Y,
@@ -506,10 +506,15 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
   const uint32_t moff = rl * uint32_t(w.words) * 4u + 8u * uint32_t(q);
   const int qcol = 32 * (q >> 1);
   // token rows past the batch read the last token's X: their products are never stored
-  const int xt = min(li, tokens - 1);
+  int xt[TG];
+  f4_t acc[TG];
+#pragma unroll
+  for (int g = 0; g < TG; ++g) {
+    xt[g] = min(16 * g + li, tokens - 1);
+    acc[g] = f4_t{0.f, 0.f, 0.f, 0.f};
+  }
   char* const area = lds_base + kExpandBytes + uint32_t(w.wave) * kExpandWaveBytes<FORM>;
 
-  f4_t acc = f4_t{0.f, 0.f, 0.f, 0.f};
   uint4 vbuf[kDepth];
   uint2 mcur, mnext;
   // the expansion table: 2 * kExpandEntries chunks of 16 bytes, loaded first so that the
@@ -545,7 +550,9 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
     xst.store(lds);
     __syncthreads();
     if (n > 0) {
-      const uint32_t b_lo = xoff(xt, q, rb), b_hi = xoff(xt, 4 + q, rb);
+      uint32_t b_lo[TG], b_hi[TG];
+#pragma unroll
+      for (int g = 0; g < TG; ++g) b_lo[g] = xoff(xt[g], q, rb), b_hi[g] = xoff(xt[g], 4 + q, rb);
       for (int s0 = 0; s0 < n; s0 += kMaskSteps) {
         mcur = mnext;
         load_m(s0 + kMaskSteps);
@@ -557,11 +564,16 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
           const uint4 cur = vbuf[j % kDepth];
           const int src = 4 * (li + 16 * j);
           // X of the step (chunks 8 (s_lo + s) ..); zero past the range (a wave-uniform test)
-          uint4 lo = make_uint4(0, 0, 0, 0), hi = make_uint4(0, 0, 0, 0);
+          uint4 lo[TG], hi[TG];
+#pragma unroll
+          for (int g = 0; g < TG; ++g) lo[g] = hi[g] = make_uint4(0, 0, 0, 0);
           if (s < n) {
             const uint32_t cb = uint32_t(s_lo + s) * 128u;
-            lo = *reinterpret_cast<const uint4*>(lds + b_lo + cb);
-            hi = *reinterpret_cast<const uint4*>(lds + b_hi + cb);
+#pragma unroll
+            for (int g = 0; g < TG; ++g) {
+              lo[g] = *reinterpret_cast<const uint4*>(lds + b_lo[g] + cb);
+              hi[g] = *reinterpret_cast<const uint4*>(lds + b_hi[g] + cb);
+            }
           }
           const uint32_t w0 = uint32_t(__builtin_amdgcn_ds_bpermute(src, int(mcur.x)));
           const uint32_t w1 = uint32_t(__builtin_amdgcn_ds_bpermute(src, int(mcur.y)));
@@ -590,9 +602,12 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
               return __builtin_amdgcn_perm(v1, v0, lo_sel) | __builtin_amdgcn_perm(v3, v2, hi_sel);
             };
             const uint4 dense = make_uint4(pick(s0.x, s0.y), pick(s0.z, s0.w), pick(s1.x, s1.y), pick(s1.z, s1.w));
-            const uint4 xf = i ? hi : lo;   // X of the word's columns 8q .. 8q+7, every token
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, dense),
-                                                         __builtin_bit_cast(h8_t, xf), acc, 0, 0, 0);
+#pragma unroll
+            for (int g = 0; g < TG; ++g) {
+              const uint4 xf = i ? hi[g] : lo[g];   // X of the word's columns 8q .. 8q+7, every token
+              acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, dense),
+                                                              __builtin_bit_cast(h8_t, xf), acc[g], 0, 0, 0);
+            }
           }
           // every lane has read the area before the next step writes it
           __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -603,7 +618,10 @@ __device__ __forceinline__ void skinny_expand_body(const uint16_t* __restrict__ 
       }
     }
   }
-  reduce_store<FORM>(w, acc, cs_count, rows, tokens, Y, lds_base, SplitWs{nullptr, nullptr, 1}, e);
+  if constexpr (TG > 1)
+    reduce_store_groups<FORM>(w, acc, cs_count, rows, tokens, Y, lds_base, e);
+  else
+    reduce_store<FORM>(w, acc[0], cs_count, rows, tokens, Y, lds_base, SplitWs{nullptr, nullptr, 1}, e);
 }
 
 // TR (row tiles per wave) is 1: one 16-row tile per wave; the parameter stays in the kernel
@@ -666,8 +684,11 @@ __global__ __launch_bounds__(kThreadsFixed) void block_skinny_wide_kernel(const 
                                                                            const uint16_t* __restrict__ X, uint16_t* Y,
                                                                            int rows, int cols, int tokens, int rg_count,
                                                                            int cs_count, int phase_cols, BlockArgs e) {
-  skinny_line_body<MODE, false, FORM, 2>(values, masks, X, Y, rows, cols, tokens, rg_count, cs_count, phase_cols,
-                                         SplitWs{nullptr, nullptr, 1}, e);
+  if constexpr (MODE == kModeExpand)
+    skinny_expand_body<FORM, 2>(values, masks, X, Y, rows, cols, tokens, rg_count, cs_count, phase_cols, e);
+  else
+    skinny_line_body<MODE, false, FORM, 2>(values, masks, X, Y, rows, cols, tokens, rg_count, cs_count, phase_cols,
+                                           SplitWs{nullptr, nullptr, 1}, e);
 }
 
 template <int MODE>
