@@ -1,5 +1,5 @@
 // Small-batch 50% products on the gfx950 matrix instructions: Y [tokens][rows] =
-// X [tokens][cols] W'^T for 1 <= tokens <= 16, W' given as the packed values and bitmask
+// X [tokens][cols] W'^T for 1 <= tokens <= 16 (32 in block_skinny_wide_kernel), W' given as the packed values and bitmask
 // (the batch side of the SpMV / SpMM split the news.bitwarelabs.com page draws in "What's
 // new"; bitmask format of the aimodeling.com page, "The Kernel Is the Other Half of the
 // Answer").
