@@ -87,7 +87,7 @@ def inputs(gen, batch, width=512, vocab=1000):
             torch.randint(0, vocab, (batch,), generator=gen, device=device()).to(torch.int32))
 
 
-@pytest.mark.parametrize("batch", [1, 3, 12, 40, 300])
+@pytest.mark.parametrize("batch", [1, 3, 12, 24, 40, 300])
 def test_a_block_of_them(batch):
     gen = generator(batch)
     block = Block(gen)
@@ -96,7 +96,7 @@ def test_a_block_of_them(batch):
     block.check(*given, block.step(*given))
 
 
-@pytest.mark.parametrize("batch", [1, 12, 40])
+@pytest.mark.parametrize("batch", [1, 12, 24, 40])
 def test_captured_and_replayed(batch):
     """Several replays with other inputs, with eager calls on the same workspaces and synchronisations
     between them: each gives what the eager calls give, to the bit."""
@@ -173,7 +173,7 @@ def test_on_another_stream():
 
 def test_the_same_bits_each_time():
     gen = generator(7)
-    for batch in (1, 7, 16, 33, 260):
+    for batch in (1, 7, 16, 24, 33, 260):
         block = Block(gen)
         block.workspaces(batch)
         given = inputs(gen, batch)
