@@ -173,13 +173,13 @@ struct Running {
   __device__ __forceinline__ Sums closed(float c) const {
     if (!(m > kNone)) return Sums{m, s, 0.0f};
     const float rest = Reference(m, c).rest(), f = __builtin_amdgcn_exp2f(-rest);
-    return Sums{m, s * f, fmaf(-t, f, rest * s)};
+    return Sums{m, s * f, f * fmaf(rest, s, -t)};   // the rest is in each term's exponent, and so in t beside s
   }
   __device__ __forceinline__ void open(float m_, float c, float s_, float t_) {   // the same, backwards
     const float rest = Reference(m_, c).rest(), f = __builtin_amdgcn_exp2f(rest);
     m = m_;
     s = s_ * f;
-    t = fmaf(-t_, f, rest * s_);
+    t = f * fmaf(rest, s_, -t_);
   }
 };
 
