@@ -95,12 +95,14 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // What a wave's terms are relative to: 2^(x c - mc), mc the rounded m c, so that a term's exponent is
-// one instruction from fp16 (its conversion in it); what the rounding of mc left goes into the sums when
-// they are closed. Where m c could overflow, the exponent is (x - m) c.
+// one instruction from fp16 (its conversion in it); what the rounding of mc left, half a step of it, goes into
+// the sums when they are closed. From 2^24 on that is more than 1 and soon past what an exponent holds: there,
+// and where m c is no number, the exponent is (x - m) c, and nothing is left.
 struct Reference {
   float m, c, mc;
   bool direct;
-  __device__ __forceinline__ Reference(float m_, float c_) : m(m_), c(c_), mc(m_ * c_), direct(fabsf(m_) > 1e30f) {}
+  __device__ __forceinline__ Reference(float m_, float c_)
+      : m(m_), c(c_), mc(m_ * c_), direct(!(fabsf(m_ * c_) < 16777216.0f)) {}
   __device__ __forceinline__ float rest() const { return direct ? 0.0f : fmaf(m, c, -mc); }
   template <bool DIRECT>
   __device__ __forceinline__ float exponent(float x) const {

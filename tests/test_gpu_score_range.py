@@ -37,3 +37,49 @@ def test_entropy_of_large_halves(offset, scale):
     assert torch.isfinite(x).all()
     tokens = torch.randint(0, 5000, (5,), generator=gen, device=device()).to(torch.int32)
     score(x, tokens, 20, scale)
+
+
+SCALES = [1.0, as_float(1 / 0.7), as_float(1 / 0.3), 10.0]
+
+
+@pytest.mark.parametrize("fill", [-1e9, -5e9, -1e10, -1e12, -1e15, -1e20, -1e30, 5e9, 1e12, 1e30])
+@pytest.mark.parametrize("vocab", [40, 3000, 70000])
+def test_finite_fills(fill, vocab):
+    """Masks far below the logits that are not the type's lowest value, and lone logits far above: the whole
+    row, its first tiles, its last ones, all but a few tokens, and a single place."""
+    gen = generator(vocab)
+    x = normal(gen, 8, vocab, spread=2.0, dtype=torch.float32)
+    x[0] = fill
+    x[1, : vocab // 2] = fill
+    x[2, vocab - vocab // 3:] = fill
+    keep = x[3, [1, vocab // 2, vocab - 1]]
+    x[3] = fill
+    x[3, [1, vocab // 2, vocab - 1]] = keep
+    x[4, vocab // 3] = fill
+    x[5, ::2] = fill
+    x[6] = fill + x[6] * abs(fill) * 2.0 ** -20           # near each other, many steps apart
+    x[7] = torch.where(x[7] > 0, x[7], x[7] * abs(fill))
+    tokens = torch.randint(0, vocab, (8,), generator=gen, device=device()).to(torch.int32)
+    tokens[3] = 1
+    for scale in SCALES:
+        say(f"scores {vocab} filled with {fill} scale {scale}")
+        score(x, tokens, 0, scale)
+        score(x, tokens, min(20, vocab), scale)
+
+
+@pytest.mark.parametrize("type_", [torch.float16, torch.float32])
+@pytest.mark.parametrize("scale", [3e3, 1e5, 1e9, 1e20, 1e30])
+def test_large_scales(type_, scale):
+    """A temperature near 0: the largest logits share the row, every other has log p far below 0."""
+    scale = as_float(scale)
+    gen = generator(11)
+    for vocab in (50, 5000, 70000):
+        x = normal(gen, 12, vocab, spread=3.0, dtype=type_) + 20.0
+        x[0, : vocab // 2] = torch.finfo(torch.float16).min
+        x[1] = torch.finfo(torch.float16).min
+        x[2, ::7] = x[2].max()
+        tokens = torch.randint(0, vocab, (12,), generator=gen, device=device()).to(torch.int32)
+        tokens[3:] = x[3:].argmax(-1).to(torch.int32)
+        say(f"scores {vocab} {type_} scale {scale}")
+        score(x, tokens, 0, scale)
+        score(x, tokens, 20, scale)
