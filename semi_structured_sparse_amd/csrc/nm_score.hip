@@ -68,19 +68,32 @@ __device__ __forceinline__ float value_of(uint64_t key) {
 }
 __device__ __forceinline__ int index_of(uint64_t key) { return int(~uint32_t(key)); }
 
+// scale * log2 e, and (a - b) times it by halves, in an order in which neither the difference nor the factor
+// has to be a float where the result is one: a and b of both ends of the type, scales past 2.3e38.
+struct Factor {
+  float scale, c;
+  __device__ __forceinline__ explicit Factor(float scale_) : scale(scale_), c(scale_ * kLog2e) {}
+  __device__ __forceinline__ float of(float a, float b) const { return (0.5f * a - 0.5f * b) * scale * (2.0f * kLog2e); }
+};
+
 // The sums of two sets; without a maximum (kNone) one holds nothing, or NaN.
-__device__ __forceinline__ Sums joined(const Sums& a, const Sums& b, float c) {
+__device__ __forceinline__ Sums joined(const Sums& a, const Sums& b, const Factor& c) {
   const bool first = a.m >= b.m;
   const Sums &hi = first ? a : b, &lo = first ? b : a;
   Sums r = hi;
   if (lo.m == kNone) {
     r.s += lo.s;
   } else {
-    const float g = fminf((hi.m - lo.m) * c, 200.0f), f = __builtin_amdgcn_exp2f(-g);   // 2^-200 is 0
+    const float g = fminf(c.of(hi.m, lo.m), 200.0f), f = __builtin_amdgcn_exp2f(-g);   // 2^-200 is 0
     r.s += f * (lo.s + 1.0f);
     r.t += f * fmaf(g, lo.s + 1.0f, lo.t);
   }
   return r;
+}
+
+// log p of a logit of x. In 64 bits, few as they are: x - m or its product alone may be past the largest float.
+__device__ __forceinline__ float log_p(float x, float m, float scale, float log_all) {
+  return float(double(scale) * (double(x) - double(m)) - double(log_all));
 }
 
 __device__ __forceinline__ float wave_max(float v) {
@@ -97,16 +110,17 @@ __device__ __forceinline__ float wave_sum(float v) {
 // What a wave's terms are relative to: 2^(x c - mc), mc the rounded m c, so that a term's exponent is
 // one instruction from fp16 (its conversion in it); what the rounding of mc left, half a step of it, goes into
 // the sums when they are closed. From 2^24 on that is more than 1 and soon past what an exponent holds: there,
-// and where m c is no number, the exponent is (x - m) c, and nothing is left.
+// and where m c is no number, the exponent is that of (x - m), and nothing is left.
 struct Reference {
-  float m, c, mc;
+  Factor f;
+  float m, mc;
   bool direct;
-  __device__ __forceinline__ Reference(float m_, float c_)
-      : m(m_), c(c_), mc(m_ * c_), direct(!(fabsf(m_ * c_) < 16777216.0f)) {}
-  __device__ __forceinline__ float rest() const { return direct ? 0.0f : fmaf(m, c, -mc); }
+  __device__ __forceinline__ Reference(float m_, const Factor& f_)
+      : f(f_), m(m_), mc(m_ * f_.c), direct(!(fabsf(m_ * f_.c) < 16777216.0f)) {}
+  __device__ __forceinline__ float rest() const { return direct ? 0.0f : fmaf(m, f.c, -mc); }
   template <bool DIRECT>
   __device__ __forceinline__ float exponent(float x) const {
-    return DIRECT ? (x - m) * c : fmaf(x, c, -mc);
+    return DIRECT ? f.of(x, m) : fmaf(x, f.c, -mc);
   }
 };
 
@@ -172,12 +186,12 @@ struct Part {
 struct Running {
   float m = kNone, s = 0.0f, t = 0.0f;
   // s and t as sums of 2^((x - m) c) and of that times (m - x) c
-  __device__ __forceinline__ Sums closed(float c) const {
+  __device__ __forceinline__ Sums closed(const Factor& c) const {
     if (!(m > kNone)) return Sums{m, s, 0.0f};
     const float rest = Reference(m, c).rest(), f = __builtin_amdgcn_exp2f(-rest);
     return Sums{m, s * f, f * fmaf(rest, s, -t)};   // the rest is in each term's exponent, and so in t beside s
   }
-  __device__ __forceinline__ void open(float m_, float c, float s_, float t_) {   // the same, backwards
+  __device__ __forceinline__ void open(float m_, const Factor& c, float s_, float t_) {   // the same, backwards
     const float rest = Reference(m_, c).rest(), f = __builtin_amdgcn_exp2f(rest);
     m = m_;
     s = s_ * f;
@@ -346,7 +360,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
   const int chunk = int(int64_t(blockIdx.x) - r * sp.chunks);
   const void* row = static_cast<const char*>(a.logits) + r * a.stride * (HALF ? 2 : 4);
   const int lo = int(min(int64_t(a.vocab), int64_t(chunk) * sp.each)), hi = int(min(int64_t(a.vocab), int64_t(lo) + sp.each));
-  const float c = a.scale * kLog2e;
+  const Factor c(a.scale);
 
   Running run;
   Largest largest;   // the lane's own
@@ -369,7 +383,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
       const float top = wave_max(mine);
       if (run.m > kNone) {
         const Sums old = run.closed(c);
-        const float g = fminf((top - run.m) * c, 200.0f), f = __builtin_amdgcn_exp2f(-g);
+        const float g = fminf(c.of(top, run.m), 200.0f), f = __builtin_amdgcn_exp2f(-g);
         const float s = lane == 0 ? old.s + 1.0f : old.s;   // the old maximum joins the others
         run.open(top, c, f * s, f * fmaf(g, s, old.t));
       }
@@ -489,7 +503,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
       if (token >= a.vocab || (token >= 0 && bad))
         lp = nan;
       else if (token >= 0)
-        lp = of_token == kNone ? kNone : fmaf(a.scale, of_token - all.m, -log_all);
+        lp = of_token == kNone ? kNone : log_p(of_token, all.m, a.scale, log_all);
       a.logprob[r] = lp;
     }
     if (a.entropy != nullptr)
@@ -507,7 +521,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
     }
     in_order(sh, n, a.top, [&](int i, uint64_t key) {
       tokens[i] = index_of(key);
-      logprobs[i] = fmaf(a.scale, value_of(key) - all.m, -log_all);
+      logprobs[i] = log_p(value_of(key), all.m, a.scale, log_all);
     });
     if (tid >= n && tid < a.top) {
       tokens[tid] = -1;

@@ -83,3 +83,33 @@ def test_large_scales(type_, scale):
         say(f"scores {vocab} {type_} scale {scale}")
         score(x, tokens, 0, scale)
         score(x, tokens, 20, scale)
+
+
+@pytest.mark.parametrize("scale", [0.1, 1e-3, 1e-37, 1e-38])
+def test_differences_past_the_largest_float(scale):
+    """Logits of both ends of the type: their difference is no float, its product with the scale is."""
+    scale = as_float(scale)
+    gen = generator(5)
+    x = normal(gen, 6, 3000, dtype=torch.float32) * 1e38
+    x = x.clamp(-3.4e38, 3.4e38)
+    x[0, ::2] = torch.finfo(torch.float32).min
+    x[1] = torch.finfo(torch.float32).min
+    x[1, [5, 2000]] = torch.finfo(torch.float32).max
+    x[2] = torch.linspace(-3.4e38, 3.4e38, 3000, device=device())
+    x[3] = x[2].flip(0)
+    tokens = x.argmin(-1).to(torch.int32)
+    score(x, tokens, 0, scale)
+    score(x, tokens, 64, scale)
+
+
+@pytest.mark.parametrize("scale", [2.3e38, 2.5e38, 3.4e38])
+def test_scales_past_what_log2_e_leaves(scale):
+    """Where scale * log2 e is no float."""
+    scale = as_float(scale)
+    gen = generator(6)
+    x = normal(gen, 6, 3000, spread=1.0, dtype=torch.float32)
+    x[:3] *= 1e-37
+    x[3:5] *= 1e-30
+    x[5] = 0.0
+    score(x, x.argmax(-1).to(torch.int32), 0, scale)
+    score(x, x.argmax(-1).to(torch.int32), 20, scale)
