@@ -113,3 +113,22 @@ def test_scales_past_what_log2_e_leaves(scale):
     x[5] = 0.0
     score(x, x.argmax(-1).to(torch.int32), 0, scale)
     score(x, x.argmax(-1).to(torch.int32), 20, scale)
+
+
+@pytest.mark.parametrize("type_", [torch.float16, torch.float32])
+@pytest.mark.parametrize("vocab", [257, 1300, 2047, 4104, 4616, 9500, 14328, 50257])
+def test_runs_that_leave_waves_empty(type_, vocab):
+    """The last run of a row ends before some of its waves' places, or masks leave a wave fewer values than it
+    is asked for: everything there meets the limit, and more than a key a thread is put in order."""
+    gen = generator(vocab)
+    x = normal(gen, 6, vocab, spread=2.0, dtype=type_)
+    x[1, -1200:] = x[1, -1200:] + 40.0                    # the best of the row are in its last run
+    x[2, -1200:] = 50.0                                   # all equal
+    places = torch.arange(vocab, device=device())
+    x[3] = torch.where(places % 128 < 2, x[3], torch.full_like(x[3], -float("inf")))      # in few lanes
+    x[4] = torch.where(places % 512 < 8, x[4].round(), torch.full_like(x[4], -float("inf")))
+    x[5] = x[5].round()                                   # long runs of ties
+    tokens = torch.randint(0, vocab, (6,), generator=gen, device=device()).to(torch.int32)
+    for top in (1, 5, 20, 64):
+        score(x, tokens, top)
+        score(x[:1], tokens[:1], top)
