@@ -47,6 +47,7 @@ constexpr int kElements = HALF ? 8 : 4;    // of a load
 struct ScoreSplit {
   int chunks;
   int each;                // elements of a chunk
+  int loads;               // of a lane's tile
   int counter_step;
   uint32_t* counters;
   char* parts;             // kPartBytes a chunk
@@ -568,17 +569,25 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
   }
 }
 
-// Loads of a lane's tile, and the tiles of a row's workgroups: whole ones, for about three workgroups a
-// CU in all. Measured (us; loads 2 / 4): fp16 64 rows of 151936 with 20 alternatives 19.0 / 20.5, 2047
-// of 128256 without 110 / 106; fp32 8 rows of 128256 with 5 11.2 / 10.7, 1024 without 90 / 94. Four
-// workgroups a CU: 64 rows of 151936 20.7, 512 of 32000 20.8 against 18.6 with three and 18.4 with two,
-// which take 36.2 for 256 of 151936 against 33.8.
-constexpr int loads_of(bool half, bool split) { return half == split ? 2 : 4; }
+// The tiles of a row's workgroups: whole ones, for about three workgroups a CU in all. Measured with four: 64
+// rows of 151936 20.7 us, 512 of 32000 20.8, against 18.6 with three and 18.4 with two, which take 36.2 for 256
+// of 151936 against 33.8.
+//
+// Loads of a lane's tile: two, with which kAtOnce workgroups fit a CU (four of fp16 take the registers of all but
+// four) and little of a row's last tile is empty. Measured (us, two / four loads): fp16 700 rows of 50257 23.5 /
+// 28.3, 1500 of 151936 98 / 109, 64 in 10 parts with 20 alternatives 19.1 / 21.0; fp32 1500 183 / 188, 64 in parts
+// 19.2 / 21.2. Four in two places:
+// - a part of two tiles becomes one of a wait less: 8 rows of 128256 fp32 11.5 / 11.1, 1 of 151936 fp16 11.5 / 11.2;
+// - rows a little past what fits at once, most of whose second round of workgroups would be empty (128256, fp16:
+//   1700 rows 95 / 98, 1800 111 / 103, 2047 125 / 112, 2500 140 / 137, 3100 164 / 170; fp32 162 / 175, 199 / 182,
+//   215 / 206, 255 / 250, 310 / 315), but for short ones, whose last tile is much of them (fp16 2047 of 50257 56 / 60).
+constexpr int kAtOnce = int(160 * 1024 / sizeof(Shared));
+constexpr int kLongTiles = 8;
 
 template <bool HALF>
 ScoreSplit split_of(int64_t rows, int64_t vocab, const DeviceInfo& dev) {
-  constexpr int64_t kTile = kThreads * loads_of(HALF, true) * kElements<HALF>;
-  ScoreSplit sp{1, int(vocab), 0, nullptr, nullptr};
+  constexpr int64_t kTile = kThreads * 2 * kElements<HALF>;
+  ScoreSplit sp{1, int(vocab), 2, 0, nullptr, nullptr};
   const int64_t tiles = (vocab + kTile - 1) / kTile;
   int64_t want = 3 * int64_t(dev.cu_count) / rows;
   if (want > kMaxChunks) want = kMaxChunks;
@@ -586,11 +595,18 @@ ScoreSplit split_of(int64_t rows, int64_t vocab, const DeviceInfo& dev) {
   const int64_t each = (tiles + want - 1) / want;
   sp.chunks = int((tiles + each - 1) / each);
   if (sp.chunks > 1) sp.each = int(each * kTile);
+  if (sp.chunks > 1 && each == 2) sp.loads = 4;
   return sp;
 }
 
 ScoreSplit split_of(int64_t rows, int64_t vocab, bool fp16, const DeviceInfo& dev) {
   return fp16 ? split_of<true>(rows, vocab, dev) : split_of<false>(rows, vocab, dev);
+}
+
+ScoreSplit whole_rows(int64_t rows, int64_t vocab, bool fp16, const DeviceInfo& dev) {
+  const int64_t fit = int64_t(kAtOnce) * dev.cu_count, tile = kThreads * 4 * (fp16 ? kElements<true> : kElements<false>);
+  const bool past = rows > fit && 2 * rows <= 3 * fit && vocab >= kLongTiles * tile;
+  return {1, int(vocab), past ? 4 : 2, 0, nullptr, nullptr};
 }
 
 size_t split_bytes(int64_t rows, int64_t vocab, bool fp16, const DeviceInfo& dev) {
@@ -599,9 +615,9 @@ size_t split_bytes(int64_t rows, int64_t vocab, bool fp16, const DeviceInfo& dev
 }
 
 template <bool HALF, bool TOP>
-const void* kernel_of(bool split) {
-  return split ? reinterpret_cast<const void*>(&score_kernel<HALF, TOP, loads_of(HALF, true)>)
-               : reinterpret_cast<const void*>(&score_kernel<HALF, TOP, loads_of(HALF, false)>);
+const void* kernel_of(int loads) {
+  return loads == 4 ? reinterpret_cast<const void*>(&score_kernel<HALF, TOP, 4>)
+                    : reinterpret_cast<const void*>(&score_kernel<HALF, TOP, 2>);
 }
 
 }  // namespace
@@ -619,7 +635,7 @@ size_t score_workspace_bytes(int64_t rows, int64_t vocab, const DeviceInfo& dev)
 hipError_t launch_score(const ScoreCall& c, bool fp16, void* workspace, size_t workspace_bytes, hipStream_t stream,
                         const DeviceInfo& dev) {
   ScoreCall a = c;
-  ScoreSplit sp{1, c.vocab, 0, nullptr, nullptr};
+  ScoreSplit sp = whole_rows(c.rows, c.vocab, fp16, dev);
   const size_t need = split_bytes(c.rows, c.vocab, fp16, dev);
   if (need > 0 && workspace != nullptr && workspace_bytes >= need) {
     sp = split_of(c.rows, c.vocab, fp16, dev);
@@ -629,9 +645,9 @@ hipError_t launch_score(const ScoreCall& c, bool fp16, void* workspace, size_t w
     sp.counters = static_cast<uint32_t*>(workspace);
     sp.parts = static_cast<char*>(workspace) + NM_DECODE_COUNTER_BYTES;
   }
-  const bool top = c.top > 0, split = sp.chunks > 1;
-  const void* k = fp16 ? (top ? kernel_of<true, true>(split) : kernel_of<true, false>(split))
-                       : (top ? kernel_of<false, true>(split) : kernel_of<false, false>(split));
+  const bool top = c.top > 0;
+  const void* k = fp16 ? (top ? kernel_of<true, true>(sp.loads) : kernel_of<true, false>(sp.loads))
+                       : (top ? kernel_of<false, true>(sp.loads) : kernel_of<false, false>(sp.loads));
   void* args[] = {&a, &sp};
   return launch(k, dim3(unsigned(int64_t(c.rows) * sp.chunks)), dim3(kThreads), args, 0, stream, dev);
 }
