@@ -13,8 +13,8 @@
 // tiles. A limit that `top` of a workgroup's 256 largest meet is met by few elements more, and they
 // are looked for in the tiles of those lanes alone, 16 or 32 elements of one lane and tile at a time, by
 // as many threads (each lane through its own elements instead, in its registers or read again, most of it
-// instructions that find nothing: 256 rows of 151936 46 us against 41). What is found is put in order
-// by counting, for each, how many go before it.
+// instructions that find nothing: 256 rows of 151936 46 us against 41); of a lane with a second such tile, in
+// all of its tiles. What is found is put in order by counting, for each, how many go before it.
 //
 // What bounds it: reading the logits once, with an exponential an element close behind (2047 rows of
 // 128256 fp16, 525 MB: 5.0 TB/s; 1024 in fp32 5.8). A row goes to several workgroups where there are few
@@ -200,15 +200,15 @@ struct Running {
   }
 };
 
-constexpr int kPlaces = 1024;              // tiles of lanes to look into
 
 struct Shared {
   uint64_t keys[kRoom];
-  int places[kPlaces];
+  int places[kThreads];     // where to look: a lane's first element in its tile,
+  int lanes[kThreads];      // or in every tile
   Sums sums[kWaves];
   uint64_t best[kWaves];
   int counts[kWaves];
-  uint32_t found, listed;
+  uint32_t found, tiles, everywhere;
   float limits[kWaves];
   uint64_t limit;
   uint32_t arrived;
@@ -343,26 +343,19 @@ __device__ __forceinline__ int candidates(const void* row, int lo, int hi, int t
   const int tid = threadIdx.x;
   const float own = met_by(mine.value, most, (top + kWaves - 1) / kWaves);
   if ((tid & 63) == 0) sh.limits[tid >> 6] = own;
-  if (tid == 0) sh.found = sh.listed = 0;
+  if (tid == 0) sh.found = sh.tiles = sh.everywhere = 0;
   __syncthreads();
   float limit = sh.limits[0];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) limit = fminf(limit, sh.limits[w]);
   limit = fmaxf(limit, HALF ? -65504.0f : -3.402823466e38f);   // -infinity meets no limit
-  // where to look: first element of the lane in the tile
-  auto list = [&](int tile) {
-    const uint32_t n = atomicAdd(&sh.listed, 1u);
-    if (n < kPlaces) sh.places[n] = tile + tid * E;
-  };
   if (mine.value >= limit) {
-    if (mine.other >= limit) {
-      for (int at = lo; at < hi; at += kTile) list(at);
-    } else {
-      list(mine.at);
-    }
+    if (mine.other >= limit) sh.lanes[atomicAdd(&sh.everywhere, 1u)] = lo + tid * E;
+    else sh.places[atomicAdd(&sh.tiles, 1u)] = mine.at + tid * E;
   }
   __syncthreads();
-  const int places = int(min(sh.listed, uint32_t(kPlaces)));
+  const int tiles = (hi - lo + kTile - 1) / kTile, lanes = int(sh.everywhere), some = int(sh.tiles);
+  const int places = some + lanes * tiles;
   const int j = tid % kGroup, offset = (j / E) * (kThreads * E) + j % E;
   for (int i = tid / kGroup; i < places; i += kAtOnce * (kThreads / kGroup)) {
     float x[kAtOnce];
@@ -370,7 +363,13 @@ __device__ __forceinline__ int candidates(const void* row, int lo, int hi, int t
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const int place = i + k * (kThreads / kGroup);
-      at[k] = place < places ? sh.places[place] + offset : hi;
+      at[k] = hi;
+      if (place < some) {
+        at[k] = sh.places[place] + offset;
+      } else if (place < places) {
+        const int tile = int(unsigned(place - some) / unsigned(lanes));
+        at[k] = sh.lanes[place - some - tile * lanes] + tile * kTile + offset;
+      }
       x[k] = kNone;
       if (at[k] < hi) x[k] = float(static_cast<const typename Part<HALF, LOADS>::Element*>(row)[at[k]]);
     }
@@ -382,9 +381,9 @@ __device__ __forceinline__ int candidates(const void* row, int lo, int hi, int t
       }
   }
   __syncthreads();
-  const uint32_t n = sh.found, listed = sh.listed;
+  const uint32_t n = sh.found;
   __syncthreads();
-  if (n > kRoom || listed > kPlaces) return one_by_one<HALF>(row, lo, hi, top, sh);
+  if (n > kRoom) return one_by_one<HALF>(row, lo, hi, top, sh);
   return n <= kThreads ? int(n) : fewer(int(n), top, sh);
 }
 
@@ -573,15 +572,17 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
 // rows of 151936 20.7 us, 512 of 32000 20.8, against 18.6 with three and 18.4 with two, which take 36.2 for 256
 // of 151936 against 33.8.
 //
-// Loads of a lane's tile: two, with which kAtOnce workgroups fit a CU (four of fp16 take the registers of all but
-// four) and little of a row's last tile is empty. Measured (us, two / four loads): fp16 700 rows of 50257 23.5 /
-// 28.3, 1500 of 151936 98 / 109, 64 in 10 parts with 20 alternatives 19.1 / 21.0; fp32 1500 183 / 188, 64 in parts
-// 19.2 / 21.2. Four in two places:
+// Loads of a lane's tile: two, with which kAtOnce workgroups fit a CU (fp16 by its registers, fp32 by LDS; four loads
+// leave room for four and five) and little of a row's last tile is empty. Measured (us, two / four loads): fp16 700
+// rows of 50257 23.5 / 28.3, 1500 of 151936 98 / 109, 64 in 10 parts with 20 alternatives 19.1 / 21.0; fp32 1500
+// 183 / 188, 64 in parts 19.2 / 21.2. Four in two places:
 // - a part of two tiles becomes one of a wait less: 8 rows of 128256 fp32 11.5 / 11.1, 1 of 151936 fp16 11.5 / 11.2;
 // - rows a little past what fits at once, most of whose second round of workgroups would be empty (128256, fp16:
-//   1700 rows 95 / 98, 1800 111 / 103, 2047 125 / 112, 2500 140 / 137, 3100 164 / 170; fp32 162 / 175, 199 / 182,
-//   215 / 206, 255 / 250, 310 / 315), but for short ones, whose last tile is much of them (fp16 2047 of 50257 56 / 60).
-constexpr int kAtOnce = int(160 * 1024 / sizeof(Shared));
+//   1700 rows 91 / 95, 1800 108 / 100, 2047 128 / 114, 2200 130 / 126, 2500 139 / 137, 2800 152 / 149; fp32: 2047
+//   206 / 212, 2049 227 / 213, 2300 243 / 234, 2500 255 / 252, 2800 278 / 280), but for short ones, whose last tile
+//   is much of them (fp16 2047 of 50257 56 / 60).
+template <bool HALF>
+constexpr int kAtOnce = HALF ? 7 : 8;
 constexpr int kLongTiles = 8;
 
 template <bool HALF>
@@ -603,9 +604,10 @@ ScoreSplit split_of(int64_t rows, int64_t vocab, bool fp16, const DeviceInfo& de
   return fp16 ? split_of<true>(rows, vocab, dev) : split_of<false>(rows, vocab, dev);
 }
 
-ScoreSplit whole_rows(int64_t rows, int64_t vocab, bool fp16, const DeviceInfo& dev) {
-  const int64_t fit = int64_t(kAtOnce) * dev.cu_count, tile = kThreads * 4 * (fp16 ? kElements<true> : kElements<false>);
-  const bool past = rows > fit && 2 * rows <= 3 * fit && vocab >= kLongTiles * tile;
+template <bool HALF>
+ScoreSplit whole_rows(int64_t rows, int64_t vocab, const DeviceInfo& dev) {
+  const int64_t fit = int64_t(kAtOnce<HALF>) * dev.cu_count, tile = kThreads * 4 * kElements<HALF>;
+  const bool past = rows > fit && 4 * rows <= 5 * fit && vocab >= kLongTiles * tile;
   return {1, int(vocab), past ? 4 : 2, 0, nullptr, nullptr};
 }
 
@@ -635,7 +637,7 @@ size_t score_workspace_bytes(int64_t rows, int64_t vocab, const DeviceInfo& dev)
 hipError_t launch_score(const ScoreCall& c, bool fp16, void* workspace, size_t workspace_bytes, hipStream_t stream,
                         const DeviceInfo& dev) {
   ScoreCall a = c;
-  ScoreSplit sp = whole_rows(c.rows, c.vocab, fp16, dev);
+  ScoreSplit sp = fp16 ? whole_rows<true>(c.rows, c.vocab, dev) : whole_rows<false>(c.rows, c.vocab, dev);
   const size_t need = split_bytes(c.rows, c.vocab, fp16, dev);
   if (need > 0 && workspace != nullptr && workspace_bytes >= need) {
     sp = split_of(c.rows, c.vocab, fp16, dev);

@@ -132,3 +132,18 @@ def test_runs_that_leave_waves_empty(type_, vocab):
     for top in (1, 5, 20, 64):
         score(x, tokens, top)
         score(x[:1], tokens[:1], top)
+
+
+@pytest.mark.parametrize("type_", [torch.float16, torch.float32])
+@pytest.mark.parametrize("vocab", [9000, 70000, 200001])
+def test_lanes_with_many_of_the_best(type_, vocab):
+    """Values that recur with every tile: the lanes that hold the best hold them in all of their tiles."""
+    gen = generator(vocab)
+    places = torch.arange(vocab, device=device())
+    x = normal(gen, 4, vocab, spread=0.01, dtype=torch.float32)
+    for i, period in enumerate((2048, 4096, 8192, 1000)):
+        x[i] += normal(gen, period, spread=3.0, dtype=torch.float32)[places % period]
+    x = x.to(type_)
+    tokens = torch.randint(0, vocab, (4,), generator=gen, device=device()).to(torch.int32)
+    for top in (1, 20, 64):
+        score(x, tokens, top)
