@@ -117,7 +117,9 @@ __device__ __forceinline__ void normalise(float (&v)[NU][8], int first, int widt
   for (int j = 0; j < NU; ++j)
 #pragma unroll
     for (int k = 0; k < 8; ++k) s = fmaf(v[j][k], v[j][k], s);
-  const float r = __builtin_amdgcn_rsqf(row_sum<G>(s, room + kMaxWaves) * each + eps);   // good to 1 ulp
+  const float square = row_sum<G>(s, room + kMaxWaves) * each + eps;
+  // v_rsq_f32 is good to 1 ulp, but takes a subnormal for 0: a power of 4 brings it to it and back
+  const float r = square < 0x1p-100f ? __builtin_amdgcn_rsqf(square * 0x1p100f) * 0x1p50f : __builtin_amdgcn_rsqf(square);
 #pragma unroll
   for (int j = 0; j < NU; ++j)
 #pragma unroll
