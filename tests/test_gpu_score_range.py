@@ -147,3 +147,13 @@ def test_lanes_with_many_of_the_best(type_, vocab):
     tokens = torch.randint(0, vocab, (4,), generator=gen, device=device()).to(torch.int32)
     for top in (1, 20, 64):
         score(x, tokens, top)
+
+
+@pytest.mark.parametrize("type_", [torch.float16, torch.float32])
+def test_the_longest_row_and_the_most_rows(type_):
+    gen = generator(24)
+    x = normal(gen, 1, 1 << 24, spread=3.0, dtype=type_)
+    score(x, x.argmax(-1).to(torch.int32), 64, 0.5)
+    x = normal(gen, 1 << 23, 3, spread=3.0, dtype=type_)
+    tokens = torch.randint(-1, 3, (1 << 23,), generator=gen, device=device()).to(torch.int32)
+    score(x, tokens, 2)
