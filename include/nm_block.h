@@ -110,8 +110,9 @@ int nm_block_norm(const void* x, const uint16_t* branch, void* h, uint16_t* y, c
  * Logits of -infinity have no probability and are never listed: entries past the last token with
  * one are -1 and -infinity. A row without any has log probabilities of -infinity and an entropy of
  * 0. A row with a NaN or +infinity has NaN for each number and -1 for each top token. Logits of the
- * type's lowest value are numbers like others. Sums over the row hold the largest term apart, so that
- * log p near 0 and small entropies keep their digits.
+ * type's lowest value are numbers like others, and so are those of any other finite mask, at any scale (beside
+ * one that leaves fewer than `top` tokens, alternatives take many times as long as beside -infinity). Sums over
+ * the row hold the largest term apart, so that log p near 0 and small entropies keep their digits.
  * NM_ERR_NULL; NM_ERR_SHAPE: rows outside 1 .. 2^23, vocab outside 1 .. 2^24, top outside 0 .. 64 or
  * above vocab, a stride below vocab or above 2^40, scale not positive and finite; NM_ERR_ALIGN. */
 int nm_logprobs(const void* logits, const int32_t* tokens, float* logprob, float* entropy, int32_t* top_tokens,

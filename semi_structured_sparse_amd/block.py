@@ -252,9 +252,10 @@ def nm_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, workspace
     """Of each row of logits, fp32 or fp16 [rows, vocab] with any row stride, times scale (a temperature's
     inverse): the log probability of tokens int32 [rows] (0 for negative ones), the entropy, and the
     `top` (at most 64) most likely tokens with their log probabilities, best first, ties to the lower
-    token. fp32 and int32. Logits of -infinity are never listed (token -1, log probability -infinity);
-    a row with NaN or +infinity gives NaN. workspace: from logprobs_workspace, or None (rows are then
-    not split over the GPU)."""
+    token. fp32 and int32. Logits of -infinity are never listed (token -1, log probability -infinity) and
+    are the mask to use where alternatives are asked for: finite ones are logits like others, whose ties
+    take long. A row with NaN or +infinity gives NaN. workspace: from logprobs_workspace, or None (rows
+    are then not split over the GPU)."""
     done = (_d._quick or _d._bound()).nm_logprobs(logits, tokens, top, scale, workspace)
     if done is not NotImplemented:
         return LogProbs(*done)
